@@ -17,6 +17,7 @@ GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_ALIGNMENT, GEMM_ER
     GEMM_ERR_CHECK = range(7)
 GEMM_F16, GEMM_BF16, GEMM_E4M3, GEMM_F32, GEMM_E2M1 = range(5)
 GEMM_SCALE_NONE, GEMM_SCALE_UE8M0_32, GEMM_SCALE_UE4M3_16 = range(3)
+GEMM_NORM_PARTS = 512          # most rows of K fp32 that gemm_norm_backward's workspace needs
 GEMM_FLAG_SYNC, GEMM_FLAG_FORCE_1CTA, GEMM_FLAG_FORCE_2CTA, GEMM_FLAG_DETERMINISTIC = 0x1, 0x2, 0x4, 0x8
 
 DTYPE = {"f16": GEMM_F16, "bf16": GEMM_BF16, "e4m3": GEMM_E4M3, "f32": GEMM_F32, "e2m1": GEMM_E2M1}
@@ -28,7 +29,8 @@ EXPORTS = ["gemm_plan_create", "gemm_run", "gemm_run_host", "gemm_plan_last_stat
            "gemm_chain_run_host", "gemm_plan_set_stream_k", "gemm_measure_tensor_rate",
            "gemm_testing_pair_tile_n", "gemm_plan_set_clock_meter", "gemm_plan_read_clock_meter",
            "gemm_testing_trace_slots", "gemm_testing_set_trace", "gemm_testing_tmem_ld_probe",
-           "gemm_testing_staging_probe", "gemm_testing_schedule", "gemm_testing_e4m3_pair_tile_n"]
+           "gemm_testing_staging_probe", "gemm_testing_schedule", "gemm_testing_e4m3_pair_tile_n",
+           "gemm_norm_run", "gemm_norm_backward", "gemm_gate_run", "gemm_gate_backward", "gemm_matvec_run"]
 
 # the per-role trace counters of one CTA, in slot order (a GB300_TRACE=1 library:
 # gemm_testing_set_trace); SM clock cycles unless the name says otherwise
@@ -127,6 +129,13 @@ def lib():
         for name in ("gemm_chain_run", "gemm_chain_run_host"):
             f = getattr(L, name)
             f.argtypes = [vp, vp, vp, vp, vp, vp, vp]
+            f.restype = st
+        L.gemm_norm_run.argtypes = [i64, i64, st, st, st, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.gemm_norm_backward.argtypes = [i64, i64, st, st, st] + [vp] * 9 + [ctypes.c_size_t, vp]
+        L.gemm_gate_run.argtypes = [i64, i64, st, st, vp, vp, vp, vp, vp, vp]
+        L.gemm_gate_backward.argtypes = [i64, i64, st, st, st, vp, vp, vp, vp, vp, vp]
+        L.gemm_matvec_run.argtypes = [i64, i64, i64, st, st, st, vp, vp, vp, vp, vp, vp]
+        for f in (L.gemm_norm_run, L.gemm_norm_backward, L.gemm_gate_run, L.gemm_gate_backward, L.gemm_matvec_run):
             f.restype = st
         _lib = L
     return _lib
@@ -271,6 +280,48 @@ def gemm_run_noalloc(M: int, N: int, K: int, ab, d, A, B, C, D, stream=None, wai
     st = lib().gemm_run_noalloc(M, N, K, DTYPE.get(ab, ab), DTYPE.get(d, d), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                 _stream(stream), int(wait))
     _check(st, "gemm_run_noalloc")
+    return st
+
+
+def gemm_norm_run(M: int, K: int, x, h, y, eps: float, X, R, W, H, Y, SFY=None, RSTD=None, stream=None) -> int:
+    """h = x + r, y = h * rstd * w: Y (and SFY for e4m3), optionally H and RSTD."""
+    st = lib().gemm_norm_run(M, K, DTYPE.get(x, x), DTYPE.get(h, h), DTYPE.get(y, y), eps, _ptr(X), _ptr(R), _ptr(W),
+                             _ptr(H), _ptr(Y), _ptr(SFY), _ptr(RSTD), _stream(stream))
+    _check(st, "gemm_norm_run")
+    return st
+
+
+def gemm_norm_backward(M: int, K: int, dy, h, y, DY, DH, H, RSTD, W, DX, DW=None, Y=None, workspace=None,
+                       workspace_bytes: int = 0, stream=None) -> int:
+    """Gradients of gemm_norm_run: DX, optionally DW (with a workspace) and the 16-bit operand Y again."""
+    st = lib().gemm_norm_backward(M, K, DTYPE.get(dy, dy), DTYPE.get(h, h), DTYPE.get(y, y), _ptr(DY), _ptr(DH), _ptr(H),
+                                  _ptr(RSTD), _ptr(W), _ptr(DX), _ptr(DW), _ptr(Y), _ptr(workspace), workspace_bytes,
+                                  _stream(stream))
+    _check(st, "gemm_norm_backward")
+    return st
+
+
+def gemm_gate_run(M: int, F: int, z, a, Z, A, SFA=None, CK=None, SFCK=None, stream=None) -> int:
+    """a = silu(g) * u of Z = [g | u]: A (and SFA for e4m3), optionally the 8-bit checkpoint CK, SFCK."""
+    st = lib().gemm_gate_run(M, F, DTYPE.get(z, z), DTYPE.get(a, a), _ptr(Z), _ptr(A), _ptr(SFA), _ptr(CK), _ptr(SFCK),
+                             _stream(stream))
+    _check(st, "gemm_gate_run")
+    return st
+
+
+def gemm_gate_backward(M: int, F: int, da, dz, a, DA, CK, SFCK, DZ, A=None, stream=None) -> int:
+    """Gradient of the gated unit from its 8-bit checkpoint: DZ, optionally the 16-bit operand A again."""
+    st = lib().gemm_gate_backward(M, F, DTYPE.get(da, da), DTYPE.get(dz, dz), DTYPE.get(a, a), _ptr(DA), _ptr(CK),
+                                  _ptr(SFCK), _ptr(DZ), _ptr(A), _stream(stream))
+    _check(st, "gemm_gate_backward")
+    return st
+
+
+def gemm_matvec_run(M: int, N: int, K: int, x, d, block_scaled: int, X, B, SFB, C, D, stream=None) -> int:
+    """D = X·B + C for 1 to 16 rows of 16-bit X and an e2m1 plan's B and SFB."""
+    st = lib().gemm_matvec_run(M, N, K, DTYPE.get(x, x), DTYPE.get(d, d), int(block_scaled), _ptr(X), _ptr(B), _ptr(SFB),
+                               _ptr(C), _ptr(D), _stream(stream))
+    _check(st, "gemm_matvec_run")
     return st
 
 

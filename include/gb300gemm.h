@@ -314,7 +314,99 @@ gemm_status gemm_chain_run(gemm_plan_t p, const void *A, const void *B, const vo
 gemm_status gemm_chain_run_host(gemm_plan_t p, const void *A, const void *B, const void *E, const void *C,
                                 void *D, void *cuda_stream);
 
-/* Static description of a status code. */
+/* ------------------------------------------------------------------------------------------
+ * The feed-forward block around the product: what makes its block-scaled operand, what stands
+ * between two products, its gradients, and its form for a few rows.  (The pages have no
+ * counterpart to these entry points; they write and read the operand formats above.)
+ *
+ * None takes a plan or allocates: the caller owns and passes every buffer, calls on different
+ * streams are independent, and each may be captured into a graph.  They enqueue on cuda_stream
+ * (a cudaStream_t of the current device, which must be compute capability 10.3) and return.
+ * M counts rows (tokens); M = 0 is allowed and does nothing (gemm_norm_backward then sets DW to
+ * zero).  Buffers are packed and row-major, and every pointer but the scale codes' and RSTD's must be
+ * 16-byte aligned (GEMM_ERR_ALIGNMENT).  Outputs must not overlap inputs except where said.
+ *
+ * Where an output is GEMM_E4M3, it is the A operand of a GEMM_SCALE_UE8M0_32 plan and its scale
+ * codes are that plan's SFA: per row, each 32 consecutive elements (the last block of a row may be
+ * short) share the code c = the smallest c >= 0 with max |v| <= 448 * 2^(c - 127), and an
+ * element is v / 2^(c - 127) rounded to nearest even.  No finite element saturates.  An infinite
+ * element makes its block decode to infinity at that element (448 * 2^120 exceeds fp32) and to zero at
+ * finite ones below 2^110; a NaN element becomes the NaN code and does not touch its block's scale.
+ */
+
+/*
+ * Residual addition and root-mean-square norm:
+ *
+ *     h[m][k] = x[m][k] + r[m][k]                 rounded to the type h
+ *     rstd[m] = 1 / sqrt(sum_k h[m][k]^2 / K + eps)
+ *     y[m][k] = h[m][k] * rstd[m] * w[k]          in the type y
+ *
+ * x and h: GEMM_F32 or GEMM_BF16 (R and H have type h); y: GEMM_E4M3 (codes in Y, M x ceil(K/32)
+ * scale codes in SFY), GEMM_BF16 or GEMM_F16.  W: K fp32.  R may be NULL (no addition); H, which may
+ * be R or (same type) X itself, and RSTD (M fp32, for the backward pass) may be NULL (not wanted).
+ * Statistics are summed in fp32 over the rounded h.  K % 16 == 0 (GEMM_ERR_ALIGNMENT) and
+ * K <= 32768 (GEMM_ERR_UNSUPPORTED); eps >= 0.
+ */
+gemm_status gemm_norm_run(int64_t M, int64_t K, gemm_dtype x, gemm_dtype h, gemm_dtype y, float eps,
+                          const void *X, const void *R, const float *W, void *H, void *Y, uint8_t *SFY,
+                          float *RSTD, void *cuda_stream);
+
+/*
+ * Its gradient, from the stored H and RSTD (the rounding of y is passed straight through):
+ *
+ *     n = h * rstd,  g = dy * w
+ *     dx[m][k] = dh[m][k] + rstd[m] * (g[m][k] - n[m][k] * sum_j(g[m][j] * n[m][j]) / K)
+ *     dw[k]    = sum_m dy[m][k] * n[m][k]
+ *     y[m][k]  = n[m][k] * w[k]                   in the type y
+ *
+ * dx is the gradient of x and of r alike.  dy: GEMM_F32 or GEMM_BF16; DH (the gradient arriving at h
+ * past the norm) and DX have type h; DH may be NULL (none) or DX itself.  DW (K fp32) and Y (the operand
+ * again for the weight's gradient, GEMM_BF16 or GEMM_F16; y is ignored without it) may be NULL.
+ * With DW the call needs a workspace of min(M, GEMM_NORM_PARTS) * K fp32 values (smaller:
+ * GEMM_ERR_INVALID_ARG), whose contents do not matter before or after.  DW is summed in fp32 in an order
+ * that depends on M, K and the GPU's SM count alone.
+ */
+#define GEMM_NORM_PARTS 512
+gemm_status gemm_norm_backward(int64_t M, int64_t K, gemm_dtype dy, gemm_dtype h, gemm_dtype y, const void *DY,
+                               const void *DH, const void *H, const float *RSTD, const float *W, void *DX, float *DW,
+                               void *Y, void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * The gated unit between the block's two products.  Z is M x 2F, row m holding g (F elements) and
+ * then u (F elements), as a product with both weight matrices side by side writes them:
+ *
+ *     a[m][f] = g[m][f] * s * u[m][f],   s = 1 / (1 + exp(-g[m][f]))
+ *
+ * z: GEMM_F32 or GEMM_BF16; a: GEMM_E4M3 (M x ceil(F/32) scale codes in SFA), GEMM_BF16 or GEMM_F16.  With
+ * CK != NULL the call also keeps g and u for the backward pass in 8 bits: CK is M x 2F e4m3 codes in Z's
+ * order and SFCK M x 2 ceil(F/32) scale codes (g's blocks of the row, then u's).  F % 16 == 0
+ * (GEMM_ERR_ALIGNMENT), F <= 2^20.
+ */
+gemm_status gemm_gate_run(int64_t M, int64_t F, gemm_dtype z, gemm_dtype a, const void *Z, void *A, uint8_t *SFA,
+                          uint8_t *CK, uint8_t *SFCK, void *cuda_stream);
+
+/*
+ * Its gradient at the checkpoint's values g, u (decoded from CK and SFCK):
+ *
+ *     dz = [ da * u * s * (1 + g * (1 - s)) | da * g * s ],    a = g * s * u
+ *
+ * da and dz: GEMM_F32 or GEMM_BF16; A (the second product's operand again, for its weight's gradient,
+ * GEMM_BF16 or GEMM_F16; a is ignored without it) may be NULL.
+ */
+gemm_status gemm_gate_backward(int64_t M, int64_t F, gemm_dtype da, gemm_dtype dz, gemm_dtype a, const void *DA,
+                               const uint8_t *CK, const uint8_t *SFCK, void *DZ, void *A, void *cuda_stream);
+
+/*
+ * D = A·B + C for 1 to 16 rows of 16-bit activations and 4-bit weights: one token, or a few, through
+ * a matrix whose other uses run as a GEMM_E2M1 plan.  X (A above): M x K, GEMM_F16 or GEMM_BF16; B and
+ * SFB: the plan's own buffers (N x K packed e2m1, N x K/32 UE8M0 or N x K/16 UE4M3 codes by
+ * block_scaled); C: M x N fp32 or NULL; D: M x N, GEMM_F32 or GEMM_BF16.  Sums in fp32.  Any N >= 1;
+ * K % 32 == 0 (GEMM_ERR_ALIGNMENT); M > 16 or K > 32768: GEMM_ERR_UNSUPPORTED.
+ */
+gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dtype x, gemm_dtype d, int block_scaled,
+                            const void *X, const void *B, const uint8_t *SFB, const float *C, void *D,
+                            void *cuda_stream);
+
 /*
  * Tensor-pipe rate probe (measurement, not part of the GEMM path).  Launches one
  * CTA (cta_group = 1) or CTA pair (cta_group = 2) per SM; in each, one thread
@@ -341,6 +433,7 @@ typedef struct {
 gemm_status gemm_measure_tensor_rate(gemm_dtype ab, int block_scaled, int cta_group, int64_t iters,
                                      gemm_tensor_rate *out);
 
+/* Static description of a status code. */
 const char *gemm_status_string(gemm_status s);
 
 #ifdef __cplusplus
