@@ -11,20 +11,22 @@
 // weight does not depend on M up to 8.  (tcgen05 would want 128-row operand tiles in shared or tensor
 // memory, that is every weight written there once more; the tensor rate is not what bounds this.)
 //
-// A warp owns 16 columns (n) and a slice of K, which it walks in chunks of 128: lane (g, t) holds k =
-// 32 t .. 32 t + 31 of columns g and g + 8, one 128-bit load each, straight from global memory (each
-// weight is used by one lane: shared memory would only add a copy).  The order of k inside an MMA is free
-// as long as both operands agree, so word j of a lane's four gives the A operand of MMAs 2j and 2j + 1, and
-// the activations are laid out in shared memory in that order when the CTA starts.
+// A warp owns 16 columns (n) and a slice of K, which it walks in chunks of 256 through a ring of its own in
+// shared memory, filled AHEAD - 1 chunks early with asynchronous copies: 128 contiguous bytes of each column and
+// its scale codes.  The order of k inside an MMA is free as long as both operands agree: in 32-block i of a chunk
+// lane (g, t) takes k = 32 i + 8 t .. + 7 of columns g and g + 8, one 32-bit word each, as the A operand of two
+// MMAs, and the activations are laid out in shared memory in that order when the CTA starts.  Those words are what
+// ldmatrix deals out of 8 x 16-byte matrices; a column's eight pieces of 16 bytes are permuted by its number, so
+// that a matrix covers the 32 banks.
 //
-// Scales.  UE4M3 (per 16): the product with an e2m1 value has at most six significant bits and
-// lies within 2^-10 .. 2688, so it is exact in fp16: weights are scaled before the MMA.  UE8M0 (per 32): a
-// lane's 32 k are one block; its weights are multiplied by 2^(c - max c of the column's four blocks in the
-// chunk), exact in fp16 down to 2^-14, and the chunk's sum by 2^(max c - 127) in fp32.
+// Scales.  UE8M0 (per 32): the two MMAs of a block start from zero and their sum is scaled in fp32.  UE4M3
+// (per 16): the product with an e2m1 value has at most six significant bits and lies within 2^-10 .. 2688, so it
+// is exact in fp16: weights are scaled before the MMA.
 // Activations.  fp16 goes in as it is.  bf16 is multiplied per row and chunk by the power of two that brings
 // the largest magnitude to 2^15 .. 2^16, which is exact in fp16 for elements down to 2^-32 of it.
-// What these rules do not hold exactly (scales further apart, activations too far apart, infinities, NaN)
-// takes products_fp32 for that chunk: the same sums in fp32 from the original values.
+// What these rules do not hold (activations too far apart within a chunk, outside 2^-50 .. 2^40, infinite or NaN in
+// bf16; UE8M0 scales from 2^65, NaN among them) takes products_fp32 for that chunk: the same sums in fp32
+// from the original values.
 //
 // A CTA's eight warps are R row tiles (of 16 columns of B) by S slices of K, and `c` CTAs of a cluster split K
 // further; the partial sums are joined in a fixed order through shared memory, the cluster's through
@@ -42,8 +44,26 @@ namespace {
 constexpr int MAX_M = 16;
 constexpr int64_t MAX_K = 32768;
 constexpr int WARPS = 8;
-constexpr int CHUNK = 128;           // k per step of a warp
-constexpr int AHEAD = 4;             // chunks in flight per warp: 1 KB of weights each
+constexpr int CHUNK = 256;           // k per step of a warp
+constexpr int BLOCKS = CHUNK / 32;   // 32-k blocks of a chunk: a column's 16-byte pieces
+#ifndef GB300_MATVEC_AHEAD
+#define GB300_MATVEC_AHEAD 4
+#endif
+constexpr int AHEAD = GB300_MATVEC_AHEAD;      // ring slots per warp
+constexpr int CTAS = 2;                        // CTAs per SM
+constexpr int W_BYTES = 16 * CHUNK / 2;        // weights of a slot
+
+// A column's scale codes of a chunk, and the 32-bit words that a slot keeps for them: with K a multiple of 256
+// every chunk's codes are aligned to their size and come in one copy; otherwise the aligned words that
+// hold them do, and the codes are shifted out of those.
+template <int MODE>
+constexpr int CODES = MODE == GEMM_SCALE_UE8M0_32 ? BLOCKS : 2 * BLOCKS;
+template <int MODE, bool ALIGNED>
+constexpr int SF_WORDS = CODES<MODE> / 4 + (ALIGNED ? 0 : 1);
+template <int MODE, bool ALIGNED>
+constexpr int SF_STRIDE = ALIGNED ? CODES<MODE> : (SF_WORDS<MODE, ALIGNED> + 1) / 2 * 8;
+template <int MODE, bool ALIGNED>
+constexpr int SLOT = W_BYTES + 16 * SF_STRIDE<MODE, ALIGNED>;
 
 struct MatvecParams {
     const void *x;
@@ -85,13 +105,34 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// weights: read once, not kept in L1; a request brings its whole line to L2
-__device__ __forceinline__ uint4 load_weights(const uint8_t *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+// asynchronous copies of 16, 4 or BYTES bytes to shared memory: the first `bytes` of them from src, the rest zero
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_codes(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// four 8 x 16-byte matrices, one row address per lane; lane (g, t) gets bytes 4 t .. 4 t + 3 of row g of each
+__device__ __forceinline__ void matrices(uint32_t addr, uint32_t (&v)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ uint32_t load_shared(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ float load_cluster(uint32_t addr) {
     float v;
@@ -105,35 +146,36 @@ __device__ __forceinline__ float2 pair_of(const __nv_bfloat16 *, uint32_t w) {
 __device__ __forceinline__ float2 pair_of(const __half *, uint32_t w) { return halves(w); }
 
 // One chunk's products in fp32 from the original values, for eight rows of X from m0: what lane (g, t) adds to
-// its accumulators (columns g, g, g + 8, g + 8 by rows 2t, 2t + 1).  codes: the lane's scale codes of the two
-// columns (UE8M0: one each, UE4M3: two each).
+// its accumulators (columns n0 + g, n0 + g, n0 + g + 8, n0 + g + 8 by rows 2t, 2t + 1).  The four lanes of a column
+// take every fourth 32-block.
 template <typename XT, int MODE>
-__device__ __noinline__ float4 products_fp32(const void *x, int K, int M, int m0, int k0, uint4 qa, uint4 qb,
-                                             uint32_t code_a, uint32_t code_b) {
-    const int t = threadIdx.x & 3;
+__device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int chunk, int m0) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3, blocks = p.K / 32;
     float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
-    const uint32_t w[2][4] = {{qa.x, qa.y, qa.z, qa.w}, {qb.x, qb.y, qb.z, qb.w}};
     for (int m = 0; m < 8; ++m) {
-        if (m0 + m >= M) break;
+        if (m0 + m >= p.M) break;
         float sum[2] = {0.f, 0.f};
-        if (k0 < K) {
-            const uint32_t *a = reinterpret_cast<const uint32_t *>(static_cast<const XT *>(x) + (int64_t)(m0 + m) * K + k0);
-            for (int col = 0; col < 2; ++col) {
-                const uint32_t code = col ? code_b : code_a;
+        for (int col = 0; col < 2; ++col) {
+            const int n = n0 + g + 8 * col;
+            for (int block = chunk * BLOCKS + t; n < p.N && block < min((chunk + 1) * BLOCKS, blocks); block += 4) {
+                const uint32_t *a = reinterpret_cast<const uint32_t *>(static_cast<const XT *>(p.x) + (int64_t)(m0 + m) * p.K) + block * 16;
+                const int64_t at = (int64_t)n * blocks + block;
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(p.b + at * 16);
                 float part[2] = {0.f, 0.f};
                 for (int i = 0; i < 4; ++i) {
                     uint32_t h[4];
-                    e2m1x8(w[col][i], h);
+                    e2m1x8(w[i], h);
                     for (int j = 0; j < 4; ++j) {
                         const float2 v = halves(h[j]), xv = pair_of((const XT *)nullptr, a[4 * i + j]);
                         part[i / 2] = fmaf(v.x, xv.x, fmaf(v.y, xv.y, part[i / 2]));
                     }
                 }
                 if (MODE == GEMM_SCALE_UE8M0_32) {
-                    sum[col] = code == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(part[0] + part[1], (int)code - 127);
+                    const uint32_t code = p.sfb[at];
+                    sum[col] += code == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(part[0] + part[1], (int)code - 127);
                 } else {
-                    const float2 s = halves(ue4m3x2(code));
-                    sum[col] = fmaf(part[0], s.x, part[1] * s.y);
+                    const float2 s = halves(ue4m3x2(reinterpret_cast<const uint16_t *>(p.sfb)[at]));
+                    sum[col] += fmaf(part[0], s.x, part[1] * s.y);
                 }
             }
         }
@@ -150,29 +192,23 @@ __device__ __noinline__ float4 products_fp32(const void *x, int K, int M, int m0
 }
 
 // The CTA's chunks [lo, hi) of X into shared memory as the MMA's B operand: eight consecutive k (one 128-bit word)
-// of row m, chunk lc at word ((lc * 4 + j) * M + m) * 4 + t for k = 32 t + 8 j.  bf16: scaled per (row, chunk);
-// scale[lc * rows + m] undoes it, or is negative where the chunk of some row does not convert exactly.
+// of row m, chunk lc at word ((lc * BLOCKS + i) * M + m) * 4 + t for k = 32 i + 8 t.  bf16: scaled per (row,
+// chunk); scale[lc * rows_x + m] undoes it, or is negative where the chunk of some row does not convert exactly.
 template <typename XT>
 __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int rows_x, uint4 *xf, float *scale) {
-    const int l = threadIdx.x & 15, j = l & 3, t = l >> 2;
-    const int pairs = (hi - lo) * p.M;
-    // every lane takes the same number of turns: the shuffles below need both halves of the warp
-    for (int first = (threadIdx.x >> 5) * 2; first < pairs; first += WARPS * 2) {
-        const int i = first + ((threadIdx.x >> 4) & 1);
-        const int lc = i / p.M, m = i - lc * p.M, k = (lo + lc) * CHUNK + l * 8;
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < (hi - lo) * p.M; i += WARPS) {
+        const int lc = i / p.M, m = i - lc * p.M, k = (lo + lc) * CHUNK + lane * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (i < pairs && k < p.K)
-            v = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + (int64_t)m * p.K + k);
-        if constexpr (sizeof(XT) == 2 && !std::is_same<XT, __half>::value) {
+        if (k < p.K) v = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + (int64_t)m * p.K + k);
+        if constexpr (!std::is_same<XT, __half>::value) {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
                                     __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-            top = max(top >> 16, top & 0xFFFFu);
-#pragma unroll
-            for (int o = 8; o > 0; o /= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 16, top & 0xFFFFu));
             const int e = top ? (int)(top >> 7) : 142;              // biased exponent; a chunk of zeros keeps scale 1
-            // within 2^-60 .. 2^60 the factors of the sums stay away from fp32's ends
-            bool fine = e >= 82 && e <= 202;
+            // magnitudes within 2^-50 .. 2^40: what underflows before the factor is applied is below 2^-100 after
+            bool fine = e >= 77 && e <= 167;
             const float up = __uint_as_float((uint32_t)(142 - e + 127) << 23);
             uint32_t h[4];
 #pragma unroll
@@ -184,29 +220,28 @@ __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, i
                 h[q] = *reinterpret_cast<const uint32_t *>(&r);
             }
             v = make_uint4(h[0], h[1], h[2], h[3]);
-            const uint32_t all = __ballot_sync(0xFFFFFFFFu, fine) >> (threadIdx.x & 16) & 0xFFFFu;
-            if (l == 0 && i < pairs)
-                scale[lc * rows_x + m] = all == 0xFFFFu ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) : -1.f;
+            const bool all = __all_sync(0xFFFFFFFFu, fine);
+            if (lane == 0) scale[lc * rows_x + m] = all ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) : -1.f;
         }
-        if (i < pairs) xf[((lc * 4 + j) * p.M + m) * 4 + t] = v;
+        xf[((lc * BLOCKS + (lane >> 2)) * p.M + m) * 4 + (lane & 3)] = v;
     }
 }
 
-template <typename XT, int MODE, int NT>
-__global__ void __launch_bounds__(WARPS * 32, 2) matvec_kernel(MatvecParams p) {
+template <typename XT, int MODE, int NT, bool ALIGNED>
+__global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_constant__ MatvecParams p) {
     constexpr bool SCALED_X = !std::is_same<XT, __half>::value;
     constexpr int ROWS_X = NT * 8;
     extern __shared__ uint4 smem[];
     uint4 *xf = smem;
-    float *xscale = reinterpret_cast<float *>(xf + (size_t)p.chunk_room * p.M * 16);
+    float *xscale = reinterpret_cast<float *>(xf + (size_t)p.chunk_room * p.M * BLOCKS * 4);
     float *parts = xscale + (SCALED_X ? p.chunk_room * ROWS_X : 0);     // [2][WARPS][NT][16][8]
     constexpr int PART = NT * 16 * 8;
+    uint8_t *rings = reinterpret_cast<uint8_t *>(parts + 2 * WARPS * PART);
 
-    uint32_t cluster = 1, rank = 0, cluster_id = blockIdx.x, clusters = gridDim.x;
+    uint32_t cluster;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
-    rank = cluster_ctarank();
-    cluster_id = blockIdx.x / cluster;
-    clusters = gridDim.x / cluster;
+    const uint32_t rank = cluster_ctarank();
+    const int first_group = blockIdx.x / cluster, group_step = gridDim.x / cluster;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int S = p.slices, R = WARPS / S, tl = warp / S, sl = warp - tl * S;
@@ -215,131 +250,189 @@ __global__ void __launch_bounds__(WARPS * 32, 2) matvec_kernel(MatvecParams p) {
     const int c0 = chunks * (int)(rank * S + sl) / T, c1 = chunks * (int)(rank * S + sl + 1) / T;
     const int tiles = (p.N + 15) / 16, groups = (tiles + R - 1) / R;
     const int blocks = p.K / 32;                        // 32-k blocks of a column
+    const int codes = blocks / BLOCKS * CODES<MODE> + blocks % BLOCKS * (CODES<MODE> / BLOCKS);       // of a column
+    const uint32_t ring = smem_addr(rings) + warp * AHEAD * SLOT<MODE, ALIGNED>;
 
-    // weights in flight: the slots hold chunks c .. c + AHEAD - 1 of a tile
-    uint4 q[AHEAD][2];
-    uint32_t code[AHEAD][2];
-    auto fetch = [&](int j, int grp, int ch) {
+    // The next chunk to request.  A copy of weights takes four columns: lane l brings piece l & 7 of columns
+    // l / 8, l / 8 + 4, + 8, + 12; `w_next` and `sf_next` are the lane's addresses in the next chunk.
+    const int piece = lane & 7, col = lane >> 3;
+    int next_group = first_group, next_chunk = c0, next_slot = 0, live = 0;
+    const uint8_t *w_next = p.b, *sf_next = p.sfb;
+    int sf_left = 0;
+    auto enter_tile = [&]() {
+        const int n0 = (next_group * R + tl) * 16;
+        live = (p.N - n0 - col + 3) / 4;                        // the lane's columns inside the matrix
+        w_next = p.b + ((int64_t)(n0 + col) * blocks + c0 * BLOCKS + piece) * 16;
+        const int n = n0 + (ALIGNED ? lane : lane >> 1);
+        const int64_t at = (int64_t)n * codes + c0 * CODES<MODE>;
+        sf_next = p.sfb + (ALIGNED ? at : (at & ~(int64_t)3) + (lane & 1) * 4);
+        // codes of the column from here on, in bytes past sf_next
+        sf_left = n >= p.N ? 0 : ALIGNED ? CODES<MODE> : codes - c0 * CODES<MODE> + (int)(at & 3) - (lane & 1) * 4;
+    };
+    auto request = [&]() {
+        if (next_group < groups) {
+            const uint32_t slot = ring + next_slot * SLOT<MODE, ALIGNED>;
+            const bool on = ALIGNED || next_chunk * BLOCKS + piece < blocks;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int n = (grp * R + tl) * 16 + g + 8 * r;
-            q[j][r] = make_uint4(0, 0, 0, 0);
-            code[j][r] = 0;
-            if (ch < c1 && n < p.N && ch * 4 + t < blocks) {
-                const int64_t block = (int64_t)n * blocks + ch * 4 + t;
-                q[j][r] = load_weights(p.b + block * 16);
-                if (MODE == GEMM_SCALE_UE8M0_32) code[j][r] = __ldg(p.sfb + block);
-                else code[j][r] = __ldg(reinterpret_cast<const uint16_t *>(p.sfb) + block);
+            for (int r = 0; r < 4; ++r) {
+                const int c = col + 4 * r;
+                const bool here = on && r < live;
+                copy16(slot + c * 128 + ((piece ^ c) & 7) * 16, here ? w_next + (int64_t)r * 4 * blocks * 16 : p.b, here ? 16 : 0);
+            }
+            const uint32_t sf = slot + W_BYTES;
+            if (ALIGNED) {
+                if (lane < 16) copy_codes<CODES<MODE>>(sf + lane * CODES<MODE>, sf_left ? sf_next : p.sfb, sf_left);
+            } else {
+                // bytes of this chunk that the column still has, from sf_next on
+                const int most = CODES<MODE> + 3 - (lane & 1) * 4, left = min(sf_left, most);
+#pragma unroll
+                for (int i = 0; i < SF_STRIDE<MODE, ALIGNED> / 4; i += 2) {
+                    const int bytes = max(0, min(left - 4 * i, 4));
+                    copy4(sf + (lane >> 1) * SF_STRIDE<MODE, ALIGNED> + (lane & 1) * 4 + i * 4, bytes ? sf_next + i * 4 : p.sfb,
+                          (uint32_t)bytes);
+                }
+                sf_left -= CODES<MODE>;
+            }
+            w_next += CHUNK / 2;
+            sf_next += CODES<MODE>;
+            next_slot = next_slot + 1 == AHEAD ? 0 : next_slot + 1;
+            if (++next_chunk == c1) {
+                next_chunk = c0;
+                next_group += group_step;
+                enter_tile();
             }
         }
+        copies_commit();
     };
-    int grp = (int)cluster_id;
-    if (grp < groups) {
-#pragma unroll
-        for (int j = 0; j < AHEAD; ++j) fetch(j, grp, c0 + j);
-    }
+    enter_tile();
+#pragma unroll 1
+    for (int j = 0; j < AHEAD - 1; ++j) request();
+
     if (SCALED_X)
         for (int i = threadIdx.x; i < (hi - lo) * ROWS_X; i += WARPS * 32) xscale[i] = 0.f;
     __syncthreads();
     stage_x<XT>(p, lo, hi, ROWS_X, xf, xscale);
     __syncthreads();
 
-    for (int turn = 0; grp < groups; grp += clusters, turn ^= 1) {
+    int slot = 0;
+    for (int grp = first_group, turn = 0; grp < groups; grp += group_step, turn ^= 1) {
         float total[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) total[nt][i] = 0.f;
+        const int n0 = (grp * R + tl) * 16;
+        // where a column's codes begin within their first word, in bits
+        const uint32_t shift[2] = {(uint32_t)((n0 + g) * (codes & 3) & 3) * 8, (uint32_t)((n0 + g + 8) * (codes & 3) & 3) * 8};
 
-        for (int base = c0; base < c1; base += AHEAD) {
-            const bool last = base + AHEAD >= c1;
-            const int next_grp = last ? grp + (int)clusters : grp, next = last ? c0 : base + AHEAD;
+#pragma unroll 1
+        for (int ch = c0; ch < c1; ++ch) {
+            copies_wait<AHEAD - 2>();
+            __syncwarp();            // every lane's copies have landed, and every lane is done with the slot before this
+            request();
+            const uint32_t w = ring + slot * SLOT<MODE, ALIGNED>;
+            slot = slot + 1 == AHEAD ? 0 : slot + 1;
+            const int lc = ch - lo;
+            float2 xs[NT];
+            bool fine = true;
+            if (SCALED_X) {
+                float worst = 0.f;
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                const int ch = base + j, lc = ch - lo;
-                if (ch < c1) {
-                    float acc[NT][4];
+                for (int nt = 0; nt < NT; ++nt) {
+                    xs[nt] = *reinterpret_cast<const float2 *>(xscale + lc * ROWS_X + nt * 8 + 2 * t);
+                    worst = fminf(worst, fminf(xs[nt].x, xs[nt].y));
+                }
+                fine = worst >= 0.f;
+            }
+            uint32_t code[2][CODES<MODE> / 4];       // the codes of columns g and g + 8
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t sf = w + W_BYTES + (g + 8 * r) * SF_STRIDE<MODE, ALIGNED>;
+                uint32_t v[SF_WORDS<MODE, ALIGNED>];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-                    float2 xs[NT];
-                    bool fine = true;
-                    if (SCALED_X) {
-                        float worst = 1.f;
+                for (int i = 0; i < SF_WORDS<MODE, ALIGNED>; ++i) v[i] = load_shared(sf + 4 * i);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            xs[nt] = *reinterpret_cast<const float2 *>(xscale + lc * ROWS_X + nt * 8 + 2 * t);
-                            worst = fminf(worst, fminf(xs[nt].x, xs[nt].y));
-                        }
-                        fine = worst >= 0.f;
+                for (int i = 0; i < CODES<MODE> / 4; ++i) code[r][i] = ALIGNED ? v[i] : __funnelshift_r(v[i], v[i + !ALIGNED], shift[r]);
+                // a code from 192 on has both top bits set
+                if (MODE == GEMM_SCALE_UE8M0_32)
+                    fine = fine && (((code[r][0] & code[r][0] << 1) | (code[r][1] & code[r][1] << 1)) & 0x80808080u) == 0;
+            }
+            if (((SCALED_X || MODE == GEMM_SCALE_UE8M0_32) && !__all_sync(0xFFFFFFFFu, fine))) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float4 add = products_fp32<XT, MODE>(p, n0, ch, nt * 8);
+                    total[nt][0] += add.x;
+                    total[nt][1] += add.y;
+                    total[nt][2] += add.z;
+                    total[nt][3] += add.w;
+                }
+                continue;
+            }
+            float sum[NT][4];            // the chunk's, before the activations' scale
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[nt][i] = 0.f;
+            uint32_t mul[2][BLOCKS];     // UE4M3: the lane's scale in each block, twice
+            if constexpr (MODE == GEMM_SCALE_UE4M3_16) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int i = 0; i < BLOCKS; i += 4) {
+                        // even codes for lanes t = 0, 1 (a block's first 16 k), odd ones for t = 2, 3
+                        const uint32_t mine = __byte_perm(code[r][i / 2], code[r][i / 2 + 1], t < 2 ? 0x6420u : 0x7531u);
+                        const uint32_t a = ue4m3x2(mine & 0xFFFFu), b = ue4m3x2(mine >> 16);
+                        mul[r][i] = __byte_perm(a, a, 0x1010);
+                        mul[r][i + 1] = __byte_perm(a, a, 0x3232);
+                        mul[r][i + 2] = __byte_perm(b, b, 0x1010);
+                        mul[r][i + 3] = __byte_perm(b, b, 0x3232);
                     }
-                    uint32_t mul[2][2];                       // scales of the two columns' halves of 16 k
-                    float row_scale[2];
-                    if (MODE == GEMM_SCALE_UE8M0_32) {
-                        const uint32_t both = code[j][0] | code[j][1] << 16;
-                        uint32_t top = __vmaxu2(both, __shfl_xor_sync(0xFFFFFFFFu, both, 1));
-                        top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            }
+            uint32_t q[4];               // words of (block i, columns g and g + 8), (block i + 1, the same)
+#pragma unroll
+            for (int i = 0; i < BLOCKS; ++i) {
+                if ((i & 1) == 0) {
+                    // row address: lanes 0-7 columns 0-7 of block i, 8-15 columns 8-15, 16-31 the same of block i + 1
+                    const int c = lane & 15, b = i + (lane >> 4);
+                    matrices(w + c * 128 + ((b ^ c) & 7) * 16, q);
+                }
+                uint32_t a[2][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    e2m1x8(q[(i & 1) * 2 + r], a[r]);
+                    if constexpr (MODE == GEMM_SCALE_UE4M3_16) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[r][e] = mul2(a[r][e], mul[r][i]);
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (nt * 8 + g < p.M) x = xf[((lc * BLOCKS + i) * p.M + nt * 8 + g) * 4 + t];
+                    if (MODE == GEMM_SCALE_UE4M3_16) {
+                        mma_16816(sum[nt], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                        mma_16816(sum[nt], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                    } else {
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_16816(acc, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                        mma_16816(acc, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const uint32_t ref = top >> (16 * r) & 0xFFFFu, down = ref - code[j][r];
-                            // (columns past N and blocks past K have weights 0 and code 0)
-                            const bool zero = ((q[j][r].x | q[j][r].y | q[j][r].z | q[j][r].w) & 0x77777777u) == 0 &&
-                                              code[j][r] != 255u;
-                            fine = fine && (zero || (down <= 14u && ref >= 64u && ref <= 190u));
-                            mul[r][0] = mul[r][1] = (15u - min(down, 14u)) * 0x04000400u;
-                            row_scale[r] = __uint_as_float(ref << 23);
-                        }
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint32_t s = ue4m3x2(code[j][r]);
-                            mul[r][0] = __byte_perm(s, s, 0x1010);
-                            mul[r][1] = __byte_perm(s, s, 0x3232);
-                        }
-                    }
-                    if (__all_sync(0xFFFFFFFFu, fine)) {
-                        const uint32_t w[2][4] = {{q[j][0].x, q[j][0].y, q[j][0].z, q[j][0].w},
-                                                  {q[j][1].x, q[j][1].y, q[j][1].z, q[j][1].w}};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t a[2][4];
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                e2m1x8(w[r][i], a[r]);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) a[r][e] = mul2(a[r][e], mul[r][i / 2]);
-                            }
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                uint4 x = make_uint4(0, 0, 0, 0);
-                                if (nt * 8 + g < p.M) x = xf[((lc * 4 + i) * p.M + nt * 8 + g) * 4 + t];
-                                mma_16816(acc[nt], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                                mma_16816(acc[nt], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
-                            }
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float f = SCALED_X ? (i & 1 ? xs[nt].y : xs[nt].x) : 1.f;
-                                if (MODE == GEMM_SCALE_UE8M0_32) f *= row_scale[i / 2];
-                                total[nt][i] = fmaf(acc[nt][i], f, total[nt][i]);
-                            }
-                    } else {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float4 add = products_fp32<XT, MODE>(p.x, p.K, p.M, nt * 8, ch * CHUNK + t * 32, q[j][0],
-                                                                       q[j][1], code[j][0], code[j][1]);
-                            total[nt][0] += add.x;
-                            total[nt][1] += add.y;
-                            total[nt][2] += add.z;
-                            total[nt][3] += add.w;
+                            // 2^(code - 127); code 0 is fp32's subnormal 2^-127
+                            const uint32_t bits = (i & 3) == 3 ? code[r][i / 4] >> 1 : code[r][i / 4] << (23 - 8 * (i & 3));
+                            const float s = __uint_as_float(max(bits & 0x7F800000u, 0x400000u));
+                            sum[nt][2 * r] = fmaf(acc[2 * r], s, sum[nt][2 * r]);
+                            sum[nt][2 * r + 1] = fmaf(acc[2 * r + 1], s, sum[nt][2 * r + 1]);
                         }
                     }
                 }
-                if (next_grp < groups) fetch(j, next_grp, next + j);
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    total[nt][i] = SCALED_X ? fmaf(sum[nt][i], i & 1 ? xs[nt].y : xs[nt].x, total[nt][i])
+                                            : total[nt][i] + sum[nt][i];
         }
 
         // join the slices of K: the CTA's, and the cluster's, always in the same order.  The two buffers
@@ -380,32 +473,48 @@ __global__ void __launch_bounds__(WARPS * 32, 2) matvec_kernel(MatvecParams p) {
     if (cluster != 1) cluster_sync();        // no CTA's shared memory goes while another may read it
 }
 
+int slot_bytes(int mode, int K) {
+    if (K % CHUNK == 0) return mode == GEMM_SCALE_UE8M0_32 ? SLOT<GEMM_SCALE_UE8M0_32, true> : SLOT<GEMM_SCALE_UE4M3_16, true>;
+    return mode == GEMM_SCALE_UE8M0_32 ? SLOT<GEMM_SCALE_UE8M0_32, false> : SLOT<GEMM_SCALE_UE4M3_16, false>;
+}
+
 // How the product is cut (see the head of this file)
 struct MatvecShape {
     int slices, cluster, chunk_room, smem, grid;
 };
-MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int sms) {
-    constexpr int X_ROOM = 88 * 1024;                    // activations in shared memory with two CTAs per SM
+MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, int sms) {
+    constexpr int SM_ROOM = 227 * 1024 / CTAS - 1024;    // shared memory of a CTA with CTAS of them per SM
+    constexpr int MOST_ROOM = 226 * 1024;
     const int nt = M > 8 ? 2 : 1, chunks = (K + CHUNK - 1) / CHUNK, tiles = (N + 15) / 16;
     const int per_chunk = M * CHUNK * 2 + (scaled_x ? nt * 8 * 4 : 0);
-    const int warps = sms * 2 * WARPS;
-    const int most = M <= 4 ? 8 : M <= 8 ? 4 : 2;        // slices: each needs the activations in its own CTA
-    MatvecShape s;
-    s.cluster = 1;
-    while (s.cluster < 8 && s.cluster * 2 <= chunks && (chunks + s.cluster - 1) / s.cluster * per_chunk > X_ROOM) s.cluster *= 2;
-    s.slices = 1;
-    while (s.slices < most && s.slices * 2 * s.cluster <= chunks && (int64_t)tiles * s.slices * s.cluster < warps) s.slices *= 2;
-    while (s.cluster < 8 && s.slices * s.cluster * 4 <= chunks && (int64_t)tiles * s.slices * s.cluster < warps) s.cluster *= 2;
-    // a CTA's chunks: slices [rank S, rank S + S) of S c equal ones
-    s.chunk_room = (chunks + s.cluster - 1) / s.cluster + 1;
-    s.smem = s.chunk_room * per_chunk + 2 * WARPS * nt * 16 * 8 * 4;
-    const int groups = (tiles + WARPS / s.slices - 1) / (WARPS / s.slices);
-    const int resident = sms * (s.smem <= 112 * 1024 ? 2 : 1) / s.cluster;
-    s.grid = (groups < resident ? groups : resident) * s.cluster;
-    return s;
+    const int fixed = 2 * WARPS * nt * 16 * 8 * 4 + WARPS * AHEAD * slot;
+    MatvecShape best{};
+    double best_cost = 0;
+    for (int c = 1; c <= 8 && c <= chunks; c *= 2)
+        for (int S = 1; S <= WARPS && S * c <= chunks; S *= 2) {
+            MatvecShape s;
+            s.cluster = c;
+            s.slices = S;
+            s.chunk_room = (chunks + c - 1) / c;
+            s.smem = s.chunk_room * per_chunk + fixed;
+            if (s.smem > MOST_ROOM) continue;
+            const int R = WARPS / S, groups = (tiles + R - 1) / R;
+            const int resident = sms * (s.smem <= SM_ROOM ? CTAS : 1) / c;
+            s.grid = (groups < resident ? groups : resident) * c;
+            // chunks a warp walks one after another, plus what starting up and joining cost in chunks
+            const int turns = (groups + s.grid / c - 1) / (s.grid / c);
+            const double walk = turns * ((chunks + c * S - 1) / (c * S)) * (s.smem <= SM_ROOM ? 1.0 : 0.75);
+            const double stage = 0.25 * M * s.chunk_room / WARPS, join = turns * (c > 1 ? 2.0 : 0.5);
+            const double cost = walk + stage + join;
+            if (best.grid == 0 || cost < best_cost) {
+                best = s;
+                best_cost = cost;
+            }
+        }
+    return best;
 }
 
-template <typename XT, int MODE, int NT>
+template <typename XT, int MODE, int NT, bool ALIGNED>
 cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
     static std::mutex mu;
     static bool ready[64];
@@ -415,7 +524,7 @@ cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t str
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[dev & 63]) {
-            e = cudaFuncSetAttribute(matvec_kernel<XT, MODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+            e = cudaFuncSetAttribute(matvec_kernel<XT, MODE, NT, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
             if (e != cudaSuccess) return e;
             ready[dev & 63] = true;
         }
@@ -431,11 +540,12 @@ cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t str
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, matvec_kernel<XT, MODE, NT>, p);
+    return cudaLaunchKernelEx(&cfg, matvec_kernel<XT, MODE, NT, ALIGNED>, p);
 }
 template <typename XT, int MODE>
 cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
-    return p.M > 8 ? launch<XT, MODE, 2>(s, p, stream) : launch<XT, MODE, 1>(s, p, stream);
+    if (p.K % CHUNK == 0) return p.M > 8 ? launch<XT, MODE, 2, true>(s, p, stream) : launch<XT, MODE, 1, true>(s, p, stream);
+    return p.M > 8 ? launch<XT, MODE, 2, false>(s, p, stream) : launch<XT, MODE, 1, false>(s, p, stream);
 }
 template <typename XT>
 cudaError_t launch(int mode, const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
@@ -464,7 +574,8 @@ extern "C" gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dty
     int sms = 0;
     gemm_status st = rows::device_sms(&sms);
     if (st != GEMM_OK) return st;
-    const MatvecShape s = matvec_shape((int)M, (int)N, (int)K, x == GEMM_BF16, sms);
+    const MatvecShape s = matvec_shape((int)M, (int)N, (int)K, x == GEMM_BF16,
+                                       slot_bytes(block_scaled, (int)K), sms);
     const MatvecParams p{X, static_cast<const uint8_t *>(B), SFB, C, D, (int)M, (int)N, (int)K, d == GEMM_BF16, s.slices, s.chunk_room};
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
     const cudaError_t e = x == GEMM_F16 ? launch<__half>(block_scaled, s, p, stream)
