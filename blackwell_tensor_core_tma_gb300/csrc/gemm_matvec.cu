@@ -25,12 +25,13 @@
 // Activations.  fp16 goes in as it is.  bf16 is multiplied per row and chunk by the power of two that brings
 // the largest magnitude to 2^15 .. 2^16, which is exact in fp16 for elements down to 2^-32 of it.
 // What these rules do not hold (activations too far apart within a chunk, outside 2^-50 .. 2^40, infinite or NaN in
-// bf16; UE8M0 scales from 2^65, NaN among them) takes products_fp32 for that chunk: the same sums in fp32
+// bf16; UE8M0 scales from 2^33, NaN among them) takes products_fp32 for that chunk: the same sums in fp32
 // from the original values.
 //
-// A CTA's eight warps are R row tiles (of 16 columns of B) by S slices of K, and `c` CTAs of a cluster split K
+// A CTA (one per SM) is 16 warps: R tiles of 16 columns by S slices of K, and `c` CTAs of a cluster split K
 // further; the partial sums are joined in a fixed order through shared memory, the cluster's through
 // distributed shared memory.
+#include <cstdio>
 #include <initializer_list>
 #include <mutex>
 #include <type_traits>
@@ -43,14 +44,15 @@ namespace {
 
 constexpr int MAX_M = 16;
 constexpr int64_t MAX_K = 32768;
-constexpr int WARPS = 8;
+constexpr int WARPS = 16;
 constexpr int CHUNK = 256;           // k per step of a warp
 constexpr int BLOCKS = CHUNK / 32;   // 32-k blocks of a chunk: a column's 16-byte pieces
 #ifndef GB300_MATVEC_AHEAD
-#define GB300_MATVEC_AHEAD 4
+#define GB300_MATVEC_AHEAD 3
 #endif
 constexpr int AHEAD = GB300_MATVEC_AHEAD;      // ring slots per warp
-constexpr int CTAS = 2;                        // CTAs per SM
+constexpr int MOST_CLUSTER = 8;
+constexpr int MOST_SMEM = 226 * 1024;
 constexpr int W_BYTES = 16 * CHUNK / 2;        // weights of a slot
 
 // A column's scale codes of a chunk, and the 32-bit words that a slot keeps for them: with K a multiple of 256
@@ -91,10 +93,14 @@ __device__ __forceinline__ uint32_t ue4m3x2(uint32_t codes) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(codes & 0x7F7Fu)));
     return h;
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
+// both halves of a times the low (high) half of s
+__device__ __forceinline__ uint32_t mul2_low(uint32_t a, uint32_t s) {
+    const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&a), __low2half2(*reinterpret_cast<const __half2 *>(&s)));
+    return *reinterpret_cast<const uint32_t *>(&d);
+}
+__device__ __forceinline__ uint32_t mul2_high(uint32_t a, uint32_t s) {
+    const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&a), __high2half2(*reinterpret_cast<const __half2 *>(&s)));
+    return *reinterpret_cast<const uint32_t *>(&d);
 }
 __device__ __forceinline__ float2 halves(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 
@@ -103,6 +109,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the same from zero
+__device__ __forceinline__ void mma_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // asynchronous copies of 16, 4 or BYTES bytes to shared memory: the first `bytes` of them from src, the rest zero
@@ -193,9 +207,10 @@ __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int 
 
 // The CTA's chunks [lo, hi) of X into shared memory as the MMA's B operand: eight consecutive k (one 128-bit word)
 // of row m, chunk lc at word ((lc * BLOCKS + i) * M + m) * 4 + t for k = 32 i + 8 t.  bf16: scaled per (row,
-// chunk); scale[lc * rows_x + m] undoes it, or is negative where the chunk of some row does not convert exactly.
+// chunk); scale[lc * rows_x + m] undoes it (times unbias), or is negative where the chunk of
+// some row does not convert exactly.
 template <typename XT>
-__device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int rows_x, uint4 *xf, float *scale) {
+__device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int rows_x, float unbias, uint4 *xf, float *scale) {
     const int lane = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < (hi - lo) * p.M; i += WARPS) {
         const int lc = i / p.M, m = i - lc * p.M, k = (lo + lc) * CHUNK + lane * 8;
@@ -221,22 +236,27 @@ __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, i
             }
             v = make_uint4(h[0], h[1], h[2], h[3]);
             const bool all = __all_sync(0xFFFFFFFFu, fine);
-            if (lane == 0) scale[lc * rows_x + m] = all ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) : -1.f;
+            if (lane == 0) scale[lc * rows_x + m] = all ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) * unbias : -1.f;
         }
         xf[((lc * BLOCKS + (lane >> 2)) * p.M + m) * 4 + (lane & 3)] = v;
     }
 }
 
 template <typename XT, int MODE, int NT, bool ALIGNED>
-__global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_constant__ MatvecParams p) {
+__global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_constant__ MatvecParams p) {
     constexpr bool SCALED_X = !std::is_same<XT, __half>::value;
     constexpr int ROWS_X = NT * 8;
+    // UE8M0 factors are taken 2^60 too large: code 0 (2^-127) is then a normal number, and a sum of 256 products
+    // under codes below 160 still stays below 2^121
+    constexpr uint32_t BIAS = MODE == GEMM_SCALE_UE8M0_32 ? 60 : 0;
+    constexpr float UNBIAS = MODE == GEMM_SCALE_UE8M0_32 ? 0x1p-60f : 1.f;
     extern __shared__ uint4 smem[];
     uint4 *xf = smem;
     float *xscale = reinterpret_cast<float *>(xf + (size_t)p.chunk_room * p.M * BLOCKS * 4);
     float *parts = xscale + (SCALED_X ? p.chunk_room * ROWS_X : 0);     // [2][WARPS][NT][16][8]
     constexpr int PART = NT * 16 * 8;
     uint8_t *rings = reinterpret_cast<uint8_t *>(parts + 2 * WARPS * PART);
+    uint4 *zeros = reinterpret_cast<uint4 *>(rings + WARPS * AHEAD * SLOT<MODE, ALIGNED>);        // what rows past M read
 
     uint32_t cluster;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
@@ -257,11 +277,14 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_c
     // l / 8, l / 8 + 4, + 8, + 12; `w_next` and `sf_next` are the lane's addresses in the next chunk.
     const int piece = lane & 7, col = lane >> 3;
     int next_group = first_group, next_chunk = c0, next_slot = 0, live = 0;
+    bool full = false;
+    const int64_t four = (int64_t)blocks * 64;               // four columns on
     const uint8_t *w_next = p.b, *sf_next = p.sfb;
     int sf_left = 0;
     auto enter_tile = [&]() {
         const int n0 = (next_group * R + tl) * 16;
         live = (p.N - n0 - col + 3) / 4;                        // the lane's columns inside the matrix
+        full = n0 + 16 <= p.N;
         w_next = p.b + ((int64_t)(n0 + col) * blocks + c0 * BLOCKS + piece) * 16;
         const int n = n0 + (ALIGNED ? lane : lane >> 1);
         const int64_t at = (int64_t)n * codes + c0 * CODES<MODE>;
@@ -272,12 +295,19 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_c
     auto request = [&]() {
         if (next_group < groups) {
             const uint32_t slot = ring + next_slot * SLOT<MODE, ALIGNED>;
-            const bool on = ALIGNED || next_chunk * BLOCKS + piece < blocks;
+            const uint32_t to = slot + col * 128, even = (piece ^ col) * 16, odd = even ^ 64;
+            if (ALIGNED && full) {
+                copy16(to + even, w_next, 16);
+                copy16(to + 512 + odd, w_next + four, 16);
+                copy16(to + 1024 + even, w_next + 2 * four, 16);
+                copy16(to + 1536 + odd, w_next + 3 * four, 16);
+            } else {
+                const bool on = next_chunk * BLOCKS + piece < blocks;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int c = col + 4 * r;
-                const bool here = on && r < live;
-                copy16(slot + c * 128 + ((piece ^ c) & 7) * 16, here ? w_next + (int64_t)r * 4 * blocks * 16 : p.b, here ? 16 : 0);
+                for (int r = 0; r < 4; ++r) {
+                    const bool here = on && r < live;
+                    copy16(to + r * 512 + (r & 1 ? odd : even), here ? w_next + r * four : p.b, here ? 16 : 0);
+                }
             }
             const uint32_t sf = slot + W_BYTES;
             if (ALIGNED) {
@@ -308,12 +338,22 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_c
 #pragma unroll 1
     for (int j = 0; j < AHEAD - 1; ++j) request();
 
+    if (threadIdx.x == 0) zeros[0] = make_uint4(0, 0, 0, 0);
     if (SCALED_X)
         for (int i = threadIdx.x; i < (hi - lo) * ROWS_X; i += WARPS * 32) xscale[i] = 0.f;
     __syncthreads();
-    stage_x<XT>(p, lo, hi, ROWS_X, xf, xscale);
+    stage_x<XT>(p, lo, hi, ROWS_X, UNBIAS, xf, xscale);
     __syncthreads();
 
+    // the lane's word of X (row nt * 8 + g) in block 0, and the step from block to block
+    const uint4 *x_lane[NT];
+    int x_step[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const bool in = nt * 8 + g < p.M;
+        x_lane[nt] = in ? xf + (nt * 8 + g) * 4 + t : zeros;
+        x_step[nt] = in ? p.M * 4 : 0;
+    }
     int slot = 0;
     for (int grp = first_group, turn = 0; grp < groups; grp += group_step, turn ^= 1) {
         float total[NT][4];
@@ -353,9 +393,10 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_c
                 for (int i = 0; i < SF_WORDS<MODE, ALIGNED>; ++i) v[i] = load_shared(sf + 4 * i);
 #pragma unroll
                 for (int i = 0; i < CODES<MODE> / 4; ++i) code[r][i] = ALIGNED ? v[i] : __funnelshift_r(v[i], v[i + !ALIGNED], shift[r]);
-                // a code from 192 on has both top bits set
+                // a code from 160 on has its top bit and one of the next two set
                 if (MODE == GEMM_SCALE_UE8M0_32)
-                    fine = fine && (((code[r][0] & code[r][0] << 1) | (code[r][1] & code[r][1] << 1)) & 0x80808080u) == 0;
+                    fine = fine && ((code[r][0] & (code[r][0] << 1 | code[r][0] << 2) | code[r][1] & (code[r][1] << 1 | code[r][1] << 2)) &
+                                    0x80808080u) == 0;
             }
             if (((SCALED_X || MODE == GEMM_SCALE_UE8M0_32) && !__all_sync(0xFFFFFFFFu, fine))) {
 #pragma unroll
@@ -373,7 +414,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_c
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[nt][i] = 0.f;
-            uint32_t mul[2][BLOCKS];     // UE4M3: the lane's scale in each block, twice
+            uint32_t mul[2][BLOCKS / 2]; // UE4M3: the lane's scales in blocks 2 i and 2 i + 1
             if constexpr (MODE == GEMM_SCALE_UE4M3_16) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
@@ -381,11 +422,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_c
                     for (int i = 0; i < BLOCKS; i += 4) {
                         // even codes for lanes t = 0, 1 (a block's first 16 k), odd ones for t = 2, 3
                         const uint32_t mine = __byte_perm(code[r][i / 2], code[r][i / 2 + 1], t < 2 ? 0x6420u : 0x7531u);
-                        const uint32_t a = ue4m3x2(mine & 0xFFFFu), b = ue4m3x2(mine >> 16);
-                        mul[r][i] = __byte_perm(a, a, 0x1010);
-                        mul[r][i + 1] = __byte_perm(a, a, 0x3232);
-                        mul[r][i + 2] = __byte_perm(b, b, 0x1010);
-                        mul[r][i + 3] = __byte_perm(b, b, 0x3232);
+                        mul[r][i / 2] = ue4m3x2(mine & 0xFFFFu);
+                        mul[r][i / 2 + 1] = ue4m3x2(mine >> 16);
                     }
             }
             uint32_t q[4];               // words of (block i, columns g and g + 8), (block i + 1, the same)
@@ -402,25 +440,24 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_c
                     e2m1x8(q[(i & 1) * 2 + r], a[r]);
                     if constexpr (MODE == GEMM_SCALE_UE4M3_16) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) a[r][e] = mul2(a[r][e], mul[r][i]);
+                        for (int e = 0; e < 4; ++e) a[r][e] = i & 1 ? mul2_high(a[r][e], mul[r][i / 2]) : mul2_low(a[r][e], mul[r][i / 2]);
                     }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (nt * 8 + g < p.M) x = xf[((lc * BLOCKS + i) * p.M + nt * 8 + g) * 4 + t];
+                    const uint4 x = x_lane[nt][(lc * BLOCKS + i) * x_step[nt]];
                     if (MODE == GEMM_SCALE_UE4M3_16) {
                         mma_16816(sum[nt], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
                         mma_16816(sum[nt], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
                     } else {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_16816(acc, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                        float acc[4];
+                        mma_16816_zero(acc, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
                         mma_16816(acc, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            // 2^(code - 127); code 0 is fp32's subnormal 2^-127
-                            const uint32_t bits = (i & 3) == 3 ? code[r][i / 4] >> 1 : code[r][i / 4] << (23 - 8 * (i & 3));
-                            const float s = __uint_as_float(max(bits & 0x7F800000u, 0x400000u));
+                            // 2^(code - 127 + BIAS)
+                            const uint32_t byte = code[r][i / 4] & 0xFFu << (8 * (i & 3));
+                            const float s = __uint_as_float(((i & 3) == 3 ? byte >> 1 : byte << (23 - 8 * (i & 3))) + (BIAS << 23));
                             sum[nt][2 * r] = fmaf(acc[2 * r], s, sum[nt][2 * r]);
                             sum[nt][2 * r + 1] = fmaf(acc[2 * r + 1], s, sum[nt][2 * r + 1]);
                         }
@@ -431,8 +468,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) matvec_kernel(const __grid_c
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    total[nt][i] = SCALED_X ? fmaf(sum[nt][i], i & 1 ? xs[nt].y : xs[nt].x, total[nt][i])
-                                            : total[nt][i] + sum[nt][i];
+                    total[nt][i] = fmaf(sum[nt][i], SCALED_X ? (i & 1 ? xs[nt].y : xs[nt].x) : UNBIAS, total[nt][i]);
         }
 
         // join the slices of K: the CTA's, and the cluster's, always in the same order.  The two buffers
@@ -482,28 +518,26 @@ int slot_bytes(int mode, int K) {
 struct MatvecShape {
     int slices, cluster, chunk_room, smem, grid;
 };
-MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, int sms) {
-    constexpr int SM_ROOM = 227 * 1024 / CTAS - 1024;    // shared memory of a CTA with CTAS of them per SM
-    constexpr int MOST_ROOM = 226 * 1024;
+// resident[c]: clusters of c CTAs that run at once
+MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, const int *resident) {
     const int nt = M > 8 ? 2 : 1, chunks = (K + CHUNK - 1) / CHUNK, tiles = (N + 15) / 16;
     const int per_chunk = M * CHUNK * 2 + (scaled_x ? nt * 8 * 4 : 0);
-    const int fixed = 2 * WARPS * nt * 16 * 8 * 4 + WARPS * AHEAD * slot;
+    const int fixed = 2 * WARPS * nt * 16 * 8 * 4 + WARPS * AHEAD * slot + 16;
     MatvecShape best{};
     double best_cost = 0;
-    for (int c = 1; c <= 8 && c <= chunks; c *= 2)
+    for (int c = 1; c <= MOST_CLUSTER && c <= chunks; ++c)
         for (int S = 1; S <= WARPS && S * c <= chunks; S *= 2) {
             MatvecShape s;
             s.cluster = c;
             s.slices = S;
             s.chunk_room = (chunks + c - 1) / c;
             s.smem = s.chunk_room * per_chunk + fixed;
-            if (s.smem > MOST_ROOM) continue;
-            const int R = WARPS / S, groups = (tiles + R - 1) / R;
-            const int resident = sms * (s.smem <= SM_ROOM ? CTAS : 1) / c;
-            s.grid = (groups < resident ? groups : resident) * c;
+            if (s.smem > MOST_SMEM || resident[c] == 0) continue;
+            const int R = WARPS / S, groups = (tiles + R - 1) / R, clusters = groups < resident[c] ? groups : resident[c];
+            s.grid = clusters * c;
             // chunks a warp walks one after another, plus what starting up and joining cost in chunks
-            const int turns = (groups + s.grid / c - 1) / (s.grid / c);
-            const double walk = turns * ((chunks + c * S - 1) / (c * S)) * (s.smem <= SM_ROOM ? 1.0 : 0.75);
+            const int turns = (groups + clusters - 1) / clusters;
+            const double walk = turns * ((chunks + c * S - 1) / (c * S));
             const double stage = 0.25 * M * s.chunk_room / WARPS, join = turns * (c > 1 ? 2.0 : 0.5);
             const double cost = walk + stage + join;
             if (best.grid == 0 || cost < best_cost) {
@@ -511,37 +545,75 @@ MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, int sms) 
                 best_cost = cost;
             }
         }
+#ifdef GB300_MATVEC_PRINT
+    printf("M %d N %d K %d: S %d c %d grid %d smem %d\n", M, N, K, best.slices, best.cluster, best.grid, best.smem);
+#endif
     return best;
 }
+
+void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, int grid, int cluster, int smem, cudaStream_t stream) {
+    cfg = cudaLaunchConfig_t{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    attr = cudaLaunchAttribute{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+}
+
+constexpr int MAX_DEVICES = 64;
 
 template <typename XT, int MODE, int NT, bool ALIGNED>
 cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
     static std::mutex mu;
-    static bool ready[64];
+    static bool ready[MAX_DEVICES];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     {
         std::lock_guard<std::mutex> lock(mu);
-        if (!ready[dev & 63]) {
-            e = cudaFuncSetAttribute(matvec_kernel<XT, MODE, NT, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (!ready[dev]) {
+            e = cudaFuncSetAttribute(matvec_kernel<XT, MODE, NT, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SMEM);
             if (e != cudaSuccess) return e;
-            ready[dev & 63] = true;
+            ready[dev] = true;
         }
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)s.grid);
-    cfg.blockDim = dim3(WARPS * 32);
-    cfg.dynamicSmemBytes = (size_t)s.smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)s.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    cluster_config(cfg, attr, s.grid, s.cluster, s.smem, stream);
     return cudaLaunchKernelEx(&cfg, matvec_kernel<XT, MODE, NT, ALIGNED>, p);
 }
+
+// How many clusters of 1 .. 8 CTAs run at once on the current device (asked once: one CTA fills an SM whatever
+// the instance, and a cluster stays within a group of SMs whose size is not a multiple of every c)
+cudaError_t resident_clusters(const int **out) {
+    static std::mutex mu;
+    static int known[MAX_DEVICES][MOST_CLUSTER + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (known[dev][1] == 0) {
+        const auto kernel = matvec_kernel<__half, GEMM_SCALE_UE4M3_16, 1, true>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SMEM);
+        int found[MOST_CLUSTER + 1] = {};
+        for (int c = 1; c <= MOST_CLUSTER && e == cudaSuccess; ++c) {
+            cudaLaunchConfig_t cfg;
+            cudaLaunchAttribute attr;
+            cluster_config(cfg, attr, c, c, MOST_SMEM, nullptr);
+            e = cudaOccupancyMaxActiveClusters(&found[c], kernel, &cfg);
+        }
+        if (e != cudaSuccess) return e;
+        for (int c = 1; c <= MOST_CLUSTER; ++c) known[dev][c] = found[c];
+    }
+    *out = known[dev];
+    return cudaSuccess;
+}
+
 template <typename XT, int MODE>
 cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
     if (p.K % CHUNK == 0) return p.M > 8 ? launch<XT, MODE, 2, true>(s, p, stream) : launch<XT, MODE, 1, true>(s, p, stream);
@@ -574,11 +646,32 @@ extern "C" gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dty
     int sms = 0;
     gemm_status st = rows::device_sms(&sms);
     if (st != GEMM_OK) return st;
-    const MatvecShape s = matvec_shape((int)M, (int)N, (int)K, x == GEMM_BF16,
-                                       slot_bytes(block_scaled, (int)K), sms);
-    const MatvecParams p{X, static_cast<const uint8_t *>(B), SFB, C, D, (int)M, (int)N, (int)K, d == GEMM_BF16, s.slices, s.chunk_room};
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
-    const cudaError_t e = x == GEMM_F16 ? launch<__half>(block_scaled, s, p, stream)
-                                        : launch<__nv_bfloat16>(block_scaled, s, p, stream);
-    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    const int *resident = nullptr;
+    if (resident_clusters(&resident) != cudaSuccess) return GEMM_ERR_CUDA;
+    // nine rows or more whose activations fit no cluster's shared memory (K past some 20000) go in two halves
+    const int slot = slot_bytes(block_scaled, (int)K);
+    MatvecShape s = matvec_shape((int)M, (int)N, (int)K, x == GEMM_BF16, slot, resident);
+    const int first = s.grid ? (int)M : 8;
+    for (int m = 0; m < (int)M; m += first) {
+        const int rows = (int)M - m < first ? (int)M - m : first;
+        if (first != (int)M) s = matvec_shape(rows, (int)N, (int)K, x == GEMM_BF16, slot, resident);
+        if (s.grid == 0) return GEMM_ERR_CUDA;
+        const int64_t out = (int64_t)m * N;
+        const MatvecParams p{static_cast<const uint8_t *>(X) + (int64_t)m * K * 2,
+                             static_cast<const uint8_t *>(B),
+                             SFB,
+                             C ? C + out : nullptr,
+                             static_cast<uint8_t *>(D) + out * (d == GEMM_BF16 ? 2 : 4),
+                             rows,
+                             (int)N,
+                             (int)K,
+                             d == GEMM_BF16,
+                             s.slices,
+                             s.chunk_room};
+        cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
+        const cudaError_t e = x == GEMM_F16 ? launch<__half>(block_scaled, s, p, stream)
+                                            : launch<__nv_bfloat16>(block_scaled, s, p, stream);
+        if (e != cudaSuccess) return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
 }
