@@ -19,9 +19,15 @@
 // ldmatrix deals out of 8 x 16-byte matrices; a column's eight pieces of 16 bytes are permuted by its number, so
 // that a matrix covers the 32 banks.
 //
-// Scales.  UE8M0 (per 32): the two MMAs of a block start from zero and their sum is scaled in fp32.  UE4M3
-// (per 16): the product with an e2m1 value has at most six significant bits and lies within 2^-10 .. 2688, so it
-// is exact in fp16: weights are scaled before the MMA.
+// Scales, more than four rows.  UE8M0 (per 32): the two MMAs of a block start from zero and their sum is scaled
+// in fp32.  UE4M3 (per 16): the product with an e2m1 value has at most six significant bits and lies within
+// 2^-10 .. 2688, so it is exact in fp16: weights are scaled before the MMA.
+// Scales, up to four rows.  An MMA has eight columns of activations, so a row of X is given 8 / FORM of them and its
+// k are dealt out so that each column sees one scale only: a block's halves of 16 k (UE4M3) or two blocks
+// (UE8M0) to neighbouring columns, and 4 / FORM such pairs to the rest; everything else in the
+// column is zero.  MMAs then run on through 4 / FORM pairs into one accumulator, whose two values per lane
+// and row are scaled by the lane's own pair of codes with one packed fp32 multiply-add: nothing is scaled per
+// weight, and no lane decodes a code that another one decodes too.
 // Activations.  fp16 goes in as it is.  bf16 is multiplied per row and chunk by the power of two that brings
 // the largest magnitude to 2^15 .. 2^16, which is exact in fp16 for elements down to 2^-32 of it.
 // What these rules do not hold (activations too far apart within a chunk, outside 2^-50 .. 2^40, infinite or NaN in
@@ -67,6 +73,9 @@ constexpr int SF_STRIDE = ALIGNED ? CODES<MODE> : (SF_WORDS<MODE, ALIGNED> + 1) 
 template <int MODE, bool ALIGNED>
 constexpr int SLOT = W_BYTES + 16 * SF_STRIDE<MODE, ALIGNED>;
 
+// Forms of the kernel: the most rows of X
+int form_of(int M) { return M <= 2 ? M : M <= 4 ? 4 : M <= 8 ? 8 : 16; }
+
 struct MatvecParams {
     const void *x;
     const uint8_t *b, *sfb;
@@ -75,7 +84,7 @@ struct MatvecParams {
     int M, N, K;
     int out_bf16;
     int slices;          // slices of K per CTA (S)
-    int chunk_room;      // chunks the activations' shared memory holds
+    int x_stride;        // bytes of shared memory per row of X
 };
 
 // eight packed e2m1 values (k ascending from the low nibble) to four pairs of halves
@@ -87,19 +96,14 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(w));
 }
-// two UE4M3 codes (bit 7 is not part of the format) to halves
+// two UE4M3 codes (bit 7, which is not part of the format, clear) to halves
 __device__ __forceinline__ uint32_t ue4m3x2(uint32_t codes) {
     uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(codes & 0x7F7Fu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
     return h;
 }
-// both halves of a times the low (high) half of s
-__device__ __forceinline__ uint32_t mul2_low(uint32_t a, uint32_t s) {
-    const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&a), __low2half2(*reinterpret_cast<const __half2 *>(&s)));
-    return *reinterpret_cast<const uint32_t *>(&d);
-}
-__device__ __forceinline__ uint32_t mul2_high(uint32_t a, uint32_t s) {
-    const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&a), __high2half2(*reinterpret_cast<const __half2 *>(&s)));
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&d);
 }
 __device__ __forceinline__ float2 halves(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
@@ -117,6 +121,17 @@ __device__ __forceinline__ void mma_16816_zero(float (&d)[4], uint32_t a0, uint3
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// (a.x * b.x + c.x, a.y * b.y + c.y)
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 
 // asynchronous copies of 16, 4 or BYTES bytes to shared memory: the first `bytes` of them from src, the rest zero
@@ -144,6 +159,33 @@ __device__ __forceinline__ uint32_t load_shared(uint32_t addr) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint2 load_shared2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t load_shared_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t load_shared_u16(uint32_t addr) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+// into v where `on`; elsewhere v stays as it is
+__device__ __forceinline__ void load_shared4_if(bool on, uint4 &v, uint32_t addr) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+                 : "r"(addr), "r"((uint32_t)on)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 load_shared4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -160,9 +202,9 @@ __device__ __forceinline__ float2 pair_of(const __nv_bfloat16 *, uint32_t w) {
 __device__ __forceinline__ float2 pair_of(const __half *, uint32_t w) { return halves(w); }
 
 // One chunk's products in fp32 from the original values, for eight rows of X from m0: what lane (g, t) adds to
-// its accumulators (columns n0 + g, n0 + g, n0 + g + 8, n0 + g + 8 by rows 2t, 2t + 1).  The four lanes of a column
+// its accumulators (columns n0 + g, n0 + g, n0 + g + 8, n0 + g + 8 by rows 2t, 2t + 1; with FEW row t in x and z).  The four lanes of a column
 // take every fourth 32-block.
-template <typename XT, int MODE>
+template <typename XT, int MODE, bool FEW>
 __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int chunk, int m0) {
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3, blocks = p.K / 32;
     float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -188,7 +230,7 @@ __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int 
                     const uint32_t code = p.sfb[at];
                     sum[col] += code == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(part[0] + part[1], (int)code - 127);
                 } else {
-                    const float2 s = halves(ue4m3x2(reinterpret_cast<const uint16_t *>(p.sfb)[at]));
+                    const float2 s = halves(ue4m3x2(reinterpret_cast<const uint16_t *>(p.sfb)[at] & 0x7F7Fu));
                     sum[col] += fmaf(part[0], s.x, part[1] * s.y);
                 }
             }
@@ -197,7 +239,10 @@ __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int 
             sum[col] += __shfl_xor_sync(0xFFFFFFFFu, sum[col], 1);
             sum[col] += __shfl_xor_sync(0xFFFFFFFFu, sum[col], 2);
         }
-        if (m / 2 == t) {
+        if (FEW && m == t) {
+            out.x = sum[0];
+            out.z = sum[1];
+        } else if (!FEW && m / 2 == t) {
             (m & 1 ? out.y : out.x) += sum[0];
             (m & 1 ? out.w : out.z) += sum[1];
         }
@@ -205,12 +250,13 @@ __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int 
     return out;
 }
 
-// The CTA's chunks [lo, hi) of X into shared memory as the MMA's B operand: eight consecutive k (one 128-bit word)
-// of row m, chunk lc at word ((lc * BLOCKS + i) * M + m) * 4 + t for k = 32 i + 8 t.  bf16: scaled per (row,
+// The CTA's chunks [lo, hi) of X into shared memory as the MMA's B operand: row by row, k ascending; lane (g, t) reads
+// the eight k of 32 i + 8 t as one 128-bit word.  A row's stride is 64 bytes past a multiple of 128, so that
+// two rows' words come from different banks.  bf16: scaled per (row,
 // chunk); scale[lc * rows_x + m] undoes it (times unbias), or is negative where the chunk of
 // some row does not convert exactly.
 template <typename XT>
-__device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int rows_x, float unbias, uint4 *xf, float *scale) {
+__device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int rows_x, float unbias, uint8_t *xf, float *scale) {
     const int lane = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < (hi - lo) * p.M; i += WARPS) {
         const int lc = i / p.M, m = i - lc * p.M, k = (lo + lc) * CHUNK + lane * 8;
@@ -238,25 +284,28 @@ __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, i
             const bool all = __all_sync(0xFFFFFFFFu, fine);
             if (lane == 0) scale[lc * rows_x + m] = all ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) * unbias : -1.f;
         }
-        xf[((lc * BLOCKS + (lane >> 2)) * p.M + m) * 4 + (lane & 3)] = v;
+        *reinterpret_cast<uint4 *>(xf + m * p.x_stride + lc * CHUNK * 2 + lane * 16) = v;
     }
 }
 
-template <typename XT, int MODE, int NT, bool ALIGNED>
+template <typename XT, int MODE, int FORM, bool ALIGNED>
 __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_constant__ MatvecParams p) {
     constexpr bool SCALED_X = !std::is_same<XT, __half>::value;
-    constexpr int ROWS_X = NT * 8;
+    constexpr bool FEW = FORM <= 4;
+    constexpr int NT = FORM == 16 ? 2 : 1;               // MMAs' columns of eight rows of X
+    // FEW: blocks whose MMAs share an accumulator, and how often a chunk's sums are scaled
+    constexpr int SPREAD = FEW ? 4 / FORM * (MODE == GEMM_SCALE_UE8M0_32 ? 2 : 1) : 1, FLUSHES = BLOCKS / SPREAD;
     // UE8M0 factors are taken 2^60 too large: code 0 (2^-127) is then a normal number, and a sum of 256 products
     // under codes below 160 still stays below 2^121
     constexpr uint32_t BIAS = MODE == GEMM_SCALE_UE8M0_32 ? 60 : 0;
     constexpr float UNBIAS = MODE == GEMM_SCALE_UE8M0_32 ? 0x1p-60f : 1.f;
-    extern __shared__ uint4 smem[];
-    uint4 *xf = smem;
-    float *xscale = reinterpret_cast<float *>(xf + (size_t)p.chunk_room * p.M * BLOCKS * 4);
-    float *parts = xscale + (SCALED_X ? p.chunk_room * ROWS_X : 0);     // [2][WARPS][NT][16][8]
-    constexpr int PART = NT * 16 * 8;
-    uint8_t *rings = reinterpret_cast<uint8_t *>(parts + 2 * WARPS * PART);
-    uint4 *zeros = reinterpret_cast<uint4 *>(rings + WARPS * AHEAD * SLOT<MODE, ALIGNED>);        // what rows past M read
+    constexpr int PART = 16 * FORM;
+    // each warp's ring; the sums to be joined [2][WARPS][16][FORM]; X; its scales
+    extern __shared__ __align__(128) uint4 smem[];
+    uint8_t *rings = reinterpret_cast<uint8_t *>(smem);
+    float *parts = reinterpret_cast<float *>(rings + WARPS * AHEAD * SLOT<MODE, ALIGNED>);
+    uint8_t *xf = reinterpret_cast<uint8_t *>(parts + 2 * WARPS * PART);
+    float *xscale = reinterpret_cast<float *>(xf + p.M * p.x_stride);
 
     uint32_t cluster;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
@@ -338,22 +387,32 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
 #pragma unroll 1
     for (int j = 0; j < AHEAD - 1; ++j) request();
 
-    if (threadIdx.x == 0) zeros[0] = make_uint4(0, 0, 0, 0);
     if (SCALED_X)
-        for (int i = threadIdx.x; i < (hi - lo) * ROWS_X; i += WARPS * 32) xscale[i] = 0.f;
+        for (int i = threadIdx.x; i < (hi - lo) * FORM; i += WARPS * 32) xscale[i] = 0.f;
     __syncthreads();
-    stage_x<XT>(p, lo, hi, ROWS_X, UNBIAS, xf, xscale);
+    stage_x<XT>(p, lo, hi, FORM, UNBIAS, xf, xscale);
     __syncthreads();
 
-    // the lane's word of X (row nt * 8 + g) in block 0, and the step from block to block
-    const uint4 *x_lane[NT];
-    int x_step[NT];
+    // The lane's word of X in block 0 of the CTA's first chunk, and whether it has one (in which blocks of SPREAD).
+    // Lanes without keep zeros in the registers that the others load.
+    uint32_t x_lane[NT];
+    bool x_on[NT];
+    int x_turn = 0;
+    uint4 x[SPREAD * NT];
+#pragma unroll
+    for (int i = 0; i < SPREAD * NT; ++i) x[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const bool in = nt * 8 + g < p.M;
-        x_lane[nt] = in ? xf + (nt * 8 + g) * 4 + t : zeros;
-        x_step[nt] = in ? p.M * 4 : 0;
+        const int m = FEW ? g / 2 % FORM : nt * 8 + g;
+        x_on[nt] = m < p.M && (!FEW || MODE == GEMM_SCALE_UE8M0_32 || (g & 1) == t / 2);
+        x_lane[nt] = smem_addr(xf + (x_on[nt] ? m : 0) * p.x_stride + t * 16);
     }
+    if (FEW) x_turn = MODE == GEMM_SCALE_UE8M0_32 ? g / 2 / FORM * 2 + (g & 1) : g / 2 / FORM;
+    // the lane's row address for ldmatrix: lanes 0-7 columns 0-7 of block i, 8-15 columns 8-15, 16-31 the same of
+    // block i + 1
+    uint32_t w_lane[BLOCKS / 2];
+#pragma unroll
+    for (int i = 0; i < BLOCKS / 2; ++i) w_lane[i] = (lane & 15) * 128 + (((2 * i + (lane >> 4)) ^ lane) & 7) * 16;
     int slot = 0;
     for (int grp = first_group, turn = 0; grp < groups; grp += group_step, turn ^= 1) {
         float total[NT][4];
@@ -373,35 +432,65 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             const uint32_t w = ring + slot * SLOT<MODE, ALIGNED>;
             slot = slot + 1 == AHEAD ? 0 : slot + 1;
             const int lc = ch - lo;
-            float2 xs[NT];
+            float2 xs[NT];               // of rows 2t and 2t + 1; FEW: of row t % FORM
             bool fine = true;
             if (SCALED_X) {
                 float worst = 0.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    xs[nt] = *reinterpret_cast<const float2 *>(xscale + lc * ROWS_X + nt * 8 + 2 * t);
+                    const float *at = xscale + lc * FORM + (FEW ? t % FORM : nt * 8 + 2 * t);
+                    xs[nt] = FEW ? make_float2(at[0], 0.f) : *reinterpret_cast<const float2 *>(at);
                     worst = fminf(worst, fminf(xs[nt].x, xs[nt].y));
                 }
                 fine = worst >= 0.f;
             }
-            uint32_t code[2][CODES<MODE> / 4];       // the codes of columns g and g + 8
+            // FEW: the lane's pair of codes for each flush, of columns g and g + 8; else those columns' codes
+            constexpr int CODE_WORDS = FEW ? FLUSHES : CODES<MODE> / 4;
+            uint32_t code[2][CODE_WORDS];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const uint32_t sf = w + W_BYTES + (g + 8 * r) * SF_STRIDE<MODE, ALIGNED>;
-                uint32_t v[SF_WORDS<MODE, ALIGNED>];
+                if constexpr (FEW && FORM < 4) {
 #pragma unroll
-                for (int i = 0; i < SF_WORDS<MODE, ALIGNED>; ++i) v[i] = load_shared(sf + 4 * i);
+                    for (int f = 0; f < FLUSHES; ++f) {
+                        const uint32_t at = sf + (f * (4 / FORM) + t / FORM) * 2;
+                        code[r][f] = ALIGNED ? load_shared_u16(at)
+                                             : load_shared_u8(at + shift[r] / 8) | load_shared_u8(at + shift[r] / 8 + 1) << 8;
+                    }
+                } else {
+                    uint32_t v[CODES<MODE> / 4 + 1];
+                    if constexpr (ALIGNED && MODE == GEMM_SCALE_UE8M0_32) {
+                        const uint2 l = load_shared2(sf);
+                        v[0] = l.x;
+                        v[1] = l.y;
+                    } else if constexpr (ALIGNED) {
+                        const uint4 l = load_shared4(sf);
+                        v[0] = l.x;
+                        v[1] = l.y;
+                        v[2] = l.z;
+                        v[3] = l.w;
+                    } else {
+                        uint32_t l[SF_WORDS<MODE, ALIGNED>];
 #pragma unroll
-                for (int i = 0; i < CODES<MODE> / 4; ++i) code[r][i] = ALIGNED ? v[i] : __funnelshift_r(v[i], v[i + !ALIGNED], shift[r]);
+                        for (int i = 0; i < SF_WORDS<MODE, ALIGNED>; ++i) l[i] = load_shared(sf + 4 * i);
+#pragma unroll
+                        for (int i = 0; i < CODES<MODE> / 4; ++i) v[i] = __funnelshift_r(l[i], l[i + 1], shift[r]);
+                    }
+#pragma unroll
+                    for (int f = 0; f < CODE_WORDS; ++f) code[r][f] = !FEW ? v[f] : f & 1 ? v[f / 2] >> 16 : v[f / 2] & 0xFFFFu;
+                }
                 // a code from 160 on has its top bit and one of the next two set
-                if (MODE == GEMM_SCALE_UE8M0_32)
-                    fine = fine && ((code[r][0] & (code[r][0] << 1 | code[r][0] << 2) | code[r][1] & (code[r][1] << 1 | code[r][1] << 2)) &
-                                    0x80808080u) == 0;
+                if (MODE == GEMM_SCALE_UE8M0_32) {
+                    uint32_t high = 0;
+#pragma unroll
+                    for (int f = 0; f < CODE_WORDS; ++f) high |= code[r][f] & (code[r][f] << 1 | code[r][f] << 2);
+                    fine = fine && (high & 0x80808080u) == 0;
+                }
             }
-            if (((SCALED_X || MODE == GEMM_SCALE_UE8M0_32) && !__all_sync(0xFFFFFFFFu, fine))) {
+            if ((SCALED_X || MODE == GEMM_SCALE_UE8M0_32) && !__all_sync(0xFFFFFFFFu, fine)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float4 add = products_fp32<XT, MODE>(p, n0, ch, nt * 8);
+                    const float4 add = products_fp32<XT, MODE, FEW>(p, n0, ch, nt * 8);
                     total[nt][0] += add.x;
                     total[nt][1] += add.y;
                     total[nt][2] += add.z;
@@ -414,71 +503,92 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[nt][i] = 0.f;
-            uint32_t mul[2][BLOCKS / 2]; // UE4M3: the lane's scales in blocks 2 i and 2 i + 1
-            if constexpr (MODE == GEMM_SCALE_UE4M3_16) {
+            uint32_t mul[2][BLOCKS];     // UE4M3 with more than four rows: the lane's scale in each block, twice
+            if constexpr (MODE == GEMM_SCALE_UE4M3_16 && !FEW) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int i = 0; i < BLOCKS; i += 4) {
-                        // even codes for lanes t = 0, 1 (a block's first 16 k), odd ones for t = 2, 3
-                        const uint32_t mine = __byte_perm(code[r][i / 2], code[r][i / 2 + 1], t < 2 ? 0x6420u : 0x7531u);
-                        mul[r][i / 2] = ue4m3x2(mine & 0xFFFFu);
-                        mul[r][i / 2 + 1] = ue4m3x2(mine >> 16);
+                    for (int i = 0; i < BLOCKS; i += 2) {
+                        // even codes for lanes t = 0, 1 (a block's first 16 k), odd ones for t = 2, 3, each twice
+                        const uint32_t twice = __byte_perm(code[r][i / 2], 0, t < 2 ? 0x2200u : 0x3311u) & 0x7F7F7F7Fu;
+                        mul[r][i] = ue4m3x2(twice);
+                        mul[r][i + 1] = ue4m3x2(twice >> 16);
                     }
             }
             uint32_t q[4];               // words of (block i, columns g and g + 8), (block i + 1, the same)
+            float acc[NT][4];
 #pragma unroll
             for (int i = 0; i < BLOCKS; ++i) {
-                if ((i & 1) == 0) {
-                    // row address: lanes 0-7 columns 0-7 of block i, 8-15 columns 8-15, 16-31 the same of block i + 1
-                    const int c = lane & 15, b = i + (lane >> 4);
-                    matrices(w + c * 128 + ((b ^ c) & 7) * 16, q);
-                }
+                if (i % 2 == 0) matrices(w + w_lane[i / 2], q);
                 uint32_t a[2][4];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     e2m1x8(q[(i & 1) * 2 + r], a[r]);
-                    if constexpr (MODE == GEMM_SCALE_UE4M3_16) {
+                    if constexpr (MODE == GEMM_SCALE_UE4M3_16 && !FEW) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) a[r][e] = i & 1 ? mul2_high(a[r][e], mul[r][i / 2]) : mul2_low(a[r][e], mul[r][i / 2]);
+                        for (int e = 0; e < 4; ++e) a[r][e] = mul2(a[r][e], mul[r][i]);
                     }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 x = x_lane[nt][(lc * BLOCKS + i) * x_step[nt]];
-                    if (MODE == GEMM_SCALE_UE4M3_16) {
-                        mma_16816(sum[nt], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                        mma_16816(sum[nt], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
-                    } else {
-                        float acc[4];
-                        mma_16816_zero(acc, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                        mma_16816(acc, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                    uint4 &b = x[i % SPREAD * NT + nt];
+                    load_shared4_if(x_on[nt] && (!FEW || x_turn == i % SPREAD), b, x_lane[nt] + lc * (CHUNK * 2) + i * 64);
+                    if constexpr (MODE == GEMM_SCALE_UE4M3_16 && !FEW) {
+                        mma_16816(sum[nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                        mma_16816(sum[nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+                        continue;
+                    }
+                    if (i % SPREAD == 0) mma_16816_zero(acc[nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                    else mma_16816(acc[nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                    mma_16816(acc[nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+                    if (i % SPREAD != SPREAD - 1) continue;
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
+                    for (int r = 0; r < 2; ++r) {
+                        // the factors of a row's two sums
+                        float2 s;
+                        if constexpr (MODE == GEMM_SCALE_UE4M3_16) {
+                            s = halves(ue4m3x2(code[r][i / SPREAD] & 0x7F7Fu));
+                        } else {
                             // 2^(code - 127 + BIAS)
-                            const uint32_t byte = code[r][i / 4] & 0xFFu << (8 * (i & 3));
-                            const float s = __uint_as_float(((i & 3) == 3 ? byte >> 1 : byte << (23 - 8 * (i & 3))) + (BIAS << 23));
-                            sum[nt][2 * r] = fmaf(acc[2 * r], s, sum[nt][2 * r]);
-                            sum[nt][2 * r + 1] = fmaf(acc[2 * r + 1], s, sum[nt][2 * r + 1]);
+                            const uint32_t pair = FEW ? code[r][i / SPREAD] : code[r][i / 4];
+                            const int k = FEW ? 0 : i % 4;
+                            const uint32_t one = pair & 0xFFu << (8 * k), two = pair & 0xFF00u;
+                            s.x = __uint_as_float((k == 3 ? one >> 1 : one << (23 - 8 * k)) + (BIAS << 23));
+                            s.y = FEW ? __uint_as_float((two << 15) + (BIAS << 23)) : s.x;
                         }
+                        const float2 d = fma2(make_float2(acc[nt][2 * r], acc[nt][2 * r + 1]), s,
+                                              make_float2(sum[nt][2 * r], sum[nt][2 * r + 1]));
+                        sum[nt][2 * r] = d.x;
+                        sum[nt][2 * r + 1] = d.y;
                     }
                 }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    total[nt][i] = fmaf(sum[nt][i], SCALED_X ? (i & 1 ? xs[nt].y : xs[nt].x) : UNBIAS, total[nt][i]);
+                for (int i = 0; i < 4; ++i) {
+                    const float factor = !SCALED_X ? UNBIAS : i & 1 && !FEW ? xs[nt].y : xs[nt].x;
+                    total[nt][i] = fmaf(sum[nt][i], factor, total[nt][i]);
+                }
         }
 
         // join the slices of K: the CTA's, and the cluster's, always in the same order.  The two buffers
         // take turns, so the barrier of the next tile also says that this one's sums have been read.
         float *mine = parts + (turn * WARPS + warp) * PART;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            *reinterpret_cast<float2 *>(mine + (nt * 16 + g) * 8 + 2 * t) = make_float2(total[nt][0], total[nt][1]);
-            *reinterpret_cast<float2 *>(mine + (nt * 16 + g + 8) * 8 + 2 * t) = make_float2(total[nt][2], total[nt][3]);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float *at = mine + (g + 8 * r) * FORM + nt * 8;
+                if constexpr (FEW) {                     // a row's columns of the MMA
+                    float v = total[nt][2 * r] + total[nt][2 * r + 1];
+                    if (FORM <= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                    if (FORM <= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+                    if (t < FORM) at[t] = v;
+                } else {
+                    *reinterpret_cast<float2 *>(at + 2 * t) = make_float2(total[nt][2 * r], total[nt][2 * r + 1]);
+                }
+            }
         if (cluster == 1) __syncthreads();
         else {
             __syncwarp();
@@ -489,7 +599,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             const int row = i & 15, m = (i >> 4) % p.M, tile = (i >> 4) / p.M;
             const int n = (grp * R + tile) * 16 + row;
             if (n >= p.N) continue;
-            const int at = (turn * WARPS + tile * S) * PART + ((m >> 3) * 16 + row) * 8 + (m & 7);
+            const int at = (turn * WARPS + tile * S) * PART + row * FORM + m;
             float v = 0.f;
             if (cluster == 1) {
                 for (int s = 0; s < S; ++s) v += parts[at + s * PART];
@@ -516,13 +626,12 @@ int slot_bytes(int mode, int K) {
 
 // How the product is cut (see the head of this file)
 struct MatvecShape {
-    int slices, cluster, chunk_room, smem, grid;
+    int slices, cluster, x_stride, smem, grid;
 };
 // resident[c]: clusters of c CTAs that run at once
 MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, const int *resident) {
-    const int nt = M > 8 ? 2 : 1, chunks = (K + CHUNK - 1) / CHUNK, tiles = (N + 15) / 16;
-    const int per_chunk = M * CHUNK * 2 + (scaled_x ? nt * 8 * 4 : 0);
-    const int fixed = 2 * WARPS * nt * 16 * 8 * 4 + WARPS * AHEAD * slot + 16;
+    const int chunks = (K + CHUNK - 1) / CHUNK, tiles = (N + 15) / 16, form = form_of(M);
+    const int fixed = WARPS * AHEAD * slot + 2 * WARPS * 16 * form * 4;
     MatvecShape best{};
     double best_cost = 0;
     for (int c = 1; c <= MOST_CLUSTER && c <= chunks; ++c)
@@ -530,15 +639,16 @@ MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, const int
             MatvecShape s;
             s.cluster = c;
             s.slices = S;
-            s.chunk_room = (chunks + c - 1) / c;
-            s.smem = s.chunk_room * per_chunk + fixed;
+            const int room = (chunks + c - 1) / c;
+            s.x_stride = room * CHUNK * 2 + 64;
+            s.smem = fixed + M * s.x_stride + (scaled_x ? room * form * 4 : 0);
             if (s.smem > MOST_SMEM || resident[c] == 0) continue;
             const int R = WARPS / S, groups = (tiles + R - 1) / R, clusters = groups < resident[c] ? groups : resident[c];
             s.grid = clusters * c;
             // chunks a warp walks one after another, plus what starting up and joining cost in chunks
             const int turns = (groups + clusters - 1) / clusters;
             const double walk = turns * ((chunks + c * S - 1) / (c * S));
-            const double stage = 0.25 * M * s.chunk_room / WARPS, join = turns * (c > 1 ? 2.0 : 0.5);
+            const double stage = 0.25 * M * room / WARPS, join = turns * (c > 1 ? 2.0 : 0.5);
             const double cost = walk + stage + join;
             if (best.grid == 0 || cost < best_cost) {
                 best = s;
@@ -567,7 +677,7 @@ void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, int grid
 
 constexpr int MAX_DEVICES = 64;
 
-template <typename XT, int MODE, int NT, bool ALIGNED>
+template <typename XT, int MODE, int FORM, bool ALIGNED>
 cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
     static std::mutex mu;
     static bool ready[MAX_DEVICES];
@@ -577,7 +687,7 @@ cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t str
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[dev]) {
-            e = cudaFuncSetAttribute(matvec_kernel<XT, MODE, NT, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SMEM);
+            e = cudaFuncSetAttribute(matvec_kernel<XT, MODE, FORM, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SMEM);
             if (e != cudaSuccess) return e;
             ready[dev] = true;
         }
@@ -585,7 +695,7 @@ cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t str
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
     cluster_config(cfg, attr, s.grid, s.cluster, s.smem, stream);
-    return cudaLaunchKernelEx(&cfg, matvec_kernel<XT, MODE, NT, ALIGNED>, p);
+    return cudaLaunchKernelEx(&cfg, matvec_kernel<XT, MODE, FORM, ALIGNED>, p);
 }
 
 // How many clusters of 1 .. 8 CTAs run at once on the current device (asked once: one CTA fills an SM whatever
@@ -598,7 +708,7 @@ cudaError_t resident_clusters(const int **out) {
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
     if (known[dev][1] == 0) {
-        const auto kernel = matvec_kernel<__half, GEMM_SCALE_UE4M3_16, 1, true>;
+        const auto kernel = matvec_kernel<__half, GEMM_SCALE_UE4M3_16, 16, true>;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SMEM);
         int found[MOST_CLUSTER + 1] = {};
         for (int c = 1; c <= MOST_CLUSTER && e == cudaSuccess; ++c) {
@@ -614,10 +724,19 @@ cudaError_t resident_clusters(const int **out) {
     return cudaSuccess;
 }
 
+template <typename XT, int MODE, bool ALIGNED>
+cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
+    switch (form_of(p.M)) {
+        case 1: return launch<XT, MODE, 1, ALIGNED>(s, p, stream);
+        case 2: return launch<XT, MODE, 2, ALIGNED>(s, p, stream);
+        case 4: return launch<XT, MODE, 4, ALIGNED>(s, p, stream);
+        case 8: return launch<XT, MODE, 8, ALIGNED>(s, p, stream);
+        default: return launch<XT, MODE, 16, ALIGNED>(s, p, stream);
+    }
+}
 template <typename XT, int MODE>
 cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
-    if (p.K % CHUNK == 0) return p.M > 8 ? launch<XT, MODE, 2, true>(s, p, stream) : launch<XT, MODE, 1, true>(s, p, stream);
-    return p.M > 8 ? launch<XT, MODE, 2, false>(s, p, stream) : launch<XT, MODE, 1, false>(s, p, stream);
+    return p.K % CHUNK == 0 ? launch<XT, MODE, true>(s, p, stream) : launch<XT, MODE, false>(s, p, stream);
 }
 template <typename XT>
 cudaError_t launch(int mode, const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
@@ -648,13 +767,18 @@ extern "C" gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dty
     if (st != GEMM_OK) return st;
     const int *resident = nullptr;
     if (resident_clusters(&resident) != cudaSuccess) return GEMM_ERR_CUDA;
-    // nine rows or more whose activations fit no cluster's shared memory (K past some 20000) go in two halves
     const int slot = slot_bytes(block_scaled, (int)K);
-    MatvecShape s = matvec_shape((int)M, (int)N, (int)K, x == GEMM_BF16, slot, resident);
-    const int first = s.grid ? (int)M : 8;
-    for (int m = 0; m < (int)M; m += first) {
-        const int rows = (int)M - m < first ? (int)M - m : first;
-        if (first != (int)M) s = matvec_shape(rows, (int)N, (int)K, x == GEMM_BF16, slot, resident);
+    // rows whose activations fit no cluster's shared memory (16 of them from K about 18000 on, 8 from about 31000)
+    // go in several passes
+    int most = (int)M;
+    MatvecShape s = matvec_shape(most, (int)N, (int)K, x == GEMM_BF16, slot, resident);
+    while (s.grid == 0 && most > 1) {
+        most = (most + 1) / 2;
+        s = matvec_shape(most, (int)N, (int)K, x == GEMM_BF16, slot, resident);
+    }
+    for (int m = 0; m < (int)M; m += most) {
+        const int rows = (int)M - m < most ? (int)M - m : most;
+        if (rows != most) s = matvec_shape(rows, (int)N, (int)K, x == GEMM_BF16, slot, resident);
         if (s.grid == 0) return GEMM_ERR_CUDA;
         const int64_t out = (int64_t)m * N;
         const MatvecParams p{static_cast<const uint8_t *>(X) + (int64_t)m * K * 2,
@@ -667,7 +791,7 @@ extern "C" gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dty
                              (int)K,
                              d == GEMM_BF16,
                              s.slices,
-                             s.chunk_room};
+                             s.x_stride};
         cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
         const cudaError_t e = x == GEMM_F16 ? launch<__half>(block_scaled, s, p, stream)
                                             : launch<__nv_bfloat16>(block_scaled, s, p, stream);
