@@ -37,7 +37,6 @@
 // A CTA (one per SM) is 16 warps: R tiles of 16 columns by S slices of K, and `c` CTAs of a cluster split K
 // further; the partial sums are joined in a fixed order through shared memory, the cluster's through
 // distributed shared memory.
-#include <cstdio>
 #include <initializer_list>
 #include <mutex>
 #include <type_traits>
@@ -53,10 +52,7 @@ constexpr int64_t MAX_K = 32768;
 constexpr int WARPS = 16;
 constexpr int CHUNK = 256;           // k per step of a warp
 constexpr int BLOCKS = CHUNK / 32;   // 32-k blocks of a chunk: a column's 16-byte pieces
-#ifndef GB300_MATVEC_AHEAD
-#define GB300_MATVEC_AHEAD 3
-#endif
-constexpr int AHEAD = GB300_MATVEC_AHEAD;      // ring slots per warp
+constexpr int AHEAD = 3;      // ring slots per warp
 constexpr int MOST_CLUSTER = 8;
 constexpr int MOST_SMEM = 226 * 1024;
 constexpr int W_BYTES = 16 * CHUNK / 2;        // weights of a slot
@@ -82,10 +78,15 @@ struct MatvecParams {
     const float *c;
     void *d;
     int M, N, K;
+    uint32_t inverse_m;  // ceil(2^16 / M)
     int out_bf16;
     int slices;          // slices of K per CTA (S)
     int x_stride;        // bytes of shared memory per row of X
+    int held;            // tiles of a warp whose sums are kept before they are joined
 };
+
+// i / M for i < 4096, M <= 16
+__device__ __forceinline__ int over_m(int i, uint32_t inverse_m) { return (int)((uint32_t)i * inverse_m >> 16); }
 
 // eight packed e2m1 values (k ascending from the low nibble) to four pairs of halves
 __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
@@ -257,11 +258,21 @@ __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int 
 // some row does not convert exactly.
 template <typename XT>
 __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int rows_x, float unbias, uint8_t *xf, float *scale) {
-    const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < (hi - lo) * p.M; i += WARPS) {
-        const int lc = i / p.M, m = i - lc * p.M, k = (lo + lc) * CHUNK + lane * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (k < p.K) v = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + (int64_t)m * p.K + k);
+    constexpr int BATCH = 4;             // loads in flight per lane
+    const int lane = threadIdx.x & 31, all = (hi - lo) * p.M;
+    for (int first = threadIdx.x >> 5; first < all; first += WARPS * BATCH) {
+        uint4 in[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int i = first + j * WARPS, lc = over_m(i, p.inverse_m), m = i - lc * p.M, k = (lo + lc) * CHUNK + lane * 8;
+            in[j] = make_uint4(0, 0, 0, 0);
+            if (i < all && k < p.K) in[j] = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + (int64_t)m * p.K + k);
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+        const int i = first + j * WARPS, lc = over_m(i, p.inverse_m), m = i - lc * p.M;
+        if (i >= all) break;
+        uint4 v = in[j];
         if constexpr (!std::is_same<XT, __half>::value) {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
@@ -281,10 +292,11 @@ __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, i
                 h[q] = *reinterpret_cast<const uint32_t *>(&r);
             }
             v = make_uint4(h[0], h[1], h[2], h[3]);
-            const bool all = __all_sync(0xFFFFFFFFu, fine);
-            if (lane == 0) scale[lc * rows_x + m] = all ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) * unbias : -1.f;
+            const bool exact = __all_sync(0xFFFFFFFFu, fine);
+            if (lane == 0) scale[lc * rows_x + m] = exact ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) * unbias : -1.f;
         }
         *reinterpret_cast<uint4 *>(xf + m * p.x_stride + lc * CHUNK * 2 + lane * 16) = v;
+        }
     }
 }
 
@@ -300,11 +312,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     constexpr uint32_t BIAS = MODE == GEMM_SCALE_UE8M0_32 ? 60 : 0;
     constexpr float UNBIAS = MODE == GEMM_SCALE_UE8M0_32 ? 0x1p-60f : 1.f;
     constexpr int PART = 16 * FORM;
-    // each warp's ring; the sums to be joined [2][WARPS][16][FORM]; X; its scales
+    // each warp's ring; the sums to be joined [held][WARPS][16][FORM]; X; its scales
     extern __shared__ __align__(128) uint4 smem[];
     uint8_t *rings = reinterpret_cast<uint8_t *>(smem);
     float *parts = reinterpret_cast<float *>(rings + WARPS * AHEAD * SLOT<MODE, ALIGNED>);
-    uint8_t *xf = reinterpret_cast<uint8_t *>(parts + 2 * WARPS * PART);
+    uint8_t *xf = reinterpret_cast<uint8_t *>(parts + p.held * WARPS * PART);
     float *xscale = reinterpret_cast<float *>(xf + p.M * p.x_stride);
 
     uint32_t cluster;
@@ -414,7 +426,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < BLOCKS / 2; ++i) w_lane[i] = (lane & 15) * 128 + (((2 * i + (lane >> 4)) ^ lane) & 7) * 16;
     int slot = 0;
-    for (int grp = first_group, turn = 0; grp < groups; grp += group_step, turn ^= 1) {
+    for (int grp = first_group, turn = 0; grp < groups; grp += group_step) {
         float total[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -516,7 +528,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                     }
             }
             uint32_t q[4];               // words of (block i, columns g and g + 8), (block i + 1, the same)
-            float acc[NT][4];
+            // sums that long chains of MMAs add to are kept twice, for every other MMA
+            constexpr int CHAINS = SPREAD >= 4 ? 2 : 1;
+            float acc[CHAINS][NT][4];
 #pragma unroll
             for (int i = 0; i < BLOCKS; ++i) {
                 if (i % 2 == 0) matrices(w + w_lane[i / 2], q);
@@ -538,9 +552,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                         mma_16816(sum[nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
                         continue;
                     }
-                    if (i % SPREAD == 0) mma_16816_zero(acc[nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
-                    else mma_16816(acc[nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
-                    mma_16816(acc[nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+                    if (i % SPREAD == 0) mma_16816_zero(acc[0][nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                    else mma_16816(acc[0][nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                    if (CHAINS == 2 && i % SPREAD == 0) mma_16816_zero(acc[1][nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+                    else mma_16816(acc[CHAINS - 1][nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
                     if (i % SPREAD != SPREAD - 1) continue;
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
@@ -556,8 +571,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                             s.x = __uint_as_float((k == 3 ? one >> 1 : one << (23 - 8 * k)) + (BIAS << 23));
                             s.y = FEW ? __uint_as_float((two << 15) + (BIAS << 23)) : s.x;
                         }
-                        const float2 d = fma2(make_float2(acc[nt][2 * r], acc[nt][2 * r + 1]), s,
-                                              make_float2(sum[nt][2 * r], sum[nt][2 * r + 1]));
+                        float2 v = make_float2(acc[0][nt][2 * r], acc[0][nt][2 * r + 1]);
+                        if (CHAINS == 2) {
+                            v.x += acc[1][nt][2 * r];
+                            v.y += acc[1][nt][2 * r + 1];
+                        }
+                        const float2 d = fma2(v, s, make_float2(sum[nt][2 * r], sum[nt][2 * r + 1]));
                         sum[nt][2 * r] = d.x;
                         sum[nt][2 * r + 1] = d.y;
                     }
@@ -572,8 +591,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                 }
         }
 
-        // join the slices of K: the CTA's, and the cluster's, always in the same order.  The two buffers
-        // take turns, so the barrier of the next tile also says that this one's sums have been read.
         float *mine = parts + (turn * WARPS + warp) * PART;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -589,30 +606,54 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                     *reinterpret_cast<float2 *>(at + 2 * t) = make_float2(total[nt][2 * r], total[nt][2 * r + 1]);
                 }
             }
-        if (cluster == 1) __syncthreads();
-        else {
+        if (++turn < p.held && grp + group_step < groups) continue;
+
+        // Join the slices of K: the CTA's, and the cluster's, always in the same order.
+        __syncthreads();
+        const int outputs = R * 16 * p.M;                // of a turn: n ascending, then row of X, then tile
+        auto place = [&](int b, int i, int &m, int &n) { // output i of turn b: where it goes, and its first slice's sum
+            const int tile = over_m(i >> 4, p.inverse_m);
+            m = (i >> 4) - tile * p.M;
+            n = ((grp - (turn - 1 - b) * group_step) * R + tile) * 16 + (i & 15);
+            return parts + (b * WARPS + tile * S) * PART + (i & 15) * FORM + m;
+        };
+        int m, n;
+        if (cluster != 1) {
+            for (int b = 0; b < turn && S > 1; ++b)
+                for (int i = threadIdx.x; i < outputs; i += WARPS * 32) {
+                    float *first = place(b, i, m, n), v = first[0];
+                    for (int s = 1; s < S; ++s) v += first[s * PART];
+                    first[0] = v;
+                }
             __syncwarp();
             cluster_sync();
         }
-        const int outputs = R * 16 * p.M;
-        for (int i = rank * WARPS * 32 + threadIdx.x; i < outputs; i += (int)cluster * WARPS * 32) {
-            const int row = i & 15, m = (i >> 4) % p.M, tile = (i >> 4) / p.M;
-            const int n = (grp * R + tile) * 16 + row;
-            if (n >= p.N) continue;
-            const int at = (turn * WARPS + tile * S) * PART + row * FORM + m;
-            float v = 0.f;
-            if (cluster == 1) {
-                for (int s = 0; s < S; ++s) v += parts[at + s * PART];
-            } else {
-                for (uint32_t r = 0; r < cluster; ++r) {
-                    const uint32_t from = mapa_shared(smem_addr(parts + at), r);
-                    for (int s = 0; s < S; ++s) v += load_cluster(from + s * PART * 4);
+        for (int b = 0; b < turn; ++b)
+            for (int i = rank * WARPS * 32 + threadIdx.x; i < outputs; i += (int)cluster * WARPS * 32) {
+                const float *first = place(b, i, m, n);
+                if (n >= p.N) continue;
+                const int64_t o = (int64_t)m * p.N + n;
+                const float c = p.c ? p.c[o] : 0.f;
+                float v = 0.f;
+                if (cluster == 1) {
+                    for (int s = 0; s < S; ++s) v += first[s * PART];
+                } else {
+                    float part[MOST_CLUSTER];
+#pragma unroll
+                    for (uint32_t r = 0; r < MOST_CLUSTER; ++r)
+                        part[r] = r < cluster ? load_cluster(mapa_shared(smem_addr(first), r)) : 0.f;
+#pragma unroll
+                    for (uint32_t r = 0; r < MOST_CLUSTER; ++r) v += part[r];
                 }
+                v += c;
+                if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.d)[o] = __float2bfloat16_rn(v);
+                else static_cast<float *>(p.d)[o] = v;
             }
-            const int64_t o = (int64_t)m * p.N + n;
-            if (p.c) v += p.c[o];
-            if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.d)[o] = __float2bfloat16_rn(v);
-            else static_cast<float *>(p.d)[o] = v;
+        turn = 0;
+        if (grp + group_step < groups) {                 // the sums have been read before others take their place
+            __syncwarp();
+            if (cluster == 1) __syncthreads();
+            else cluster_sync();
         }
     }
     __syncwarp();
@@ -626,12 +667,12 @@ int slot_bytes(int mode, int K) {
 
 // How the product is cut (see the head of this file)
 struct MatvecShape {
-    int slices, cluster, x_stride, smem, grid;
+    int slices, cluster, x_stride, held, smem, grid;
 };
 // resident[c]: clusters of c CTAs that run at once
 MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, const int *resident) {
     const int chunks = (K + CHUNK - 1) / CHUNK, tiles = (N + 15) / 16, form = form_of(M);
-    const int fixed = WARPS * AHEAD * slot + 2 * WARPS * 16 * form * 4;
+    const int ring = WARPS * AHEAD * slot, part = WARPS * 16 * form * 4;
     MatvecShape best{};
     double best_cost = 0;
     for (int c = 1; c <= MOST_CLUSTER && c <= chunks; ++c)
@@ -641,23 +682,23 @@ MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, const int
             s.slices = S;
             const int room = (chunks + c - 1) / c;
             s.x_stride = room * CHUNK * 2 + 64;
-            s.smem = fixed + M * s.x_stride + (scaled_x ? room * form * 4 : 0);
-            if (s.smem > MOST_SMEM || resident[c] == 0) continue;
+            const int base = ring + M * s.x_stride + (scaled_x ? room * form * 4 : 0);
+            if (base + part > MOST_SMEM || resident[c] == 0) continue;
             const int R = WARPS / S, groups = (tiles + R - 1) / R, clusters = groups < resident[c] ? groups : resident[c];
+            const int turns = (groups + clusters - 1) / clusters, fit = (MOST_SMEM - base) / part;
+            s.held = turns < fit ? turns : fit;
+            s.smem = base + s.held * part;
             s.grid = clusters * c;
             // chunks a warp walks one after another, plus what starting up and joining cost in chunks
-            const int turns = (groups + clusters - 1) / clusters;
+            const int joins = (turns + s.held - 1) / s.held;
             const double walk = turns * ((chunks + c * S - 1) / (c * S));
-            const double stage = 0.25 * M * room / WARPS, join = turns * (c > 1 ? 2.0 : 0.5);
+            const double stage = 0.1 * M * room / WARPS, join = 0.15 * turns + joins * (c > 1 ? 3.0 : 0.5);
             const double cost = walk + stage + join;
             if (best.grid == 0 || cost < best_cost) {
                 best = s;
                 best_cost = cost;
             }
         }
-#ifdef GB300_MATVEC_PRINT
-    printf("M %d N %d K %d: S %d c %d grid %d smem %d\n", M, N, K, best.slices, best.cluster, best.grid, best.smem);
-#endif
     return best;
 }
 
@@ -789,9 +830,11 @@ extern "C" gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dty
                              rows,
                              (int)N,
                              (int)K,
+                             (65536u + (uint32_t)rows - 1) / (uint32_t)rows,
                              d == GEMM_BF16,
                              s.slices,
-                             s.x_stride};
+                             s.x_stride,
+                             s.held};
         cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
         const cudaError_t e = x == GEMM_F16 ? launch<__half>(block_scaled, s, p, stream)
                                             : launch<__nv_bfloat16>(block_scaled, s, p, stream);
