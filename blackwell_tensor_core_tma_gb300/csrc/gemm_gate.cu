@@ -6,7 +6,7 @@
 //
 // The checkpoint keeps g and u as e4m3 codes with a UE8M0 scale per 32: a quarter of fp32's bytes.
 // The gradient is that of the unit at the checkpoint's values.  Both kernels are one pass over
-// memory: a thread takes eight consecutive elements of each half of a row.
+// memory: a thread takes 16 (forward) or 8 (backward) consecutive elements of each half of a row.
 #include <initializer_list>
 
 #include "gemm_rows.cuh"
@@ -16,63 +16,54 @@ namespace {
 
 using namespace rows;
 
-// s * g and s itself; exp(-g) infinite gives s = 0
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
+// 1 / (1 + exp(-g)), with the fast exponential and reciprocal (2 + 1.173 |g| and 1 units in the last place): the
+// outputs are rounded to 8 or 16 bits or compared at 1e-6.  exp(-g) infinite gives 0.
+__device__ __forceinline__ float sigmoid(float g) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
+    return r;
+}
 
 struct GateParams {
     const void *z;
     void *a;
     uint8_t *sfa, *ck, *sfck;
-    int64_t M;
+    Units units;
     int F;
 };
 
-// Units are counted as if every row had whole blocks of four, so that a block never straddles the
-// lanes of two rows; the units past a row's end do nothing.
-__device__ __forceinline__ bool place(int64_t i, int per_row, int F, int64_t M, int64_t &row, int &u) {
-    row = i / per_row;
-    u = (int)(i - row * per_row);
-    return row < M && u * UNIT < F;
-}
-
 template <typename ZT, typename AT>
-__global__ void __launch_bounds__(256) gate_kernel(GateParams p) {
-    const int blocks = (p.F + BLOCK - 1) / BLOCK, per_row = blocks * 4;
+__global__ void __launch_bounds__(256) gate_kernel(const __grid_constant__ GateParams p) {
+    constexpr int N = 16;
+    const int blocks = (p.F + BLOCK - 1) / BLOCK;
     int64_t row;
     int u;
-    const bool on = place((int64_t)blockIdx.x * 256 + threadIdx.x, per_row, p.F, p.M, row, u);
-    float g[UNIT], v[UNIT], a[UNIT];
-#pragma unroll
-    for (int i = 0; i < UNIT; ++i) g[i] = v[i] = 0.f;
-    if (on) {
-        const ZT *z = static_cast<const ZT *>(p.z) + row * 2 * p.F + u * UNIT;
-        load_unit(z, g);
-        load_unit(z + p.F, v);
+    const bool on = p.units.place(blockIdx.x * 256 + threadIdx.x, row, u) && u * N < p.F;
+    float g[N], v[N], a[N];
+    {
+        uint4 gq[PIECES<ZT, N>], vq[PIECES<ZT, N>];
+        const ZT *z = static_cast<const ZT *>(p.z) + row * 2 * p.F + u * N;
+        load_pieces(z, on, gq);
+        load_pieces(z + p.F, on, vq);
+        unpack(z, gq, g);
+        unpack(z, vq, v);
     }
 #pragma unroll
-    for (int i = 0; i < UNIT; ++i) a[i] = g[i] * sigmoid(g[i]) * v[i];
+    for (int i = 0; i < N; ++i) a[i] = g[i] * sigmoid(g[i]) * v[i];
+    const bool first = on && (u & 1) == 0;           // of its block
     uint32_t code;
     if constexpr (sizeof(AT) == 1) {
-        const uint2 q = quantise_unit(a, code);
-        if (on) {
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.a) + row * p.F + u * UNIT) = q;
-            if ((u & 3) == 0) p.sfa[row * blocks + u / 4] = (uint8_t)code;
-        }
+        code = quantise(a, static_cast<uint8_t *>(p.a) + row * p.F + u * N, on);
+        if (first) p.sfa[row * blocks + u / 2] = (uint8_t)code;
     } else if (on) {
-        store_unit(static_cast<AT *>(p.a) + row * p.F + u * UNIT, a);
+        store(static_cast<AT *>(p.a) + row * p.F + u * N, a);
     }
     if (p.ck) {
-        uint8_t *ck = p.ck + row * 2 * p.F + u * UNIT, *sf = p.sfck + row * 2 * blocks + u / 4;
-        uint2 q = quantise_unit(g, code);
-        if (on) {
-            *reinterpret_cast<uint2 *>(ck) = q;
-            if ((u & 3) == 0) sf[0] = (uint8_t)code;
-        }
-        q = quantise_unit(v, code);
-        if (on) {
-            *reinterpret_cast<uint2 *>(ck + p.F) = q;
-            if ((u & 3) == 0) sf[blocks] = (uint8_t)code;
-        }
+        uint8_t *ck = p.ck + row * 2 * p.F + u * N, *sf = p.sfck + row * 2 * blocks + u / 2;
+        code = quantise(g, ck, on);
+        if (first) sf[0] = (uint8_t)code;
+        code = quantise(v, ck + p.F, on);
+        if (first) sf[blocks] = (uint8_t)code;
     }
 }
 
@@ -80,36 +71,34 @@ struct GateBackParams {
     const void *da;
     const uint8_t *ck, *sfck;
     void *dz, *a;
-    int64_t M;
+    Units units;
     int F;
 };
 
 template <typename GT, typename ZT, typename AT>
-__global__ void __launch_bounds__(256) gate_back_kernel(GateBackParams p) {
+__global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ GateBackParams p) {
+    constexpr int N = 8;             // no block is shared: the smaller unit keeps each access of a warp contiguous
     const int blocks = (p.F + BLOCK - 1) / BLOCK;
     int64_t row;
     int u;
-    if (!place((int64_t)blockIdx.x * 256 + threadIdx.x, p.F / UNIT, p.F, p.M, row, u)) return;
-    const uint8_t *ck = p.ck + row * 2 * p.F + u * UNIT, *sf = p.sfck + row * 2 * blocks + u / 4;
-    float g[UNIT], v[UNIT], d[UNIT], a[UNIT];
-    load_unit(static_cast<const GT *>(p.da) + row * p.F + u * UNIT, d);
-    decode_unit(*reinterpret_cast<const uint2 *>(ck), scale_value(sf[0]), g);
-    decode_unit(*reinterpret_cast<const uint2 *>(ck + p.F), scale_value(sf[blocks]), v);
+    if (!p.units.place(blockIdx.x * 256 + threadIdx.x, row, u)) return;
+    const uint8_t *ck = p.ck + row * 2 * p.F + u * N, *sf = p.sfck + row * 2 * blocks + u / 4;
+    float g[N], v[N], d[N], a[N];
+    load(static_cast<const GT *>(p.da) + row * p.F + u * N, d);
+    decode(*reinterpret_cast<const uint2 *>(ck), scale_value(sf[0]), g);
+    decode(*reinterpret_cast<const uint2 *>(ck + p.F), scale_value(sf[blocks]), v);
 #pragma unroll
-    for (int i = 0; i < UNIT; ++i) {
+    for (int i = 0; i < N; ++i) {
         const float s = sigmoid(g[i]), gs = g[i] * s, dgs = s * (1.f + g[i] * (1.f - s));
         a[i] = gs * v[i];
         g[i] = d[i] * v[i] * dgs;
         d[i] *= gs;
     }
-    ZT *dz = static_cast<ZT *>(p.dz) + row * 2 * p.F + u * UNIT;
-    store_unit(dz, g);
-    store_unit(dz + p.F, d);
-    if (p.a) store_unit(static_cast<AT *>(p.a) + row * p.F + u * UNIT, a);
+    ZT *dz = static_cast<ZT *>(p.dz) + row * 2 * p.F + u * N;
+    store(dz, g);
+    store(dz + p.F, d);
+    if (p.a) store(static_cast<AT *>(p.a) + row * p.F + u * N, a);
 }
-
-// CTAs for n threads' work
-unsigned ctas(int64_t n) { return (unsigned)((n + 255) / 256); }
 
 template <typename ZT>
 cudaError_t gate_launch(gemm_dtype a, unsigned n, const GateParams &p, cudaStream_t stream) {
@@ -128,7 +117,6 @@ cudaError_t back_launch(gemm_dtype a, unsigned n, const GateBackParams &p, cudaS
 bool real(gemm_dtype t) { return t == GEMM_F32 || t == GEMM_BF16; }
 gemm_status check_sizes(int64_t M, int64_t F) {
     if (M < 0 || F <= 0 || M > INT32_MAX || F > (1 << 20)) return GEMM_ERR_INVALID_ARG;
-    if (M * ((F + BLOCK - 1) / BLOCK * 4) / 256 >= INT32_MAX) return GEMM_ERR_UNSUPPORTED;   // more CTAs than a launch holds
     return F % 16 == 0 ? GEMM_OK : GEMM_ERR_ALIGNMENT;
 }
 
@@ -140,7 +128,7 @@ using namespace gb300;
 extern "C" gemm_status gemm_gate_run(int64_t M, int64_t F, gemm_dtype z, gemm_dtype a, const void *Z, void *A,
                                      uint8_t *SFA, uint8_t *CK, uint8_t *SFCK, void *cuda_stream) {
     gemm_status st = check_sizes(M, F);
-    if (st == GEMM_ERR_INVALID_ARG || st == GEMM_ERR_UNSUPPORTED) return st;
+    if (st == GEMM_ERR_INVALID_ARG) return st;
     if (!real(z) || (a != GEMM_E4M3 && a != GEMM_BF16 && a != GEMM_F16)) return GEMM_ERR_UNSUPPORTED;
     if (st != GEMM_OK || M == 0) return st;
     if (!Z || !A || (a == GEMM_E4M3 && !SFA) || (CK && !SFCK)) return GEMM_ERR_INVALID_ARG;
@@ -149,19 +137,20 @@ extern "C" gemm_status gemm_gate_run(int64_t M, int64_t F, gemm_dtype z, gemm_dt
     int sms = 0;
     st = rows::device_sms(&sms);
     if (st != GEMM_OK) return st;
-    const GateParams p{Z, A, SFA, CK, SFCK, M, (int)F};
-    const unsigned n = ctas(M * ((F + BLOCK - 1) / BLOCK * 4));
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
-    const cudaError_t e = z == GEMM_F32 ? gate_launch<float>(a, n, p, stream)
-                                        : gate_launch<__nv_bfloat16>(a, n, p, stream);
-    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    GateParams p{Z, A, SFA, CK, SFCK, Units{}, (int)F};
+    // whole blocks of two units per row, so that no block straddles the lanes of two rows
+    return over_rows(M, (int)((F + BLOCK - 1) / BLOCK * 2), [&](const Units &units, unsigned n) {
+        p.units = units;
+        return z == GEMM_F32 ? gate_launch<float>(a, n, p, stream) : gate_launch<__nv_bfloat16>(a, n, p, stream);
+    });
 }
 
 extern "C" gemm_status gemm_gate_backward(int64_t M, int64_t F, gemm_dtype da, gemm_dtype dz, gemm_dtype a,
                                           const void *DA, const uint8_t *CK, const uint8_t *SFCK, void *DZ, void *A,
                                           void *cuda_stream) {
     gemm_status st = check_sizes(M, F);
-    if (st == GEMM_ERR_INVALID_ARG || st == GEMM_ERR_UNSUPPORTED) return st;
+    if (st == GEMM_ERR_INVALID_ARG) return st;
     if (!real(da) || !real(dz) || (A && a != GEMM_BF16 && a != GEMM_F16)) return GEMM_ERR_UNSUPPORTED;
     if (st != GEMM_OK || M == 0) return st;
     if (!DA || !CK || !SFCK || !DZ) return GEMM_ERR_INVALID_ARG;
@@ -170,14 +159,14 @@ extern "C" gemm_status gemm_gate_backward(int64_t M, int64_t F, gemm_dtype da, g
     int sms = 0;
     st = rows::device_sms(&sms);
     if (st != GEMM_OK) return st;
-    const GateBackParams p{DA, CK, SFCK, DZ, A, M, (int)F};
-    const unsigned n = ctas(M * (F / UNIT));
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
-    cudaError_t e;
-    if (da == GEMM_F32)
-        e = dz == GEMM_F32 ? back_launch<float, float>(a, n, p, stream) : back_launch<float, __nv_bfloat16>(a, n, p, stream);
-    else
-        e = dz == GEMM_F32 ? back_launch<__nv_bfloat16, float>(a, n, p, stream)
-                           : back_launch<__nv_bfloat16, __nv_bfloat16>(a, n, p, stream);
-    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    GateBackParams p{DA, CK, SFCK, DZ, A, Units{}, (int)F};
+    return over_rows(M, (int)(F / 8), [&](const Units &units, unsigned n) {
+        p.units = units;
+        if (da == GEMM_F32)
+            return dz == GEMM_F32 ? back_launch<float, float>(a, n, p, stream)
+                                  : back_launch<float, __nv_bfloat16>(a, n, p, stream);
+        return dz == GEMM_F32 ? back_launch<__nv_bfloat16, float>(a, n, p, stream)
+                              : back_launch<__nv_bfloat16, __nv_bfloat16>(a, n, p, stream);
+    });
 }

@@ -1,9 +1,7 @@
-// Shared pieces of the row operators (gemm_norm.cu, gemm_gate.cu): eight-element vectors in every
-// element type, the e4m3 block scale rule, and the per-device facts their launches need.
+// Shared pieces of the row operators (gemm_norm.cu, gemm_gate.cu): vectors of consecutive elements in every element
+// type, the e4m3 block scale rule, the row and unit a thread of many rows takes, and the per-device facts of a launch.
 //
-// A "unit" is eight consecutive elements of a row: 16 bytes of a 16-bit type (one 128-bit access per
-// thread, consecutive threads on consecutive units), 32 bytes of fp32, 8 bytes of e4m3.  A scale
-// block (32 elements) is four units, held by four consecutive lanes of a warp.
+// A thread works on units of N consecutive elements of a row, N = 8 or 16.
 #pragma once
 
 #include <cstdint>
@@ -16,24 +14,40 @@
 namespace gb300 {
 namespace rows {
 
-constexpr int UNIT = 8;           // elements per unit
 constexpr int BLOCK = 32;         // elements per scale
 
 // ------------------------------------------------------------------ elements
 
-__device__ __forceinline__ void load_unit(const float *p, float (&v)[UNIT]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// 16-byte pieces of N elements
+template <typename T, int N>
+constexpr int PIECES = sizeof(T) * N / 16;
+
+template <int P>
+__device__ __forceinline__ void load_pieces(const void *p, bool on, uint4 (&q)[P]) {       // zeros where not `on`
+#pragma unroll
+    for (int i = 0; i < P; ++i) q[i] = on ? static_cast<const uint4 *>(p)[i] : make_uint4(0, 0, 0, 0);
 }
 
-__device__ __forceinline__ void load_unit(const __nv_bfloat16 *p, float (&v)[UNIT]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+template <int N>
+__device__ __forceinline__ void unpack(const float *, const uint4 *q, float (&v)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < N / 4; ++i) {
+        v[4 * i] = __uint_as_float(q[i].x);
+        v[4 * i + 1] = __uint_as_float(q[i].y);
+        v[4 * i + 2] = __uint_as_float(q[i].z);
+        v[4 * i + 3] = __uint_as_float(q[i].w);
+    }
+}
+template <int N>
+__device__ __forceinline__ void unpack(const __nv_bfloat16 *, const uint4 *q, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+            v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
     }
 }
 
@@ -45,21 +59,48 @@ __device__ __forceinline__ uint32_t pack2(const __half *, float lo, float hi) {
     const __half2 p = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
-
-__device__ __forceinline__ void store_unit(float *p, const float (&v)[UNIT]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
 template <typename T16>
-__device__ __forceinline__ void store_unit(T16 *p, const float (&v)[UNIT]) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(p, v[0], v[1]), pack2(p, v[2], v[3]), pack2(p, v[4], v[5]),
-                                               pack2(p, v[6], v[7]));
+__device__ __forceinline__ uint4 pack8(const T16 *t, const float *v) {
+    return make_uint4(pack2(t, v[0], v[1]), pack2(t, v[2], v[3]), pack2(t, v[4], v[5]), pack2(t, v[6], v[7]));
 }
 
-// v rounded to the type's values, in fp32
-__device__ __forceinline__ float round_as(const float *, float v) { return v; }
-__device__ __forceinline__ float round_as(const __nv_bfloat16 *, float v) {
-    return __bfloat162float(__float2bfloat16_rn(v));
+template <int N>
+__device__ __forceinline__ void load(const float *p, float (&v)[N]) {
+    uint4 q[N / 4];
+    load_pieces(p, true, q);
+    unpack(p, q, v);
+}
+template <int N>
+__device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&v)[N]) {
+    uint4 q[N / 8];
+    load_pieces(p, true, q);
+    unpack(p, q, v);
+}
+template <int N>
+__device__ __forceinline__ void store(float *p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+template <typename T16, int N>
+__device__ __forceinline__ void store(T16 *p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) reinterpret_cast<uint4 *>(p)[i] = pack8(p, v + 8 * i);
+}
+
+// v rounded to the type of p, stored there where `on`, and kept in fp32
+template <int N>
+__device__ __forceinline__ void round_store(float *p, bool on, float (&v)[N]) {
+    if (on) store(p, v);
+}
+template <int N>
+__device__ __forceinline__ void round_store(__nv_bfloat16 *p, bool on, float (&v)[N]) {
+    uint4 q[N / 8];
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+        q[i] = pack8(p, v + 8 * i);
+        if (on) reinterpret_cast<uint4 *>(p)[i] = q[i];
+    }
+    unpack(p, q, v);
 }
 
 // ------------------------------------------------------------- e4m3 with UE8M0
@@ -86,24 +127,31 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// Quantise a unit against its block (four consecutive lanes, all of them active; lanes past the row's
-// end pass zeros): returns the codes, and the block's scale code in every lane.
-__device__ __forceinline__ uint2 quantise_unit(const float (&v)[UNIT], uint32_t &code) {
+// Quantise 16 or 8 elements of a block (the rest is with the neighbouring one or three lanes; all of them are active, and
+// pass zeros past a row's end): stores the codes at p where `on`; returns the block's scale code.
+template <int N>
+__device__ __forceinline__ uint32_t quantise(const float (&v)[N], uint8_t *p, bool on) {
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < UNIT; ++i) amax = fmaxf(amax, fabsf(v[i]));     // fmaxf drops NaN
+    for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(v[i]));      // fmaxf drops NaN
     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    code = scale_code(amax);
+    if (N == 8) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    const uint32_t code = scale_code(amax);
     const float inv = scale_inverse(code);
-    uint32_t h[4];
+    uint32_t w[N / 4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
-    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    for (int i = 0; i < N / 4; ++i)
+        w[i] = e4m3x2(v[4 * i] * inv, v[4 * i + 1] * inv) | e4m3x2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+    if constexpr (N == 16) {
+        if (on) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        if (on) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+    return code;
 }
 
 // eight e4m3 codes times a scale
-__device__ __forceinline__ void decode_unit(uint2 q, float s, float (&v)[UNIT]) {
+__device__ __forceinline__ void decode(uint2 q, float s, float (&v)[8]) {
     const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -113,6 +161,39 @@ __device__ __forceinline__ void decode_unit(uint2 q, float s, float (&v)[UNIT]) 
         v[2 * i] = f.x * s;
         v[2 * i + 1] = f.y * s;
     }
+}
+
+// -------------------------------------------------------------- units of many rows
+
+// Which unit of which row thread i of a launch takes: i / per_row by a multiplication, exact for i < 2^31.
+struct Units {
+    int64_t row0;            // the launch's first row
+    int rows, per_row;
+    uint32_t inverse, shift; // ceil(2^(32 + shift) / per_row), shift = floor(log2(per_row - 1))
+
+    __device__ __forceinline__ bool place(uint32_t i, int64_t &row, int &u) const {
+        const uint32_t r = per_row == 1 ? i : __umulhi(i, inverse) >> shift;
+        row = row0 + r;
+        u = (int)(i - r * per_row);
+        return r < (uint32_t)rows;
+    }
+};
+
+// Launch over M rows of per_row units each, 256 threads per CTA: one launch, or more where the units number 2^31 or
+// over.  launch(units, ctas) returns its cudaError_t.
+template <typename F>
+gemm_status over_rows(int64_t M, int per_row, F launch) {
+    Units u{};
+    u.per_row = per_row;
+    while (((per_row - 1) >> (u.shift + 1)) != 0) ++u.shift;
+    if (per_row > 1) u.inverse = (uint32_t)((((uint64_t)1 << (32 + u.shift)) + per_row - 1) / per_row);
+    const int64_t most = ((int64_t)INT32_MAX - 255) / per_row;
+    for (; u.row0 < M; u.row0 += most) {
+        u.rows = (int)(M - u.row0 < most ? M - u.row0 : most);
+        const unsigned ctas = (unsigned)(((int64_t)u.rows * per_row + 255) / 256);
+        if (launch(u, ctas) != cudaSuccess) return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
 }
 
 // ------------------------------------------------------------------ host side
