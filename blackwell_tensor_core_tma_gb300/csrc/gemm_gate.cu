@@ -32,8 +32,9 @@ struct GateParams {
     int F;
 };
 
+// (64 registers: four CTAs per SM.  Three take 41.0 us instead of 38.2 at 4096 x 8192 to e4m3 with checkpoint, five spill: 46.7)
 template <typename ZT, typename AT>
-__global__ void __launch_bounds__(256) gate_kernel(const __grid_constant__ GateParams p) {
+__global__ void __launch_bounds__(256, 4) gate_kernel(const __grid_constant__ GateParams p) {
     constexpr int N = 16;
     const int blocks = (p.F + BLOCK - 1) / BLOCK;
     int64_t row;

@@ -37,6 +37,7 @@
 // A CTA (one per SM) is 16 warps: R tiles of 16 columns by S slices of K, and `c` CTAs of a cluster split K
 // further; the partial sums are joined in a fixed order through shared memory, the cluster's through
 // distributed shared memory.
+#include <atomic>
 #include <initializer_list>
 #include <mutex>
 #include <type_traits>
@@ -670,7 +671,7 @@ struct MatvecShape {
     int slices, cluster, x_stride, held, smem, grid;
 };
 // resident[c]: clusters of c CTAs that run at once
-MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, const int *resident) {
+MatvecShape search_shape(int M, int N, int K, bool scaled_x, int slot, const int *resident) {
     const int chunks = (K + CHUNK - 1) / CHUNK, tiles = (N + 15) / 16, form = form_of(M);
     const int ring = WARPS * AHEAD * slot, part = WARPS * 16 * form * 4;
     MatvecShape best{};
@@ -702,6 +703,24 @@ MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, const int
     return best;
 }
 
+// The search is a microsecond of the caller's time: each thread keeps the last few sizes' results.
+MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, const int *resident) {
+    struct Known {
+        int M, N, K, scaled_x, slot;
+        const int *resident;
+        MatvecShape shape;
+    };
+    constexpr int KNOWN = 8;
+    static thread_local Known known[KNOWN];
+    static thread_local int next;
+    for (const Known &k : known)
+        if (k.M == M && k.N == N && k.K == K && k.scaled_x == scaled_x && k.slot == slot && k.resident == resident) return k.shape;
+    known[next] = Known{M, N, K, scaled_x, slot, resident, search_shape(M, N, K, scaled_x, slot, resident)};
+    const MatvecShape s = known[next].shape;
+    next = (next + 1) % KNOWN;
+    return s;
+}
+
 void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, int grid, int cluster, int smem, cudaStream_t stream) {
     cfg = cudaLaunchConfig_t{};
     cfg.gridDim = dim3((unsigned)grid);
@@ -713,25 +732,21 @@ void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, int grid
     attr.val.clusterDim.x = (unsigned)cluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
 }
 
 constexpr int MAX_DEVICES = 64;
 
 template <typename XT, int MODE, int FORM, bool ALIGNED>
 cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t stream) {
-    static std::mutex mu;
-    static bool ready[MAX_DEVICES];
+    static std::atomic<bool> ready[MAX_DEVICES];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!ready[dev]) {
-            e = cudaFuncSetAttribute(matvec_kernel<XT, MODE, FORM, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SMEM);
-            if (e != cudaSuccess) return e;
-            ready[dev] = true;
-        }
+    if (!ready[dev].load(std::memory_order_acquire)) {               // (setting it twice does no harm)
+        e = cudaFuncSetAttribute(matvec_kernel<XT, MODE, FORM, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SMEM);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
@@ -756,6 +771,7 @@ cudaError_t resident_clusters(const int **out) {
             cudaLaunchConfig_t cfg;
             cudaLaunchAttribute attr;
             cluster_config(cfg, attr, c, c, MOST_SMEM, nullptr);
+            cfg.numAttrs = 1;
             e = cudaOccupancyMaxActiveClusters(&found[c], kernel, &cfg);
         }
         if (e != cudaSuccess) return e;

@@ -144,19 +144,19 @@ def lib():
 def _ptr(x):
     if x is None:
         return None
+    try:                                           # first what every call passes: a torch tensor
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if hasattr(x, "ctypes"):                       # numpy array (host buffers)
         return x.ctypes.data
     raise TypeError(f"cannot pass {type(x)} as a pointer")
 
 
 def _stream(s):
-    if s is None:
-        return None
-    if isinstance(s, int):
+    if s is None or isinstance(s, int):
         return s
     return s.cuda_stream
 
@@ -285,43 +285,48 @@ def gemm_run_noalloc(M: int, N: int, K: int, ab, d, A, B, C, D, stream=None, wai
 
 def gemm_norm_run(M: int, K: int, x, h, y, eps: float, X, R, W, H, Y, SFY=None, RSTD=None, stream=None) -> int:
     """h = x + r, y = h * rstd * w: Y (and SFY for e4m3), optionally H and RSTD."""
-    st = lib().gemm_norm_run(M, K, DTYPE.get(x, x), DTYPE.get(h, h), DTYPE.get(y, y), eps, _ptr(X), _ptr(R), _ptr(W),
+    st = (_lib or lib()).gemm_norm_run(M, K, DTYPE.get(x, x), DTYPE.get(h, h), DTYPE.get(y, y), eps, _ptr(X), _ptr(R), _ptr(W),
                              _ptr(H), _ptr(Y), _ptr(SFY), _ptr(RSTD), _stream(stream))
-    _check(st, "gemm_norm_run")
+    if st:
+        raise GemmError(st, "gemm_norm_run")
     return st
 
 
 def gemm_norm_backward(M: int, K: int, dy, h, y, DY, DH, H, RSTD, W, DX, DW=None, Y=None, workspace=None,
                        workspace_bytes: int = 0, stream=None) -> int:
     """Gradients of gemm_norm_run: DX, optionally DW (with a workspace) and the 16-bit operand Y again."""
-    st = lib().gemm_norm_backward(M, K, DTYPE.get(dy, dy), DTYPE.get(h, h), DTYPE.get(y, y), _ptr(DY), _ptr(DH), _ptr(H),
+    st = (_lib or lib()).gemm_norm_backward(M, K, DTYPE.get(dy, dy), DTYPE.get(h, h), DTYPE.get(y, y), _ptr(DY), _ptr(DH), _ptr(H),
                                   _ptr(RSTD), _ptr(W), _ptr(DX), _ptr(DW), _ptr(Y), _ptr(workspace), workspace_bytes,
                                   _stream(stream))
-    _check(st, "gemm_norm_backward")
+    if st:
+        raise GemmError(st, "gemm_norm_backward")
     return st
 
 
 def gemm_gate_run(M: int, F: int, z, a, Z, A, SFA=None, CK=None, SFCK=None, stream=None) -> int:
     """a = silu(g) * u of Z = [g | u]: A (and SFA for e4m3), optionally the 8-bit checkpoint CK, SFCK."""
-    st = lib().gemm_gate_run(M, F, DTYPE.get(z, z), DTYPE.get(a, a), _ptr(Z), _ptr(A), _ptr(SFA), _ptr(CK), _ptr(SFCK),
+    st = (_lib or lib()).gemm_gate_run(M, F, DTYPE.get(z, z), DTYPE.get(a, a), _ptr(Z), _ptr(A), _ptr(SFA), _ptr(CK), _ptr(SFCK),
                              _stream(stream))
-    _check(st, "gemm_gate_run")
+    if st:
+        raise GemmError(st, "gemm_gate_run")
     return st
 
 
 def gemm_gate_backward(M: int, F: int, da, dz, a, DA, CK, SFCK, DZ, A=None, stream=None) -> int:
     """Gradient of the gated unit from its 8-bit checkpoint: DZ, optionally the 16-bit operand A again."""
-    st = lib().gemm_gate_backward(M, F, DTYPE.get(da, da), DTYPE.get(dz, dz), DTYPE.get(a, a), _ptr(DA), _ptr(CK),
+    st = (_lib or lib()).gemm_gate_backward(M, F, DTYPE.get(da, da), DTYPE.get(dz, dz), DTYPE.get(a, a), _ptr(DA), _ptr(CK),
                                   _ptr(SFCK), _ptr(DZ), _ptr(A), _stream(stream))
-    _check(st, "gemm_gate_backward")
+    if st:
+        raise GemmError(st, "gemm_gate_backward")
     return st
 
 
 def gemm_matvec_run(M: int, N: int, K: int, x, d, block_scaled: int, X, B, SFB, C, D, stream=None) -> int:
     """D = X·B + C for 1 to 16 rows of 16-bit X and an e2m1 plan's B and SFB."""
-    st = lib().gemm_matvec_run(M, N, K, DTYPE.get(x, x), DTYPE.get(d, d), int(block_scaled), _ptr(X), _ptr(B), _ptr(SFB),
+    st = (_lib or lib()).gemm_matvec_run(M, N, K, DTYPE.get(x, x), DTYPE.get(d, d), int(block_scaled), _ptr(X), _ptr(B), _ptr(SFB),
                                _ptr(C), _ptr(D), _stream(stream))
-    _check(st, "gemm_matvec_run")
+    if st:
+        raise GemmError(st, "gemm_matvec_run")
     return st
 
 
