@@ -79,13 +79,15 @@ struct MatvecParams {
     const float *c;
     void *d;
     int M, N, K;
-    uint32_t inverse_m;  // ceil(2^16 / M)
+    uint32_t inverse_m;  // ceil(2^16 / M), and of the rows of X in shared memory
+    uint32_t inverse_x;
     int out_bf16;
     int slices;          // slices of K per CTA (S)
     int x_stride;        // bytes of shared memory per row of X
     int held;            // tiles of a warp whose sums are kept before they are joined
 };
 
+uint32_t inverse16(int d) { return (65536u + (uint32_t)d - 1) / (uint32_t)d; }
 // i / M for i < 4096, M <= 16
 __device__ __forceinline__ int over_m(int i, uint32_t inverse_m) { return (int)((uint32_t)i * inverse_m >> 16); }
 
@@ -252,6 +254,9 @@ __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int 
     return out;
 }
 
+// Rows of X in shared memory: forms 8 and 16 have zeros where X has no row
+__host__ __device__ constexpr int x_rows(int form, int M) { return form > 4 ? form : M; }
+
 // The CTA's chunks [lo, hi) of X into shared memory as the MMA's B operand: row by row, k ascending; lane (g, t) reads
 // the eight k of 32 i + 8 t as one 128-bit word.  A row's stride is 64 bytes past a multiple of 128, so that
 // two rows' words come from different banks.  bf16: scaled per (row,
@@ -260,18 +265,18 @@ __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int 
 template <typename XT>
 __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int rows_x, float unbias, uint8_t *xf, float *scale) {
     constexpr int BATCH = 4;             // loads in flight per lane
-    const int lane = threadIdx.x & 31, all = (hi - lo) * p.M;
+    const int lane = threadIdx.x & 31, rows = x_rows(rows_x, p.M), all = (hi - lo) * rows;
     for (int first = threadIdx.x >> 5; first < all; first += WARPS * BATCH) {
         uint4 in[BATCH];
 #pragma unroll
         for (int j = 0; j < BATCH; ++j) {
-            const int i = first + j * WARPS, lc = over_m(i, p.inverse_m), m = i - lc * p.M, k = (lo + lc) * CHUNK + lane * 8;
+            const int i = first + j * WARPS, lc = over_m(i, p.inverse_x), m = i - lc * rows, k = (lo + lc) * CHUNK + lane * 8;
             in[j] = make_uint4(0, 0, 0, 0);
-            if (i < all && k < p.K) in[j] = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + (int64_t)m * p.K + k);
+            if (i < all && m < p.M && k < p.K) in[j] = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + (int64_t)m * p.K + k);
         }
 #pragma unroll
         for (int j = 0; j < BATCH; ++j) {
-        const int i = first + j * WARPS, lc = over_m(i, p.inverse_m), m = i - lc * p.M;
+        const int i = first + j * WARPS, lc = over_m(i, p.inverse_x), m = i - lc * rows;
         if (i >= all) break;
         uint4 v = in[j];
         if constexpr (!std::is_same<XT, __half>::value) {
@@ -318,7 +323,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     uint8_t *rings = reinterpret_cast<uint8_t *>(smem);
     float *parts = reinterpret_cast<float *>(rings + WARPS * AHEAD * SLOT<MODE, ALIGNED>);
     uint8_t *xf = reinterpret_cast<uint8_t *>(parts + p.held * WARPS * PART);
-    float *xscale = reinterpret_cast<float *>(xf + p.M * p.x_stride);
+    float *xscale = reinterpret_cast<float *>(xf + x_rows(FORM, p.M) * p.x_stride);
 
     uint32_t cluster;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int m = FEW ? g / 2 % FORM : nt * 8 + g;
-        x_on[nt] = m < p.M && (!FEW || MODE == GEMM_SCALE_UE8M0_32 || (g & 1) == t / 2);
+        x_on[nt] = !FEW || (m < p.M && (MODE == GEMM_SCALE_UE8M0_32 || (g & 1) == t / 2));
         x_lane[nt] = smem_addr(xf + (x_on[nt] ? m : 0) * p.x_stride + t * 16);
     }
     if (FEW) x_turn = MODE == GEMM_SCALE_UE8M0_32 ? g / 2 / FORM * 2 + (g & 1) : g / 2 / FORM;
@@ -547,7 +552,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     uint4 &b = x[i % SPREAD * NT + nt];
-                    load_shared4_if(x_on[nt] && (!FEW || x_turn == i % SPREAD), b, x_lane[nt] + lc * (CHUNK * 2) + i * 64);
+                    const uint32_t at = x_lane[nt] + lc * (CHUNK * 2) + i * 64;
+                    if constexpr (FEW) load_shared4_if(x_on[nt] && x_turn == i % SPREAD, b, at);
+                    else b = load_shared4(at);
                     if constexpr (MODE == GEMM_SCALE_UE4M3_16 && !FEW) {
                         mma_16816(sum[nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
                         mma_16816(sum[nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
@@ -683,7 +690,7 @@ MatvecShape search_shape(int M, int N, int K, bool scaled_x, int slot, const int
             s.slices = S;
             const int room = (chunks + c - 1) / c;
             s.x_stride = room * CHUNK * 2 + 64;
-            const int base = ring + M * s.x_stride + (scaled_x ? room * form * 4 : 0);
+            const int base = ring + x_rows(form, M) * s.x_stride + (scaled_x ? room * form * 4 : 0);
             if (base + part > MOST_SMEM || resident[c] == 0) continue;
             const int R = WARPS / S, groups = (tiles + R - 1) / R, clusters = groups < resident[c] ? groups : resident[c];
             const int turns = (groups + clusters - 1) / clusters, fit = (MOST_SMEM - base) / part;
@@ -846,7 +853,8 @@ extern "C" gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dty
                              rows,
                              (int)N,
                              (int)K,
-                             (65536u + (uint32_t)rows - 1) / (uint32_t)rows,
+                             inverse16(rows),
+                             inverse16(x_rows(form_of(rows), rows)),
                              d == GEMM_BF16,
                              s.slices,
                              s.x_stride,
