@@ -53,7 +53,9 @@ constexpr int64_t MAX_K = 32768;
 constexpr int WARPS = 16;
 constexpr int CHUNK = 256;           // k per step of a warp
 constexpr int BLOCKS = CHUNK / 32;   // 32-k blocks of a chunk: a column's 16-byte pieces
-constexpr int AHEAD = 3;      // ring slots per warp
+// Ring slots per warp, by the form (below).  Sixteen rows are bound by shared memory and issue, not by the requests in
+// flight, and their activations need the room: 16 x 8192 x 16384 (UE8M0) 31.5 us with two slots, 39.1 with three.
+__host__ __device__ constexpr int ahead_of(int form) { return form == 16 ? 2 : 3; }
 constexpr int MOST_CLUSTER = 8;
 constexpr int MOST_SMEM = 226 * 1024;
 constexpr int W_BYTES = 16 * CHUNK / 2;        // weights of a slot
@@ -261,10 +263,9 @@ __host__ __device__ constexpr int x_rows(int form, int M) { return form > 4 ? fo
 // the eight k of 32 i + 8 t as one 128-bit word.  A row's stride is 64 bytes past a multiple of 128, so that
 // two rows' words come from different banks.  bf16: scaled per (row,
 // chunk); scale[lc * rows_x + m] undoes it (times unbias), or is negative where the chunk of
-// some row does not convert exactly.
-template <typename XT>
+// some row does not convert exactly.  BATCH loads are in flight per lane.
+template <typename XT, int BATCH>
 __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int rows_x, float unbias, uint8_t *xf, float *scale) {
-    constexpr int BATCH = 4;             // loads in flight per lane
     const int lane = threadIdx.x & 31, rows = x_rows(rows_x, p.M), all = (hi - lo) * rows;
     for (int first = threadIdx.x >> 5; first < all; first += WARPS * BATCH) {
         uint4 in[BATCH];
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     // under codes below 160 still stays below 2^121
     constexpr uint32_t BIAS = MODE == GEMM_SCALE_UE8M0_32 ? 60 : 0;
     constexpr float UNBIAS = MODE == GEMM_SCALE_UE8M0_32 ? 0x1p-60f : 1.f;
-    constexpr int PART = 16 * FORM;
+    constexpr int PART = 16 * FORM, AHEAD = ahead_of(FORM);
     // each warp's ring; the sums to be joined [held][WARPS][16][FORM]; X; its scales
     extern __shared__ __align__(128) uint4 smem[];
     uint8_t *rings = reinterpret_cast<uint8_t *>(smem);
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     if (SCALED_X)
         for (int i = threadIdx.x; i < (hi - lo) * FORM; i += WARPS * 32) xscale[i] = 0.f;
     __syncthreads();
-    stage_x<XT>(p, lo, hi, FORM, UNBIAS, xf, xscale);
+    stage_x<XT, FORM == 16 ? 12 : FORM == 8 ? 8 : 4>(p, lo, hi, FORM, UNBIAS, xf, xscale);
     __syncthreads();
 
     // The lane's word of X in block 0 of the CTA's first chunk, and whether it has one (in which blocks of SPREAD).
@@ -680,7 +681,7 @@ struct MatvecShape {
 // resident[c]: clusters of c CTAs that run at once
 MatvecShape search_shape(int M, int N, int K, bool scaled_x, int slot, const int *resident) {
     const int chunks = (K + CHUNK - 1) / CHUNK, tiles = (N + 15) / 16, form = form_of(M);
-    const int ring = WARPS * AHEAD * slot, part = WARPS * 16 * form * 4;
+    const int ring = WARPS * ahead_of(form) * slot, part = WARPS * 16 * form * 4;
     MatvecShape best{};
     double best_cost = 0;
     for (int c = 1; c <= MOST_CLUSTER && c <= chunks; ++c)
