@@ -376,7 +376,8 @@ RowLaunch row_launch(int64_t M, const RowShape &s, int most, int stage, int sms)
     while (per_sm > 1 && RING_SMEM / per_sm < stage) --per_sm;
     const int fit = RING_SMEM / per_sm / stage;
     l.stages = fit < MAX_STAGES ? fit : MAX_STAGES;
-    l.ctas = (int)(groups < (int64_t)sms * per_sm ? groups : (int64_t)sms * per_sm);
+    const int64_t all = (int64_t)sms * per_sm < GEMM_NORM_PARTS ? sms * per_sm : GEMM_NORM_PARTS;
+    l.ctas = (int)(groups < all ? groups : all);
     if (groups <= l.ctas) l.stages = 0;      // one row each: straight to registers
     l.smem = l.stages * stage;
     return l;

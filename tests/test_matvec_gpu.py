@@ -61,6 +61,15 @@ def test_product(M, N, K, mode, x):
     check(run(M, N, K, x, d, mode, *t), d, t[0], t[1], t[2], mode, t[3])
 
 
+# more columns than run at once, K cut over warps and over clusters, activations past one pass
+@pytest.mark.parametrize("M,N,K,mode", [(1, 40000, 512, 2), (1, 6001, 16384, 1), (2, 30000, 1056, 1), (3, 9000, 8192, 2), (4, 20000, 4096, 1),
+                                        (5, 30000, 2080, 1), (8, 12000, 6144, 2), (8, 1500, 32768, 2), (16, 20000, 2048, 1),
+                                        (12, 6000, 8224, 2), (16, 700, 32768, 1), (9, 300, 32736, 2)])
+def test_many_columns(M, N, K, mode):
+    t = make(M, N, K, "bf16", mode, seed=M + N + K, c=True)
+    check(run(M, N, K, "bf16", "f32", mode, *t), "f32", t[0], t[1], t[2], mode, t[3])
+
+
 @pytest.mark.parametrize("M", range(1, 17))
 def test_every_row_count(M):
     for mode in (1, 2):

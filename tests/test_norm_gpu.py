@@ -77,6 +77,18 @@ def test_forward(M, K, x, h, y):
     ref.assert_operand("y", Y, SF, v, ref.NORM_REL, y)
 
 
+@pytest.mark.parametrize("M,K,x,h,y", [(800, 2064, "bf16", "bf16", "e4m3"), (500, 8208, "bf16", "bf16", "bf16"),
+                                       (400, 4096, "f32", "bf16", "e4m3"), (2000, 1040, "f32", "f32", "e4m3")])
+def test_forward_of_many_rows(M, K, x, h, y):
+    X, R, W = inputs(M, K, x, h, seed=K)
+    H, Y, SF, RS = run_forward(M, K, x, h, y, X, R, W)
+    want = rounded_sum(X, R, h)
+    assert torch.equal(H.cpu(), want)
+    v, rstd = ref.norm(want, W, EPS)
+    ref.assert_within("rstd", RS, rstd, ref.NORM_REL * rstd)
+    ref.assert_operand("y", Y, SF, v, ref.NORM_REL, y)
+
+
 def test_optional_outputs_and_in_place_residual():
     M, K = 11, 1008
     X, R, W = inputs(M, K, "bf16", "bf16", seed=4)
@@ -219,6 +231,18 @@ def check_backward(M, dy, h, y, got, DY, DH, H, RS, W):
 def test_backward(M, K, dy, h, y):
     t = back_inputs(M, K, dy, h, seed=M + 3 * K)
     check_backward(M, dy, h, y, run_backward(M, K, dy, h, y, *t), *t)
+
+
+# more rows than run at once: each CTA walks several, with the next ones on their way
+@pytest.mark.parametrize("M,K,dy,h", [(1000, 2064, "bf16", "bf16"), (700, 4112, "f32", "f32"), (600, 8192, "bf16", "bf16"),
+                                      (500, 8208, "f32", "bf16"), (330, 16400, "bf16", "f32"), (320, 16400, "bf16", "bf16"),
+                                      (310, 32768, "bf16", "bf16"), (305, 32768, "f32", "f32"), (5000, 112, "bf16", "bf16")])
+def test_backward_of_many_rows(M, K, dy, h):
+    t = back_inputs(M, K, dy, h, seed=M + K)
+    got = run_backward(M, K, dy, h, "bf16", *t)
+    check_backward(M, dy, h, "bf16", got, *t)
+    again = run_backward(M, K, dy, h, "bf16", *t, in_place=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
 def test_backward_optional_parts_and_repeatability():
