@@ -30,9 +30,9 @@
 // weight, and no lane decodes a code that another one decodes too.
 // Activations.  fp16 goes in as it is.  bf16 is multiplied per row and chunk by the power of two that brings
 // the largest magnitude to 2^15 .. 2^16, which is exact in fp16 for elements down to 2^-32 of it.
-// What these rules do not hold (activations too far apart within a chunk, outside 2^-50 .. 2^40, infinite or NaN in
-// bf16; UE8M0 scales from 2^33, NaN among them) takes products_fp32 for that chunk: the same sums in fp32
-// from the original values.
+// What these rules do not hold (bf16 activations too far apart within a chunk, outside 2^-50 .. 2^40, infinite or
+// NaN; UE8M0 scales from 2^33, NaN among them) takes products_64 for that chunk: the same sums in 64 bits from
+// the original values.
 //
 // A CTA (one per SM) is 16 warps: R tiles of 16 columns by S slices of K, and `c` CTAs of a cluster split K
 // further; the partial sums are joined in a fixed order through shared memory, the cluster's through
@@ -111,6 +111,12 @@ __device__ __forceinline__ uint32_t ue4m3x2(uint32_t codes) {
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&d);
+}
+// bytes of (a, b) by four-bit selectors, whose top bit takes the byte's sign instead (__byte_perm has no such bit)
+__device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t selector) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(selector));
+    return d;
 }
 __device__ __forceinline__ float2 halves(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 
@@ -207,37 +213,38 @@ __device__ __forceinline__ float2 pair_of(const __nv_bfloat16 *, uint32_t w) {
 }
 __device__ __forceinline__ float2 pair_of(const __half *, uint32_t w) { return halves(w); }
 
-// One chunk's products in fp32 from the original values, for eight rows of X from m0: what lane (g, t) adds to
-// its accumulators (columns n0 + g, n0 + g, n0 + g + 8, n0 + g + 8 by rows 2t, 2t + 1; with FEW row t in x and z).  The four lanes of a column
-// take every fourth 32-block.
+// One chunk's products in 64 bits from the original values, for eight rows of X from m0: what lane (g, t) adds to its
+// accumulators (columns n0 + g, n0 + g, n0 + g + 8, n0 + g + 8 by rows 2t, 2t + 1; with FEW row t in x and z).  The
+// four lanes of a column take every fourth 32-block.  64 bits hold every product of the formats' extremes (an activation
+// of 2^127 under a scale of 2^-120), and this is off the path of ordinary data.
 template <typename XT, int MODE, bool FEW>
-__device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int chunk, int m0) {
+__device__ __noinline__ float4 products_64(const MatvecParams &p, int n0, int chunk, int m0) {
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3, blocks = p.K / 32;
     float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int m = 0; m < 8; ++m) {
         if (m0 + m >= p.M) break;
-        float sum[2] = {0.f, 0.f};
+        const uint32_t *x = reinterpret_cast<const uint32_t *>(static_cast<const XT *>(p.x) + (int64_t)(m0 + m) * p.K);
+        double sum[2] = {0., 0.};
         for (int col = 0; col < 2; ++col) {
             const int n = n0 + g + 8 * col;
             for (int block = chunk * BLOCKS + t; n < p.N && block < min((chunk + 1) * BLOCKS, blocks); block += 4) {
-                const uint32_t *a = reinterpret_cast<const uint32_t *>(static_cast<const XT *>(p.x) + (int64_t)(m0 + m) * p.K) + block * 16;
                 const int64_t at = (int64_t)n * blocks + block;
                 const uint32_t *w = reinterpret_cast<const uint32_t *>(p.b + at * 16);
-                float part[2] = {0.f, 0.f};
+                double part[2] = {0., 0.};               // the block's halves
                 for (int i = 0; i < 4; ++i) {
                     uint32_t h[4];
                     e2m1x8(w[i], h);
                     for (int j = 0; j < 4; ++j) {
-                        const float2 v = halves(h[j]), xv = pair_of((const XT *)nullptr, a[4 * i + j]);
-                        part[i / 2] = fmaf(v.x, xv.x, fmaf(v.y, xv.y, part[i / 2]));
+                        const float2 v = halves(h[j]), xv = pair_of((const XT *)nullptr, x[block * 16 + 4 * i + j]);
+                        part[i / 2] += (double)v.x * xv.x + (double)v.y * xv.y;
                     }
                 }
                 if (MODE == GEMM_SCALE_UE8M0_32) {
-                    const uint32_t code = p.sfb[at];
-                    sum[col] += code == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(part[0] + part[1], (int)code - 127);
+                    const int code = p.sfb[at];
+                    sum[col] += code == 255 ? (double)__uint_as_float(0x7FC00000u) : ldexp(part[0] + part[1], code - 127);
                 } else {
                     const float2 s = halves(ue4m3x2(reinterpret_cast<const uint16_t *>(p.sfb)[at] & 0x7F7Fu));
-                    sum[col] += fmaf(part[0], s.x, part[1] * s.y);
+                    sum[col] += part[0] * s.x + part[1] * s.y;
                 }
             }
         }
@@ -245,12 +252,9 @@ __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int 
             sum[col] += __shfl_xor_sync(0xFFFFFFFFu, sum[col], 1);
             sum[col] += __shfl_xor_sync(0xFFFFFFFFu, sum[col], 2);
         }
-        if (FEW && m == t) {
-            out.x = sum[0];
-            out.z = sum[1];
-        } else if (!FEW && m / 2 == t) {
-            (m & 1 ? out.y : out.x) += sum[0];
-            (m & 1 ? out.w : out.z) += sum[1];
+        if (FEW ? m == t : m / 2 == t) {
+            (!FEW && m & 1 ? out.y : out.x) = (float)sum[0];
+            (!FEW && m & 1 ? out.w : out.z) = (float)sum[1];
         }
     }
     return out;
@@ -260,13 +264,12 @@ __device__ __noinline__ float4 products_fp32(const MatvecParams &p, int n0, int 
 __host__ __device__ constexpr int x_rows(int form, int M) { return form > 4 ? form : M; }
 
 // The CTA's chunks [lo, hi) of X into shared memory as the MMA's B operand: row by row, k ascending; lane (g, t) reads
-// the eight k of 32 i + 8 t as one 128-bit word.  A row's stride is 64 bytes past a multiple of 128, so that
-// two rows' words come from different banks.  bf16: scaled per (row,
-// chunk); scale[lc * rows_x + m] undoes it (times unbias), or is negative where the chunk of
-// some row does not convert exactly.  BATCH loads are in flight per lane.
+// the eight k of 32 i + 8 t as one 128-bit word.  A row's stride is 64 bytes past a multiple of 128, so that two rows'
+// words come from different banks.  bf16: scaled per (row, chunk); scale[lc * form + m] undoes it (times unbias), or
+// is negative where the row's chunk does not convert exactly.  BATCH loads are in flight per lane.
 template <typename XT, int BATCH>
-__device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int rows_x, float unbias, uint8_t *xf, float *scale) {
-    const int lane = threadIdx.x & 31, rows = x_rows(rows_x, p.M), all = (hi - lo) * rows;
+__device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int form, float unbias, uint8_t *xf, float *scale) {
+    const int lane = threadIdx.x & 31, rows = x_rows(form, p.M), all = (hi - lo) * rows;
     for (int first = threadIdx.x >> 5; first < all; first += WARPS * BATCH) {
         uint4 in[BATCH];
 #pragma unroll
@@ -277,32 +280,31 @@ __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, i
         }
 #pragma unroll
         for (int j = 0; j < BATCH; ++j) {
-        const int i = first + j * WARPS, lc = over_m(i, p.inverse_x), m = i - lc * rows;
-        if (i >= all) break;
-        uint4 v = in[j];
-        if constexpr (!std::is_same<XT, __half>::value) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                                    __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-            top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 16, top & 0xFFFFu));
-            const int e = top ? (int)(top >> 7) : 142;              // biased exponent; a chunk of zeros keeps scale 1
-            // magnitudes within 2^-50 .. 2^40: what underflows before the factor is applied is below 2^-100 after
-            bool fine = e >= 77 && e <= 167;
-            const float up = __uint_as_float((uint32_t)(142 - e + 127) << 23);
-            uint32_t h[4];
+            const int i = first + j * WARPS, lc = over_m(i, p.inverse_x), m = i - lc * rows;
+            if (i >= all) break;
+            if constexpr (!std::is_same<XT, __half>::value) {
+                const uint32_t w[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
+                uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                        __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+                top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 16, top & 0xFFFFu));
+                const int e = top ? (int)(top >> 7) : 142;              // biased exponent; a chunk of zeros keeps scale 1
+                // magnitudes within 2^-50 .. 2^40: what underflows before the factor is applied is below 2^-100 after
+                bool fine = e >= 77 && e <= 167;
+                const float up = __uint_as_float((uint32_t)(142 - e + 127) << 23);
+                uint32_t h[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 f = pair_of((const XT *)nullptr, w[q]);
-                const __half2 r = __floats2half2_rn(f.x * up, f.y * up);
-                const float2 back = __half22float2(r);
-                fine = fine && back.x == f.x * up && back.y == f.y * up;
-                h[q] = *reinterpret_cast<const uint32_t *>(&r);
+                for (int q = 0; q < 4; ++q) {
+                    const float2 f = pair_of((const XT *)nullptr, w[q]);
+                    const __half2 r = __floats2half2_rn(f.x * up, f.y * up);
+                    const float2 back = __half22float2(r);
+                    fine = fine && back.x == f.x * up && back.y == f.y * up;
+                    h[q] = *reinterpret_cast<const uint32_t *>(&r);
+                }
+                in[j] = make_uint4(h[0], h[1], h[2], h[3]);
+                const bool exact = __all_sync(0xFFFFFFFFu, fine);
+                if (lane == 0) scale[lc * form + m] = exact ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) * unbias : -1.f;
             }
-            v = make_uint4(h[0], h[1], h[2], h[3]);
-            const bool exact = __all_sync(0xFFFFFFFFu, fine);
-            if (lane == 0) scale[lc * rows_x + m] = exact ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) * unbias : -1.f;
-        }
-        *reinterpret_cast<uint4 *>(xf + m * p.x_stride + lc * CHUNK * 2 + lane * 16) = v;
+            *reinterpret_cast<uint4 *>(xf + m * p.x_stride + lc * CHUNK * 2 + lane * 16) = in[j];
         }
     }
 }
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             if ((SCALED_X || MODE == GEMM_SCALE_UE8M0_32) && !__all_sync(0xFFFFFFFFu, fine)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float4 add = products_fp32<XT, MODE, FEW>(p, n0, ch, nt * 8);
+                    const float4 add = products_64<XT, MODE, FEW>(p, n0, ch, nt * 8);
                     total[nt][0] += add.x;
                     total[nt][1] += add.y;
                     total[nt][2] += add.z;
@@ -533,6 +535,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                         mul[r][i] = ue4m3x2(twice);
                         mul[r][i + 1] = ue4m3x2(twice >> 16);
                     }
+            }
+            // UE8M0 with more than four rows: the codes plus BIAS, cut where a float's third and fourth byte meet
+            uint32_t high7[2][2], low1[2][2];
+            if constexpr (MODE == GEMM_SCALE_UE8M0_32 && !FEW) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t c = code[i / 2][i % 2] + BIAS * 0x01010101u;
+                    high7[i / 2][i % 2] = c >> 1 & 0x7F7F7F7Fu;
+                    low1[i / 2][i % 2] = c << 7 & 0x80808080u;
+                }
             }
             uint32_t q[4];               // words of (block i, columns g and g + 8), (block i + 1, the same)
             // sums that long chains of MMAs add to are kept twice, for every other MMA
@@ -572,13 +584,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                         float2 s;
                         if constexpr (MODE == GEMM_SCALE_UE4M3_16) {
                             s = halves(ue4m3x2(code[r][i / SPREAD] & 0x7F7Fu));
-                        } else {
+                        } else if constexpr (FEW) {
                             // 2^(code - 127 + BIAS)
-                            const uint32_t pair = FEW ? code[r][i / SPREAD] : code[r][i / 4];
-                            const int k = FEW ? 0 : i % 4;
-                            const uint32_t one = pair & 0xFFu << (8 * k), two = pair & 0xFF00u;
-                            s.x = __uint_as_float((k == 3 ? one >> 1 : one << (23 - 8 * k)) + (BIAS << 23));
-                            s.y = FEW ? __uint_as_float((two << 15) + (BIAS << 23)) : s.x;
+                            const uint32_t pair = code[r][i / SPREAD];
+                            s.x = __uint_as_float(((pair & 0xFFu) << 23) + (BIAS << 23));
+                            s.y = __uint_as_float(((pair & 0xFF00u) << 15) + (BIAS << 23));
+                        } else {
+                            // the same in one permutation: selector 8 takes a byte's top bit, which is 0 in high7
+                            const int k = i % 4;
+                            s.x = s.y = __uint_as_float(permute(high7[r][i / 4], low1[r][i / 4], k << 12 | (4 + k) << 8 | 0x88));
                         }
                         float2 v = make_float2(acc[0][nt][2 * r], acc[0][nt][2 * r + 1]);
                         if (CHAINS == 2) {

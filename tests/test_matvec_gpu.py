@@ -94,6 +94,15 @@ def test_wide_ranges(x):
     check(run(M, N, K, x, "f32", 1, X, B, SFB, None), "f32", X, B, SFB, 1, None)
 
 
+def test_huge_activations_under_tiny_scales():
+    """Products that pass fp32's ends on the way come out at their value."""
+    M, N, K = 2, 40, 320
+    X, B, SFB, _ = make(M, N, K, "bf16", 1, seed=9, low=5, high=12)
+    X = (X.float().sign() * 3e38).bfloat16()
+    X[1] = X[1] * 2.0 ** -60
+    check(run(M, N, K, "bf16", "f32", 1, X, B, SFB, None), "f32", X, B, SFB, 1, None)
+
+
 def test_outlier_under_a_zero_weight():
     """An activation 2^60 above the others whose weight is zero leaves the others' sum as it is."""
     M, N, K = 2, 32, 256
