@@ -50,7 +50,7 @@ namespace {
 
 constexpr int MAX_M = 16;
 constexpr int64_t MAX_K = 32768;
-constexpr int WARPS = 16;
+constexpr int LOG_WARPS = 4, WARPS = 1 << LOG_WARPS;
 constexpr int CHUNK = 256;           // k per step of a warp
 constexpr int BLOCKS = CHUNK / 32;   // 32-k blocks of a chunk: a column's 16-byte pieces
 // Ring slots per warp, by the form (below).  Sixteen rows are bound by shared memory and issue, not by the requests in
@@ -81,17 +81,22 @@ struct MatvecParams {
     const float *c;
     void *d;
     int M, N, K;
-    uint32_t inverse_m;  // ceil(2^16 / M), and of the rows of X in shared memory
-    uint32_t inverse_x;
+    uint32_t inverse_m, inverse_x, inverse_c;        // ceil(2^16 / d): of M, X's rows in shared memory, the cluster
+    uint32_t inverse_t;  // ceil(2^32 / (cluster * slices)), or 0 for 2^32
     int out_bf16;
-    int slices;          // slices of K per CTA (S)
+    int cluster, clusters;
+    int log_slices;      // slices of K per CTA: S = 2^log_slices
     int x_stride;        // bytes of shared memory per row of X
     int held;            // tiles of a warp whose sums are kept before they are joined
 };
 
+// Divisions by what a launch fixes, as multiplications: integer division would be a third of a small product's time.
 uint32_t inverse16(int d) { return (65536u + (uint32_t)d - 1) / (uint32_t)d; }
-// i / M for i < 4096, M <= 16
-__device__ __forceinline__ int over_m(int i, uint32_t inverse_m) { return (int)((uint32_t)i * inverse_m >> 16); }
+// i / d for i < 4096, d <= 16
+__device__ __forceinline__ int over(int i, uint32_t inverse) { return (int)((uint32_t)i * inverse >> 16); }
+// i / T for i < 2^24, T <= 128 (0 stands for T = 1)
+uint32_t inverse32(int T) { return (uint32_t)(((1ull << 32) + (uint32_t)T - 1) / (uint32_t)T); }
+__device__ __forceinline__ int over_t(int i, uint32_t inverse) { return inverse ? (int)__umulhi((uint32_t)i, inverse) : i; }
 
 // eight packed e2m1 values (k ascending from the low nibble) to four pairs of halves
 __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
@@ -272,17 +277,21 @@ __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, i
     const int lane = threadIdx.x & 31, rows = x_rows(form, p.M), all = (hi - lo) * rows;
     for (int first = threadIdx.x >> 5; first < all; first += WARPS * BATCH) {
         uint4 in[BATCH];
+        int lc[BATCH], m[BATCH];
 #pragma unroll
         for (int j = 0; j < BATCH; ++j) {
-            const int i = first + j * WARPS, lc = over_m(i, p.inverse_x), m = i - lc * rows, k = (lo + lc) * CHUNK + lane * 8;
+            const int i = first + j * WARPS;
+            lc[j] = over(i, p.inverse_x);
+            m[j] = i - lc[j] * rows;
+            const int k = (lo + lc[j]) * CHUNK + lane * 8;
             in[j] = make_uint4(0, 0, 0, 0);
-            if (i < all && m < p.M && k < p.K) in[j] = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + (int64_t)m * p.K + k);
+            if (i < all && m[j] < p.M && k < p.K)
+                in[j] = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + (int64_t)m[j] * p.K + k);
         }
+        // (no branch between the batch's members: their chains of reductions overlap)
+        if constexpr (!std::is_same<XT, __half>::value) {
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            const int i = first + j * WARPS, lc = over_m(i, p.inverse_x), m = i - lc * rows;
-            if (i >= all) break;
-            if constexpr (!std::is_same<XT, __half>::value) {
+            for (int j = 0; j < BATCH; ++j) {
                 const uint32_t w[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
                 uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
                                         __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
@@ -297,15 +306,19 @@ __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, i
                     const float2 f = pair_of((const XT *)nullptr, w[q]);
                     const __half2 r = __floats2half2_rn(f.x * up, f.y * up);
                     const float2 back = __half22float2(r);
-                    fine = fine && back.x == f.x * up && back.y == f.y * up;
+                    fine = fine & (back.x == f.x * up) & (back.y == f.y * up);
                     h[q] = *reinterpret_cast<const uint32_t *>(&r);
                 }
                 in[j] = make_uint4(h[0], h[1], h[2], h[3]);
                 const bool exact = __all_sync(0xFFFFFFFFu, fine);
-                if (lane == 0) scale[lc * form + m] = exact ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) * unbias : -1.f;
+                if (lane == 0 && first + j * WARPS < all)
+                    scale[lc[j] * form + m[j]] = exact ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) * unbias : -1.f;
             }
-            *reinterpret_cast<uint4 *>(xf + m * p.x_stride + lc * CHUNK * 2 + lane * 16) = in[j];
         }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+            if (first + j * WARPS < all)
+                *reinterpret_cast<uint4 *>(xf + m[j] * p.x_stride + lc[j] * CHUNK * 2 + lane * 16) = in[j];
     }
 }
 
@@ -328,17 +341,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     uint8_t *xf = reinterpret_cast<uint8_t *>(parts + p.held * WARPS * PART);
     float *xscale = reinterpret_cast<float *>(xf + x_rows(FORM, p.M) * p.x_stride);
 
-    uint32_t cluster;
-    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
-    const uint32_t rank = cluster_ctarank();
-    const int first_group = blockIdx.x / cluster, group_step = gridDim.x / cluster;
+    const int cluster = p.cluster, first_group = over(blockIdx.x, p.inverse_c), group_step = p.clusters;
+    const int rank = blockIdx.x - first_group * cluster;              // in the cluster
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int S = p.slices, R = WARPS / S, tl = warp / S, sl = warp - tl * S;
-    const int chunks = (p.K + CHUNK - 1) / CHUNK, T = (int)cluster * S;
-    const int lo = chunks * (int)(rank * S) / T, hi = chunks * (int)(rank * S + S) / T;
-    const int c0 = chunks * (int)(rank * S + sl) / T, c1 = chunks * (int)(rank * S + sl + 1) / T;
-    const int tiles = (p.N + 15) / 16, groups = (tiles + R - 1) / R;
+    const int S = 1 << p.log_slices, R = WARPS >> p.log_slices, tl = warp >> p.log_slices, sl = warp - (tl << p.log_slices);
+    const int chunks = (p.K + CHUNK - 1) / CHUNK, first_slice = rank << p.log_slices;
+    const int c0 = over_t(chunks * (first_slice + sl), p.inverse_t), c1 = over_t(chunks * (first_slice + sl + 1), p.inverse_t);
+    const int lo = over_t(chunks * first_slice, p.inverse_t), hi = over_t(chunks * (first_slice + S), p.inverse_t);
+    const int tiles = (p.N + 15) / 16, groups = (tiles + R - 1) >> (LOG_WARPS - p.log_slices);
     const int blocks = p.K / 32;                        // 32-k blocks of a column
     const int codes = blocks / BLOCKS * CODES<MODE> + blocks % BLOCKS * (CODES<MODE> / BLOCKS);       // of a column
     const uint32_t ring = smem_addr(rings) + warp * AHEAD * SLOT<MODE, ALIGNED>;
@@ -411,7 +422,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     if (SCALED_X)
         for (int i = threadIdx.x; i < (hi - lo) * FORM; i += WARPS * 32) xscale[i] = 0.f;
     __syncthreads();
-    stage_x<XT, FORM == 16 ? 12 : FORM == 8 ? 8 : 4>(p, lo, hi, FORM, UNBIAS, xf, xscale);
+    stage_x<XT, FORM == 16 ? 8 : FORM == 8 ? 4 : 2>(p, lo, hi, FORM, UNBIAS, xf, xscale);
     __syncthreads();
 
     // The lane's word of X in block 0 of the CTA's first chunk, and whether it has one (in which blocks of SPREAD).
@@ -635,7 +646,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
         __syncthreads();
         const int outputs = R * 16 * p.M;                // of a turn: n ascending, then row of X, then tile
         auto place = [&](int b, int i, int &m, int &n) { // output i of turn b: where it goes, and its first slice's sum
-            const int tile = over_m(i >> 4, p.inverse_m);
+            const int tile = over(i >> 4, p.inverse_m);
             m = (i >> 4) - tile * p.M;
             n = ((grp - (turn - 1 - b) * group_step) * R + tile) * 16 + (i & 15);
             return parts + (b * WARPS + tile * S) * PART + (i & 15) * FORM + m;
@@ -652,7 +663,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             cluster_sync();
         }
         for (int b = 0; b < turn; ++b)
-            for (int i = rank * WARPS * 32 + threadIdx.x; i < outputs; i += (int)cluster * WARPS * 32) {
+            for (int i = rank * WARPS * 32 + threadIdx.x; i < outputs; i += cluster * WARPS * 32) {
                 const float *first = place(b, i, m, n);
                 if (n >= p.N) continue;
                 const int64_t o = (int64_t)m * p.N + n;
@@ -663,10 +674,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                 } else {
                     float part[MOST_CLUSTER];
 #pragma unroll
-                    for (uint32_t r = 0; r < MOST_CLUSTER; ++r)
+                    for (int r = 0; r < MOST_CLUSTER; ++r)
                         part[r] = r < cluster ? load_cluster(mapa_shared(smem_addr(first), r)) : 0.f;
 #pragma unroll
-                    for (uint32_t r = 0; r < MOST_CLUSTER; ++r) v += part[r];
+                    for (int r = 0; r < MOST_CLUSTER; ++r) v += part[r];
                 }
                 v += c;
                 if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.d)[o] = __float2bfloat16_rn(v);
@@ -690,7 +701,7 @@ int slot_bytes(int mode, int K) {
 
 // How the product is cut (see the head of this file)
 struct MatvecShape {
-    int slices, cluster, x_stride, held, smem, grid;
+    int log_slices, cluster, x_stride, held, smem, grid;
 };
 // resident[c]: clusters of c CTAs that run at once
 MatvecShape search_shape(int M, int N, int K, bool scaled_x, int slot, const int *resident) {
@@ -699,10 +710,11 @@ MatvecShape search_shape(int M, int N, int K, bool scaled_x, int slot, const int
     MatvecShape best{};
     double best_cost = 0;
     for (int c = 1; c <= MOST_CLUSTER && c <= chunks; ++c)
-        for (int S = 1; S <= WARPS && S * c <= chunks; S *= 2) {
+        for (int log_s = 0; log_s <= LOG_WARPS && (c << log_s) <= chunks; ++log_s) {
+            const int S = 1 << log_s;
             MatvecShape s;
             s.cluster = c;
-            s.slices = S;
+            s.log_slices = log_s;
             const int room = (chunks + c - 1) / c;
             s.x_stride = room * CHUNK * 2 + 64;
             const int base = ring + x_rows(form, M) * s.x_stride + (scaled_x ? room * form * 4 : 0);
@@ -870,8 +882,12 @@ extern "C" gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dty
                              (int)K,
                              inverse16(rows),
                              inverse16(x_rows(form_of(rows), rows)),
+                             inverse16(s.cluster),
+                             s.cluster << s.log_slices == 1 ? 0u : inverse32(s.cluster << s.log_slices),
                              d == GEMM_BF16,
-                             s.slices,
+                             s.cluster,
+                             s.grid / s.cluster,
+                             s.log_slices,
                              s.x_stride,
                              s.held};
         cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
