@@ -268,14 +268,31 @@ __device__ __noinline__ float4 products_64(const MatvecParams &p, int n0, int ch
 // Rows of X in shared memory: forms 8 and 16 have zeros where X has no row
 __host__ __device__ constexpr int x_rows(int form, int M) { return form > 4 ? form : M; }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t min_s16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.s16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // The CTA's chunks [lo, hi) of X into shared memory as the MMA's B operand: row by row, k ascending; lane (g, t) reads
 // the eight k of 32 i + 8 t as one 128-bit word.  A row's stride is 64 bytes past a multiple of 128, so that two rows'
-// words come from different banks.  bf16: scaled per (row, chunk); scale[lc * form + m] undoes it (times unbias), or
-// is negative where the row's chunk does not convert exactly.  BATCH loads are in flight per lane.
-template <typename XT, int BATCH>
-__device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int form, float unbias, uint8_t *xf, float *scale) {
-    const int lane = threadIdx.x & 31, rows = x_rows(form, p.M), all = (hi - lo) * rows;
-    for (int first = threadIdx.x >> 5; first < all; first += WARPS * BATCH) {
+// words come from different banks.  BATCH loads are in flight per lane, and `then` runs behind the first of them.
+//
+// bf16: scaled per (row, chunk) by the power of two that takes the largest magnitude's exponent to 30, the top of
+// f16's normal numbers; scale[lc * form + m] undoes it (times unbias), or is negative where the row's chunk does not
+// convert exactly.  Two values are converted at once on their bits: the exponent less the largest's plus 30, three
+// places up.  That is exact for zeros and what is within 2^-29 of the largest.
+template <typename XT, int BATCH, typename Then>
+__device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, int form, float unbias, uint8_t *xf, float *scale,
+                                        Then then) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = x_rows(form, p.M), all = (hi - lo) * rows;
+#pragma unroll 1
+    for (int first = warp; first == warp || first < all; first += WARPS * BATCH) {
         uint4 in[BATCH];
         int lc[BATCH], m[BATCH];
 #pragma unroll
@@ -288,29 +305,28 @@ __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, i
             if (i < all && m[j] < p.M && k < p.K)
                 in[j] = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + (int64_t)m[j] * p.K + k);
         }
+        if (first == warp) then();
         // (no branch between the batch's members: their chains of reductions overlap)
         if constexpr (!std::is_same<XT, __half>::value) {
 #pragma unroll
             for (int j = 0; j < BATCH; ++j) {
-                const uint32_t w[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
-                uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                                        __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-                top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 16, top & 0xFFFFu));
-                const int e = top ? (int)(top >> 7) : 142;              // biased exponent; a chunk of zeros keeps scale 1
-                // magnitudes within 2^-50 .. 2^40: what underflows before the factor is applied is below 2^-100 after
-                bool fine = e >= 77 && e <= 167;
-                const float up = __uint_as_float((uint32_t)(142 - e + 127) << 23);
-                uint32_t h[4];
+                uint32_t w[4] = {in[j].x, in[j].y, in[j].z, in[j].w}, low = 0x7FFF7FFFu, high = 0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float2 f = pair_of((const XT *)nullptr, w[q]);
-                    const __half2 r = __floats2half2_rn(f.x * up, f.y * up);
-                    const float2 back = __half22float2(r);
-                    fine = fine & (back.x == f.x * up) & (back.y == f.y * up);
-                    h[q] = *reinterpret_cast<const uint32_t *>(&r);
+                    low = min_s16x2(low, (w[q] | 0x80008000u) - 0x00010001u);       // |x| - 1 - 2^15, of zeros 2^15 - 1
+                    high = max_u16x2(high, w[q] & 0x7FFF7FFFu);
                 }
-                in[j] = make_uint4(h[0], h[1], h[2], h[3]);
-                const bool exact = __all_sync(0xFFFFFFFFu, fine);
+                const int top = (int)__reduce_max_sync(0xFFFFFFFFu, max(high >> 16, high & 0xFFFFu));
+                const int least = min((int)low >> 16, (int)(int16_t)low) + 32769;
+                const int e = top ? top >> 7 : 142;              // biased exponent; a chunk of zeros keeps scale 1
+                const int base = (e - 30) << 7;
+                // magnitudes within 2^-50 .. 2^40: what underflows before the factor is applied is below 2^-100 after
+                const bool exact = __all_sync(0xFFFFFFFFu, least >= base + 128) && e >= 77 && e <= 167;
+                const uint32_t both = (uint32_t)base * 0x10001u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    w[q] = (w[q] & 0x80008000u) | (max_u16x2(w[q] & 0x7FFF7FFFu, both) - both) << 3;
+                in[j] = make_uint4(w[0], w[1], w[2], w[3]);
                 if (lane == 0 && first + j * WARPS < all)
                     scale[lc[j] * form + m[j]] = exact ? __uint_as_float((uint32_t)(e - 142 + 127) << 23) * unbias : -1.f;
             }
@@ -416,13 +432,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
         copies_commit();
     };
     enter_tile();
+    // X's first loads go out before the weights', which take longer
+    stage_x<XT, FORM == 16 ? 8 : FORM == 8 ? 4 : 2>(p, lo, hi, FORM, UNBIAS, xf, xscale, [&]() {
 #pragma unroll 1
-    for (int j = 0; j < AHEAD - 1; ++j) request();
-
-    if (SCALED_X)
-        for (int i = threadIdx.x; i < (hi - lo) * FORM; i += WARPS * 32) xscale[i] = 0.f;
-    __syncthreads();
-    stage_x<XT, FORM == 16 ? 8 : FORM == 8 ? 4 : 2>(p, lo, hi, FORM, UNBIAS, xf, xscale);
+        for (int j = 0; j < AHEAD - 1; ++j) request();
+    });
+    if (SCALED_X && FEW)
+        for (int i = threadIdx.x; i < (hi - lo) * FORM; i += WARPS * 32)
+            if (i % FORM >= p.M) xscale[i] = 0.f;
     __syncthreads();
 
     // The lane's word of X in block 0 of the CTA's first chunk, and whether it has one (in which blocks of SPREAD).
