@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "gemm_rows.cuh"
+#include "ptx.cuh"
 
 namespace gb300 {
 namespace rows {
@@ -147,13 +148,32 @@ __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_
     }
 }
 
-// Rows ahead come through a ring in shared memory by asynchronous copies.  Every thread copies the very units that it
-// reads, so the ring needs no barrier of its own.
+// Rows ahead come through a ring in shared memory by asynchronous copies.  Every thread (with fp32, every warp)
+// copies the very units that it reads, so the ring needs no barrier of its own.
 constexpr int MAX_STAGES = 4;
-// `part`: the lanes' pieces are 32 bytes apart, so half of each sector is another copy's: keep it in L1 for that
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool part) {
-    if (part) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+constexpr int BACK_THREADS = 512;        // w, dw, g and n are 64 registers of each with two units per thread
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Where a piece of a thread's unit lies, in 16-byte places.  Pairs (fp32) lie as in memory, so that a copy's lines stay
+// whole, but every other line has them swapped: the same piece of eight threads then comes from all the banks.
+template <int PIECES_>
+__device__ __forceinline__ int place_of(int thread, int piece) {
+    if (PIECES_ == 1) return thread;
+    const int at = thread * 2 + piece;
+    return at ^ (at >> 3 & 1);
+}
+// The copies of a warp's units (or of the part of it that has one row, a power of two of lanes): contiguous ones, lane
+// by lane.  Calls put(threads from the lane's own, piece).
+template <int PIECES_, typename Put>
+__device__ __forceinline__ void deal_copies(int tpr, Put put) {
+    if constexpr (PIECES_ == 1) {
+        put(0, 0);
+    } else {
+        const int lanes = min(tpr, 32), l = threadIdx.x & (lanes - 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) put((lanes * i + l) / 2 - l, l & 1);
+    }
 }
 __device__ __forceinline__ uint4 load_shared4(uint32_t addr) {
     uint4 v;
@@ -168,61 +188,110 @@ __device__ __forceinline__ void wait_stage(int stages) {         // all but the 
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-
 struct NormBackParams {
     const void *dy, *dh, *h;
     const float *rstd, *w;
     void *dx, *y;
-    float *parts;        // one row of K per CTA, or null when dw is not wanted
+    float *parts;        // one row of K per CTA (cluster), or null when dw is not wanted
     int64_t M;
     int K;
     float inverse_k;
-    int stages;          // rows of the ring (up to MAX_STAGES), or 0: a row does not fit, and is loaded where it is used
+    int stages;          // rows of the ring (up to MAX_STAGES), or 0: one row per CTA, loaded where it is used
+    int cluster, share;  // CTAs that a row is split over, and the units of each but the last
 };
 
-// A CTA walks rows (rpc at a time) with dw in registers; a row costs one barrier, that of its sum.
-template <typename GT, typename HT, typename YT, int U, int THREADS>
-__global__ void __launch_bounds__(THREADS, U == 1 ? 2 : 1) norm_back_kernel(const __grid_constant__ NormBackParams p) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Sum over a cluster's threads, the same in each and in a fixed order: every warp's sum goes to every CTA, as an
+// asynchronous store that counts on a barrier there.  (A barrier of the cluster would have the warp's stores to memory
+// wait too: 1.2 us.)  `red` holds a float per warp of the cluster.
+constexpr int MOST_SPLIT = 8, CLUSTER_WARPS = MOST_SPLIT * 16;
+constexpr int SUMS = 4;                      // rows whose sums have a place
+__device__ __forceinline__ void publish_sum(float v, float *red, uint64_t *bar, int cluster, int rank) {
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    if (lane < cluster)
+        asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                         mapa_shared(smem_addr(red + rank * warps + threadIdx.x / 32), lane)),
+                     "r"(__float_as_uint(v)), "r"(mapa_shared(smem_addr(bar), lane))
+                     : "memory");
+}
+// NaN, and with it the rest of the gradient, if the others' sums have not come after seconds
+constexpr int MOST_PROBES = 1 << 25;
+__device__ __forceinline__ float published_sum(const float *red, uint64_t *bar, uint32_t parity, int cluster, bool &lost) {
+    for (int i = 0; !lost && !mbar_try_wait_cluster(smem_addr(bar), parity); ++i) lost = i >= MOST_PROBES;
+    const int sums = cluster * (int)(blockDim.x / 32);
+    float v = 0.f;
+    for (int i = threadIdx.x & 31; i < sums; i += 32) v += red[i];
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return __any_sync(0xFFFFFFFFu, lost) ? __uint_as_float(0x7FC00000u) : v;
+}
+
+// A CTA walks rows (rpc at a time) with w and dw in registers; a row costs one barrier, that of its sum.  SPLIT: a row
+// is the work of a cluster, a share of its columns each.  Its sum then takes longer than a row's bytes should, so the
+// row before is finished meanwhile, for which dy and h are read from the ring once more.
+template <typename GT, typename HT, typename YT, int U, bool SPLIT>
+__global__ void __launch_bounds__(BACK_THREADS, U == 1 ? 2 : 1) norm_back_kernel(const __grid_constant__ NormBackParams p) {
     extern __shared__ uint4 ring[];                    // [stages][pieces of a unit: dy, h, dh][U][threads]
-    __shared__ float red[2][MAX_WARPS];
+    __shared__ float red[SPLIT ? SUMS : 2][SPLIT ? CLUSTER_WARPS : MAX_WARPS];
+    __shared__ uint64_t arrived[SUMS];                 // SPLIT: that a row's sums have
     constexpr int PG = PIECES<GT, UNIT>, PH = PIECES<HT, UNIT>, PER_UNIT = PG + 2 * PH;
-    constexpr bool KEEP = THREADS == 512;                      // g and n stay in registers over the sum; else they are read again
-    constexpr bool KEEP_W = U <= 2;
-    const int units = p.K / UNIT, tpr = blockDim.x, threads = tpr * blockDim.y, tid = threadIdx.y * tpr + threadIdx.x;
-    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + tid * 16;
+    const int group = SPLIT ? blockIdx.x / p.cluster : blockIdx.x, groups = SPLIT ? gridDim.x / p.cluster : gridDim.x;
+    const int rank = SPLIT ? blockIdx.x - group * p.cluster : 0, first = rank * p.share;       // the CTA's first unit
+    const int units = SPLIT ? min(p.share, p.K / UNIT - first) : p.K / UNIT;
+    const int tpr = blockDim.x, threads = tpr * blockDim.y, tid = threadIdx.y * tpr + threadIdx.x;
+    const uint32_t places = smem_addr(ring);
     const uint32_t unit_bytes = threads * 16, stage_bytes = PER_UNIT * U * unit_bytes;
 
-    const GT *dy = static_cast<const GT *>(p.dy);
-    const HT *h = static_cast<const HT *>(p.h), *dh = static_cast<const HT *>(p.dh);
+    const GT *dy = static_cast<const GT *>(p.dy) + first * UNIT;
+    const HT *h = static_cast<const HT *>(p.h) + first * UNIT;
+    const HT *dh = p.dh ? static_cast<const HT *>(p.dh) + first * UNIT : nullptr;
+    const float *weight = p.w + first * UNIT;
+    HT *dx = static_cast<HT *>(p.dx) + first * UNIT;
+    YT *again = p.y ? static_cast<YT *>(p.y) + first * UNIT : nullptr;
+    const uint32_t sums_bytes = p.cluster * (tpr / 32) * sizeof(float);
+    if (SPLIT) {                               // (the wait is before the loop: no CTA stores into one that has not begun)
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < SUMS; ++i) mbar_init(&arrived[i], 1);
+            fence_mbarrier_init();
+            for (int i = 0; i < SUMS; ++i) mbar_arrive_expect_tx(&arrived[i], sums_bytes);
+        }
+        __syncwarp();
+        cluster_arrive();
+    }
     auto request = [&](int64_t row, int slot) {
+        if (PG + PH > 2) __syncwarp();                 // a warp shares its copies: all of it has read what lay there
         if (row < p.M) {
+            const uint32_t stage = places + slot * stage_bytes;
+            auto copy = [&](auto *from, int first_piece, int j) {
+                constexpr int P = PIECES<std::remove_const_t<std::remove_pointer_t<decltype(from)>>, UNIT>;
+                deal_copies<P>(tpr, [&](int off, int piece) {
+                    const int u = threadIdx.x + off + j * tpr;
+                    if (u < units)
+                        copy16(stage + (first_piece * U + P * j) * unit_bytes + place_of<P>(tid + off, piece) * 16,
+                               from + row * p.K + u * UNIT + piece * 4);
+                });
+            };
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const int u = threadIdx.x + j * tpr;
-                if (u >= units) continue;
-                const int64_t at = row * p.K + u * UNIT;
-                const uint32_t to = mine + slot * stage_bytes + j * unit_bytes;
-#pragma unroll
-                for (int i = 0; i < PG; ++i) copy16(to + i * U * unit_bytes, dy + at + i * 4, PG > 1);
-#pragma unroll
-                for (int i = 0; i < PH; ++i) copy16(to + (PG + i) * U * unit_bytes, h + at + i * 4, PH > 1);
-                if (dh) {
-#pragma unroll
-                    for (int i = 0; i < PH; ++i) copy16(to + (PG + PH + i) * U * unit_bytes, dh + at + i * 4, PH > 1);
-                }
+                copy(dy, 0, j);
+                copy(h, PG, j);
+                if (dh) copy(dh, PG + PH, j);
             }
         }
         copies_commit();
     };
-    auto read = [&](auto *from, int64_t row, int slot, int j, int piece, float (&v)[UNIT]) {      // piece: of the ring
+    auto read = [&](auto *from, int64_t row, int slot, int j, int piece, float (&v)[UNIT]) {      // piece: the first of the ring's
         using T = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
-        if (p.stages == 0) {
+        if (!SPLIT && p.stages == 0) {
             load(from + row * p.K + (threadIdx.x + j * tpr) * UNIT, v);
             return;
         }
-        uint4 q[PIECES<T, UNIT>];
+        constexpr int P = PIECES<T, UNIT>;
+        uint4 q[P];
 #pragma unroll
-        for (int i = 0; i < PIECES<T, UNIT>; ++i) q[i] = load_shared4(mine + slot * stage_bytes + ((piece + i) * U + j) * unit_bytes);
+        for (int i = 0; i < P; ++i)
+            q[i] = load_shared4(places + slot * stage_bytes + (piece * U + P * j) * unit_bytes + place_of<P>(tid, i) * 16);
         unpack(from, q, v);
     };
     float dw[U][UNIT];
@@ -231,81 +300,120 @@ __global__ void __launch_bounds__(THREADS, U == 1 ? 2 : 1) norm_back_kernel(cons
 #pragma unroll
         for (int i = 0; i < UNIT; ++i) dw[j][i] = 0.f;
 
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    const int64_t own = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;      // this thread's first row
+    const int64_t step = (int64_t)groups * blockDim.y;
+    const int64_t own = (int64_t)group * blockDim.y + threadIdx.y;      // this thread's first row
     for (int s = 0; s < p.stages; ++s) request(own + s * step, s);
-    float w[KEEP_W ? U : 1][UNIT];
-    if (KEEP_W) {
+    float w[U][UNIT];
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (threadIdx.x + j * tpr < units) load(p.w + (threadIdx.x + j * tpr) * UNIT, w[j]);
-    }
+    for (int j = 0; j < U; ++j)
+        if (threadIdx.x + j * tpr < units) load(weight + (threadIdx.x + j * tpr) * UNIT, w[j]);
     float next_rstd = own < p.M ? p.rstd[own] : 0.f;     // a row ahead, so that no row waits for it
-    int turn = 0, slot = 0;
-    for (int64_t row = own; row - threadIdx.y < p.M; row += step, turn ^= 1) {
-        const bool live = row < p.M;
-        const float rstd = next_rstd;
-        next_rstd = row + step < p.M ? p.rstd[row + step] : 0.f;
-        if (p.stages) wait_stage(p.stages);
-        float g[KEEP ? U : 1][UNIT], n[KEEP ? U : 1][UNIT];
-        float sum = 0.f, sum2 = 0.f;
+    int slot = 0;
+    auto first_pass = [&](int64_t row, int j, float rstd, float (&g)[UNIT], float (&n)[UNIT], float (&sum)[2]) {
+        const int u = threadIdx.x + j * tpr;
+        read(dy, row, slot, j, 0, g);
+        read(h, row, slot, j, PG, n);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int u = threadIdx.x + j * tpr, k = KEEP ? j : 0, kw = KEEP_W ? j : 0;
-            if (live && u < units) {
-                read(dy, row, slot, j, 0, g[k]);
-                read(h, row, slot, j, PG, n[k]);
-                if (!KEEP_W) load(p.w + u * UNIT, w[kw]);
-#pragma unroll
-                for (int i = 0; i < UNIT; ++i) {
-                    n[k][i] *= rstd;
-                    dw[j][i] = fmaf(g[k][i], n[k][i], dw[j][i]);
-                    g[k][i] *= w[kw][i];
-                    (i & 1 ? sum2 : sum) = fmaf(g[k][i], n[k][i], i & 1 ? sum2 : sum);
-                }
-                if (p.y) {
-                    float y[UNIT];
-#pragma unroll
-                    for (int i = 0; i < UNIT; ++i) y[i] = n[k][i] * w[kw][i];
-                    store(static_cast<YT *>(p.y) + row * p.K + u * UNIT, y);
-                }
-            }
+        for (int i = 0; i < UNIT; ++i) {
+            n[i] *= rstd;
+            dw[j][i] = fmaf(g[i], n[i], dw[j][i]);
+            g[i] *= w[j][i];
+            sum[i & 1] = fmaf(g[i], n[i], sum[i & 1]);
         }
-        const float c = row_sum(sum + sum2, red[turn]) * p.inverse_k;
+        if (again) {
+            float y[UNIT];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int u = threadIdx.x + j * tpr, k = KEEP ? j : 0, kw = KEEP_W ? j : 0;
-            if (live && u < units) {
-                if (!KEEP) {
-                    read(dy, row, slot, j, 0, g[k]);
-                    read(h, row, slot, j, PG, n[k]);
-                    if (!KEEP_W) load(p.w + u * UNIT, w[kw]);
+            for (int i = 0; i < UNIT; ++i) y[i] = n[i] * w[j][i];
+            store(again + row * p.K + u * UNIT, y);
+        }
+    };
+    auto second_pass = [&](int64_t row, int at, int j, float rstd, float c, const float (&g)[UNIT], const float (&n)[UNIT]) {
+        float d[UNIT];
+        if (dh) {
+            read(dh, row, at, j, PG + PH, d);
+        } else {
+#pragma unroll
+            for (int i = 0; i < UNIT; ++i) d[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < UNIT; ++i) d[i] += rstd * (g[i] - n[i] * c);
+        store(dx + row * p.K + (threadIdx.x + j * tpr) * UNIT, d);
+    };
+    if constexpr (SPLIT) {
+        cluster_wait();
+        float rstd_before = 0.f;
+        int before = 0, place = 0, place_before = 0;                 // the slot of the row before, and its sums'
+        uint32_t parity = 0;
+        bool lost = false;
+        for (int64_t row = own; row - step < p.M; row += step) {
+            const float rstd = next_rstd;
+            next_rstd = row + step < p.M ? p.rstd[row + step] : 0.f;
+            if (row < p.M) {                                         // (the same in the whole cluster)
+                wait_stage(p.stages - 1);
+                if (PG + PH > 2) __syncwarp();
+                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    float g[UNIT], n[UNIT];
+                    if (threadIdx.x + j * tpr < units) first_pass(row, j, rstd, g, n, sum);
+                }
+                publish_sum(sum[0] + sum[1], red[place], &arrived[place], p.cluster, rank);
+            }
+            if (row != own) {
+                // A place is written again four rows on, for which its writer has every warp's sum of the second row on,
+                // sent behind this read.
+                const float c =
+                    published_sum(red[place_before], &arrived[place_before], parity, p.cluster, lost) * p.inverse_k;
+                if (threadIdx.x == 0) mbar_arrive_expect_tx(&arrived[place_before], sums_bytes);
+                if (place_before == SUMS - 1) parity ^= 1;
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    if (threadIdx.x + j * tpr >= units) continue;
+                    float g[UNIT], n[UNIT];
+                    read(dy, row - step, before, j, 0, g);
+                    read(h, row - step, before, j, PG, n);
 #pragma unroll
                     for (int i = 0; i < UNIT; ++i) {
-                        n[k][i] *= rstd;
-                        g[k][i] *= w[kw][i];
+                        n[i] *= rstd_before;
+                        g[i] *= w[j][i];
                     }
+                    second_pass(row - step, before, j, rstd_before, c, g, n);
                 }
-                float d[UNIT];
-                if (dh) {
-                    read(dh, row, slot, j, PG + PH, d);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < UNIT; ++i) d[i] = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < UNIT; ++i) d[i] += rstd * (g[k][i] - n[k][i] * c);
-                store(static_cast<HT *>(p.dx) + row * p.K + u * UNIT, d);
+                request(row + (p.stages - 1) * step, before);        // the thread itself has read what lay there
             }
+            rstd_before = rstd;
+            before = slot;
+            slot = slot + 1 == p.stages ? 0 : slot + 1;
+            place_before = place;
+            place = (place + 1) % SUMS;
         }
-        if (p.stages) request(row + p.stages * step, slot);          // the thread itself has read what lay there
-        slot = slot + 1 >= p.stages ? 0 : slot + 1;
+    } else {
+        int turn = 0;
+        for (int64_t row = own; row - threadIdx.y < p.M; row += step, turn ^= 1) {
+            const bool live = row < p.M;
+            const float rstd = next_rstd;
+            next_rstd = row + step < p.M ? p.rstd[row + step] : 0.f;
+            if (p.stages) {
+                wait_stage(p.stages);
+                if (PG + PH > 2) __syncwarp();
+            }
+            float g[U][UNIT], n[U][UNIT], sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (live && threadIdx.x + j * tpr < units) first_pass(row, j, rstd, g[j], n[j], sum);
+            const float c = row_sum(sum[0] + sum[1], red[turn]) * p.inverse_k;
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (live && threadIdx.x + j * tpr < units) second_pass(row, slot, j, rstd, c, g[j], n[j]);
+            if (p.stages) request(row + p.stages * step, slot);          // the thread itself has read what lay there
+            slot = slot + 1 >= p.stages ? 0 : slot + 1;
+        }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!p.parts) return;
 
     // the CTA's sums in a fixed order: rows of threads first, then (norm_dw_kernel) CTAs
-    float *part = p.parts + (int64_t)blockIdx.x * p.K;
+    float *part = p.parts + (int64_t)group * p.K + first * UNIT;
     if (blockDim.y == 1) {
 #pragma unroll
         for (int j = 0; j < U; ++j) {
@@ -367,18 +475,18 @@ constexpr int RING_SMEM = 220 * 1024;        // of an SM, for the CTAs that shar
 
 // A launch of persistent CTAs: at most `most` of them per SM, fewer where a row (stage bytes) would not fit otherwise
 struct RowLaunch {
-    int ctas, stages, smem;
+    int groups, stages, smem;                // groups: CTAs, or clusters of them
 };
-RowLaunch row_launch(int64_t M, const RowShape &s, int most, int stage, int sms) {
+RowLaunch row_launch(int64_t M, int rpc, int most, int stage, int resident, bool split) {
     RowLaunch l;
-    const int64_t groups = (M + s.rpc - 1) / s.rpc;
+    const int64_t groups = (M + rpc - 1) / rpc;
     int per_sm = most;
     while (per_sm > 1 && RING_SMEM / per_sm < stage) --per_sm;
     const int fit = RING_SMEM / per_sm / stage;
     l.stages = fit < MAX_STAGES ? fit : MAX_STAGES;
-    const int64_t all = (int64_t)sms * per_sm < GEMM_NORM_PARTS ? sms * per_sm : GEMM_NORM_PARTS;
-    l.ctas = (int)(groups < all ? groups : all);
-    if (groups <= l.ctas) l.stages = 0;      // one row each: straight to registers
+    const int64_t all = (int64_t)resident * per_sm < GEMM_NORM_PARTS ? resident * per_sm : GEMM_NORM_PARTS;
+    l.groups = (int)(groups < all ? groups : all);
+    if (groups <= l.groups && !split) l.stages = 0;      // one row each: straight to registers
     l.smem = l.stages * stage;
     return l;
 }
@@ -423,34 +531,110 @@ cudaError_t norm_launch(gemm_dtype h, gemm_dtype y, int sms, const NormParams &p
     return h == GEMM_F32 ? norm_launch<XT, float>(y, sms, p, stream) : norm_launch<XT, __nv_bfloat16>(y, sms, p, stream);
 }
 
-constexpr size_t back_unit(gemm_dtype dy, gemm_dtype h) { return (dy == GEMM_F32 ? 32 : 16) + 2 * (h == GEMM_F32 ? 32 : 16); }
-
-template <typename GT, typename HT, typename YT, int U, int THREADS>
-cudaError_t back_launch(const RowShape &s, const RowLaunch &l, NormBackParams p, cudaStream_t stream) {
-    const cudaError_t e = allow_smem<norm_back_kernel<GT, HT, YT, U, THREADS>>();
+cudaLaunchConfig_t back_config(int ctas, dim3 block, int smem, int cluster, cudaLaunchAttribute *attr, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = (unsigned)cluster;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cfg;
+}
+// How many clusters of `cluster` CTAs run at once, each CTA with an SM's shared memory to itself
+template <auto KERNEL>
+cudaError_t resident_clusters(int cluster, int *out) {
+    static std::mutex mu;
+    static int known[64][MOST_SPLIT + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    int &n = known[dev][cluster];
+    if (n == 0) {
+        cudaLaunchAttribute attr{};
+        const cudaLaunchConfig_t cfg = back_config(cluster, dim3(BACK_THREADS), RING_SMEM, cluster, &attr, nullptr);
+        e = cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg);
+        if (e == cudaSuccess && n <= 0) e = cudaErrorInvalidConfiguration;
+    }
+    *out = n;
+    return e;
+}
+
+// A unit of a row in the ring: dy, h, dh
+template <typename GT, typename HT>
+constexpr int UNIT_BYTES = (PIECES<GT, UNIT> + 2 * PIECES<HT, UNIT>) * 16;
+// How the rows are spread: over threads, and over a cluster's CTAs from `share` units on
+struct BackShape {
+    RowShape s;
+    int cluster, share;
+};
+// Few rows: as many threads as there are units.  Many: two units per thread with everything in registers, 512 threads
+// per SM and the ring as deep as fits (4096 x 8192, bf16: 57.2 us; with 64 registers, twice the threads and g and n
+// read again from the ring 67.6).
+// Rows of more than 8192 elements, and those of which an SM's shared memory does not hold three, are split over 2, 4 or
+// 8 CTAs.  2048 x 16384, bf16: 60.5 us with two CTAs per row; by one CTA with four units per thread, and w read again
+// for every row, 88.3.  4096 x 8192, all fp32: 96.9 us with two, 106.6 with one and a ring of two rows.
+constexpr int LINE = 16;                     // units of 256 bytes
+BackShape back_shape(int64_t M, int K, int sms, int unit_bytes) {
+    const int units = K / UNIT;
+    BackShape b;
+    b.cluster = 1;
+    while (units > b.cluster * 2 * BACK_THREADS) b.cluster *= 2;
+    for (;; b.cluster *= 2) {
+        if (b.cluster == 1) {
+            b.share = units;
+            b.s = row_shape(units, units <= (M <= 3 * sms ? BACK_THREADS : 128) ? 1 : 2);
+        } else {
+            b.share = (units + LINE * b.cluster - 1) / (LINE * b.cluster) * LINE;        // whole lines of memory
+            b.s = row_shape(b.share, 2);
+            b.s.rpc = 1;
+        }
+        if (b.s.u == 1 || b.s.tpr * b.s.rpc * 2 * unit_bytes * 3 <= RING_SMEM) return b;
+    }
+}
+
+// `parts`: how many rows of partial sums there are
+template <typename GT, typename HT, typename YT, int U, bool SPLIT>
+cudaError_t back_launch(const BackShape &b, NormBackParams p, float *dw, int sms, int *parts, cudaStream_t stream) {
+    constexpr auto KERNEL = norm_back_kernel<GT, HT, YT, U, SPLIT>;
+    cudaError_t e = allow_smem<KERNEL>();
+    int resident = sms;
+    if (e == cudaSuccess && SPLIT) e = resident_clusters<KERNEL>(b.cluster, &resident);
+    if (e != cudaSuccess) return e;
+    const int threads = b.s.tpr * b.s.rpc, most = SPLIT ? 1 : U == 1 ? 1024 / threads : BACK_THREADS / threads;
+    const RowLaunch l = row_launch(p.M, b.s.rpc, most < 1 ? 1 : most > 3 ? 3 : most, threads * U * UNIT_BYTES<GT, HT>,
+                                   resident, SPLIT);
     p.stages = l.stages;
-    const int joined = s.rpc > 1 ? s.rpc * p.K * (int)sizeof(float) : 0;
-    norm_back_kernel<GT, HT, YT, U, THREADS><<<l.ctas, dim3(s.tpr, s.rpc), l.smem > joined ? l.smem : joined, stream>>>(p);
-    return cudaGetLastError();
+    p.cluster = b.cluster;
+    p.share = b.share;
+    if (dw && l.groups == 1) p.parts = dw;               // a lone group's sums are dw itself
+    *parts = l.groups;
+    const int joined = b.s.rpc > 1 ? b.s.rpc * p.K * (int)sizeof(float) : 0;
+    cudaLaunchAttribute attr{};
+    const cudaLaunchConfig_t cfg = back_config(l.groups * b.cluster, dim3(b.s.tpr, b.s.rpc), l.smem > joined ? l.smem : joined,
+                                               b.cluster, &attr, stream);
+    return cudaLaunchKernelEx(&cfg, KERNEL, p);
 }
 template <typename GT, typename HT, typename YT>
-cudaError_t back_launch(const RowShape &s, const RowLaunch &l, const NormBackParams &p, cudaStream_t stream) {
-    if (s.u == 1) return back_launch<GT, HT, YT, 1, 512>(s, l, p, stream);
-    if (s.u == 2) return back_launch<GT, HT, YT, 2, 512>(s, l, p, stream);
-    if (s.tpr <= 512) return back_launch<GT, HT, YT, 4, 512>(s, l, p, stream);
-    return back_launch<GT, HT, YT, 4, 1024>(s, l, p, stream);
+cudaError_t back_launch(const NormBackParams &p, float *dw, int sms, int *parts, cudaStream_t stream) {
+    const BackShape b = back_shape(p.M, p.K, sms, UNIT_BYTES<GT, HT>);
+    if (b.cluster > 1) return back_launch<GT, HT, YT, 2, true>(b, p, dw, sms, parts, stream);
+    if (b.s.u == 1) return back_launch<GT, HT, YT, 1, false>(b, p, dw, sms, parts, stream);
+    return back_launch<GT, HT, YT, 2, false>(b, p, dw, sms, parts, stream);
 }
 template <typename GT, typename HT>
-cudaError_t back_launch(gemm_dtype y, const RowShape &s, const RowLaunch &l, const NormBackParams &p, cudaStream_t stream) {
-    return y == GEMM_F16 ? back_launch<GT, HT, __half>(s, l, p, stream)
-                         : back_launch<GT, HT, __nv_bfloat16>(s, l, p, stream);
+cudaError_t back_launch(gemm_dtype y, const NormBackParams &p, float *dw, int sms, int *parts, cudaStream_t stream) {
+    return y == GEMM_F16 ? back_launch<GT, HT, __half>(p, dw, sms, parts, stream)
+                         : back_launch<GT, HT, __nv_bfloat16>(p, dw, sms, parts, stream);
 }
 template <typename GT>
-cudaError_t back_launch(gemm_dtype h, gemm_dtype y, const RowShape &s, const RowLaunch &l, const NormBackParams &p,
-                        cudaStream_t stream) {
-    return h == GEMM_F32 ? back_launch<GT, float>(y, s, l, p, stream)
-                         : back_launch<GT, __nv_bfloat16>(y, s, l, p, stream);
+cudaError_t back_launch(gemm_dtype h, gemm_dtype y, const NormBackParams &p, float *dw, int sms, int *parts, cudaStream_t stream) {
+    return h == GEMM_F32 ? back_launch<GT, float>(y, p, dw, sms, parts, stream)
+                         : back_launch<GT, __nv_bfloat16>(y, p, dw, sms, parts, stream);
 }
 
 bool real(gemm_dtype t) { return t == GEMM_F32 || t == GEMM_BF16; }
@@ -507,23 +691,15 @@ extern "C" gemm_status gemm_norm_backward(int64_t M, int64_t K, gemm_dtype dy, g
     if (st != GEMM_OK) return st;
 
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
-    // Few rows: as many threads as there are units.  Many: two units per thread with everything in registers, 512
-    // threads per SM and the ring as deep as fits (4096 x 8192, bf16: 57.2 us; with 64 registers, twice the threads and
-    // g and n read again from the ring 67.6; 8192 x 4096: 49.6, one unit per thread 56.1).
-    const int units = (int)K / UNIT;
-    const RowShape s = row_shape(units, units <= (M <= 3 * sms ? 512 : 128) ? 1 : units <= 1024 ? 2 : 4);
-    const int threads = s.tpr * s.rpc, most = s.u == 1 ? 1024 / threads : 512 / threads;
-    const RowLaunch l = row_launch(M, s, most < 1 ? 1 : most > 3 ? 3 : most, threads * s.u * (int)back_unit(dy, h), sms);
-    const int ctas = l.ctas;
+    int parts = 0;
     if (M > 0) {
-        // a lone CTA's sums are dw itself
-        float *parts = !DW ? nullptr : ctas == 1 ? DW : static_cast<float *>(workspace);
-        const NormBackParams p{DY, DH, H, RSTD, W, DX, Y, parts, M, (int)K, 1.f / (float)K, 0};
-        const cudaError_t e = dy == GEMM_F32 ? back_launch<float>(h, y, s, l, p, stream)
-                                             : back_launch<__nv_bfloat16>(h, y, s, l, p, stream);
+        const NormBackParams p{DY, DH, H, RSTD, W, DX, Y, DW ? static_cast<float *>(workspace) : nullptr, M, (int)K,
+                               1.f / (float)K, 0, 1, 0};
+        const cudaError_t e = dy == GEMM_F32 ? back_launch<float>(h, y, p, DW, sms, &parts, stream)
+                                             : back_launch<__nv_bfloat16>(h, y, p, DW, sms, &parts, stream);
         if (e != cudaSuccess) return GEMM_ERR_CUDA;
     }
-    if (DW && ctas != 1 && dw_launch(static_cast<const float *>(workspace), ctas, (int)K, DW, stream) != cudaSuccess)
+    if (DW && parts != 1 && dw_launch(static_cast<const float *>(workspace), parts, (int)K, DW, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
     return GEMM_OK;
 }

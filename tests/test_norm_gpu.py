@@ -245,6 +245,21 @@ def test_backward_of_many_rows(M, K, dy, h):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+# rows that several multiprocessors share, each with several of them, and the sizes next to where the sharing changes
+@pytest.mark.parametrize("M,K,dy,h", [(800, 8208, "bf16", "bf16"), (700, 9008, "f32", "f32"), (500, 8192, "f32", "f32"),
+                                      (500, 7168, "f32", "f32"), (500, 7184, "bf16", "f32"), (77, 12304, "bf16", "bf16"),
+                                      (400, 16384, "f32", "f32"), (400, 16384, "f32", "bf16"), (300, 16400, "f32", "f32"),
+                                      (200, 20496, "bf16", "f32"), (170, 28688, "f32", "f32"), (76, 16384, "bf16", "bf16")])
+def test_backward_of_shared_rows(M, K, dy, h):
+    t = back_inputs(M, K, dy, h, seed=M + K)
+    got = run_backward(M, K, dy, h, "f16", *t)
+    check_backward(M, dy, h, "f16", got, *t)
+    again = run_backward(M, K, dy, h, "f16", *t, in_place=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    lone = run_backward(M, K, dy, h, "f16", *t, again=False, want_dw=False)
+    assert torch.equal(lone[0], got[0])
+
+
 def test_backward_optional_parts_and_repeatability():
     M, K = 333, 2064
     DY, DH, H, RS, W = back_inputs(M, K, "bf16", "bf16", 5)
