@@ -208,11 +208,20 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ float load_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ void add4(float4 &a, float4 b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+}
+// Where the sums of row m of X and four of a tile's columns lie, in floats: a row's four quads swapped about by the row,
+// so that neither the MMAs' layout of them nor rows of them meet in the banks more than twice
+__device__ __forceinline__ int quad_of(int m, int quad) { return m * 16 + ((quad ^ (m >> 1)) & 3) * 4; }
 
 __device__ __forceinline__ float2 pair_of(const __nv_bfloat16 *, uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -339,6 +348,87 @@ __device__ __forceinline__ void stage_x(const MatvecParams &p, int lo, int hi, i
     }
 }
 
+// Joins the slices of K, the CTA's and the cluster's, always in the same order, and writes D: the `turns` groups of tiles
+// from `group` on.
+template <int FORM>
+__device__ __forceinline__ void join_slices(const MatvecParams &p, float *parts, int group, int turns, int rank) {
+    constexpr int PART = 16 * FORM;
+    const int S = 1 << p.log_slices, R = WARPS >> p.log_slices, cluster = p.cluster;
+    const int quads = R * 4 * p.M;                       // of a turn's outputs: n ascending, then row of X, then tile
+    int from = 0, to = quads;
+    if (cluster != 1) {
+        for (int i = threadIdx.x; i < turns * quads && S > 1; i += WARPS * 32) {
+            const int b = i / quads, q = i - b * quads, tile = over(q >> 2, p.inverse_m), m = (q >> 2) - tile * p.M;
+            float4 *first = reinterpret_cast<float4 *>(parts + (b * WARPS + tile * S) * PART + quad_of(m, q & 3)), v = first[0];
+            for (int s = 1; s < S; ++s) add4(v, first[s * PART / 4]);
+            first[0] = v;
+        }
+        __syncwarp();
+        cluster_sync();
+        const int share = over(R * p.M + cluster - 1, p.inverse_c) * 4;        // whole rows of a tile
+        from = min(rank * share, quads);
+        to = min(from + share, quads);
+    }
+    const int each = to - from;
+    const bool whole = p.N % 4 == 0;
+    for (int i = threadIdx.x; i < turns * each; i += WARPS * 32) {
+        const int b = i / each, q = from + i - b * each, tile = over(q >> 2, p.inverse_m), m = (q >> 2) - tile * p.M;
+        const int n = ((group + b * p.clusters) * R + tile) * 16 + (q & 3) * 4;
+        const float4 *first = reinterpret_cast<const float4 *>(parts + (b * WARPS + tile * S) * PART + quad_of(m, q & 3));
+        if (n >= p.N) continue;
+        const int64_t o = (int64_t)m * p.N + n;
+        float4 c = make_float4(0.f, 0.f, 0.f, 0.f), v = c;
+        if (p.c && whole) {
+            c = *reinterpret_cast<const float4 *>(p.c + o);
+        } else if (p.c) {
+            c.x = p.c[o];
+            if (n + 1 < p.N) c.y = p.c[o + 1];
+            if (n + 2 < p.N) c.z = p.c[o + 2];
+            if (n + 3 < p.N) c.w = p.c[o + 3];
+        }
+        if (cluster == 1) {
+            for (int s = 0; s < S; ++s) add4(v, first[s * PART / 4]);
+        } else {
+            constexpr int AT_ONCE = FORM > 4 ? 8 : 4;        // (the registers of the loop over K are kept meanwhile)
+            static_assert(MOST_CLUSTER % AT_ONCE == 0, "");
+#pragma unroll 1
+            for (int r0 = 0; r0 < cluster; r0 += AT_ONCE) {
+                float4 part[AT_ONCE];
+#pragma unroll
+                for (int r = 0; r < AT_ONCE; ++r)
+                    if (r0 + r < cluster) part[r] = load_cluster4(mapa_shared(smem_addr(first), r0 + r));
+#pragma unroll
+                for (int r = 0; r < AT_ONCE; ++r)
+                    if (r0 + r < cluster) add4(v, part[r]);
+            }
+        }
+        add4(v, c);
+        if (p.out_bf16) {
+            __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(p.d) + o;
+            const __nv_bfloat162 low = __floats2bfloat162_rn(v.x, v.y), high = __floats2bfloat162_rn(v.z, v.w);
+            if (whole) {
+                *reinterpret_cast<uint2 *>(d) =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&low), *reinterpret_cast<const uint32_t *>(&high));
+            } else {
+                d[0] = low.x;
+                if (n + 1 < p.N) d[1] = low.y;
+                if (n + 2 < p.N) d[2] = high.x;
+                if (n + 3 < p.N) d[3] = high.y;
+            }
+        } else {
+            float *d = static_cast<float *>(p.d) + o;
+            if (whole) {
+                *reinterpret_cast<float4 *>(d) = v;
+            } else {
+                d[0] = v.x;
+                if (n + 1 < p.N) d[1] = v.y;
+                if (n + 2 < p.N) d[2] = v.z;
+                if (n + 3 < p.N) d[3] = v.w;
+            }
+        }
+    }
+}
+
 template <typename XT, int MODE, int FORM, bool ALIGNED>
 __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_constant__ MatvecParams p) {
     constexpr bool SCALED_X = !std::is_same<XT, __half>::value;
@@ -448,9 +538,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     uint32_t x_lane[NT];
     bool x_on[NT];
     int x_turn = 0;
-    uint4 x[SPREAD * NT];
-#pragma unroll
-    for (int i = 0; i < SPREAD * NT; ++i) x[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int m = FEW ? g / 2 % FORM : nt * 8 + g;
@@ -470,6 +557,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) total[nt][i] = 0.f;
+        uint4 x[SPREAD * NT];
+#pragma unroll
+        for (int i = 0; i < SPREAD * NT; ++i) x[i] = make_uint4(0, 0, 0, 0);
         const int n0 = (grp * R + tl) * 16;
         // where a column's codes begin within their first word, in bits
         const uint32_t shift[2] = {(uint32_t)((n0 + g) * (codes & 3) & 3) * 8, (uint32_t)((n0 + g + 8) * (codes & 3) & 3) * 8};
@@ -648,59 +738,22 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float *at = mine + (g + 8 * r) * FORM + nt * 8;
+                const int quad = 2 * r + (g >> 2);
                 if constexpr (FEW) {                     // a row's columns of the MMA
                     float v = total[nt][2 * r] + total[nt][2 * r + 1];
                     if (FORM <= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
                     if (FORM <= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-                    if (t < FORM) at[t] = v;
+                    if (t < FORM) mine[quad_of(t, quad) + (g & 3)] = v;
                 } else {
-                    *reinterpret_cast<float2 *>(at + 2 * t) = make_float2(total[nt][2 * r], total[nt][2 * r + 1]);
+                    float *at = mine + quad_of(nt * 8 + 2 * t, quad) + (g & 3);         // (the next row's is 16 on)
+                    at[0] = total[nt][2 * r];
+                    at[16] = total[nt][2 * r + 1];
                 }
             }
         if (++turn < p.held && grp + group_step < groups) continue;
 
-        // Join the slices of K: the CTA's, and the cluster's, always in the same order.
         __syncthreads();
-        const int outputs = R * 16 * p.M;                // of a turn: n ascending, then row of X, then tile
-        auto place = [&](int b, int i, int &m, int &n) { // output i of turn b: where it goes, and its first slice's sum
-            const int tile = over(i >> 4, p.inverse_m);
-            m = (i >> 4) - tile * p.M;
-            n = ((grp - (turn - 1 - b) * group_step) * R + tile) * 16 + (i & 15);
-            return parts + (b * WARPS + tile * S) * PART + (i & 15) * FORM + m;
-        };
-        int m, n;
-        if (cluster != 1) {
-            for (int b = 0; b < turn && S > 1; ++b)
-                for (int i = threadIdx.x; i < outputs; i += WARPS * 32) {
-                    float *first = place(b, i, m, n), v = first[0];
-                    for (int s = 1; s < S; ++s) v += first[s * PART];
-                    first[0] = v;
-                }
-            __syncwarp();
-            cluster_sync();
-        }
-        for (int b = 0; b < turn; ++b)
-            for (int i = rank * WARPS * 32 + threadIdx.x; i < outputs; i += cluster * WARPS * 32) {
-                const float *first = place(b, i, m, n);
-                if (n >= p.N) continue;
-                const int64_t o = (int64_t)m * p.N + n;
-                const float c = p.c ? p.c[o] : 0.f;
-                float v = 0.f;
-                if (cluster == 1) {
-                    for (int s = 0; s < S; ++s) v += first[s * PART];
-                } else {
-                    float part[MOST_CLUSTER];
-#pragma unroll
-                    for (int r = 0; r < MOST_CLUSTER; ++r)
-                        part[r] = r < cluster ? load_cluster(mapa_shared(smem_addr(first), r)) : 0.f;
-#pragma unroll
-                    for (int r = 0; r < MOST_CLUSTER; ++r) v += part[r];
-                }
-                v += c;
-                if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.d)[o] = __float2bfloat16_rn(v);
-                else static_cast<float *>(p.d)[o] = v;
-            }
+        join_slices<FORM>(p, parts, grp - (turn - 1) * group_step, turn, rank);
         turn = 0;
         if (grp + group_step < groups) {                 // the sums have been read before others take their place
             __syncwarp();
@@ -709,7 +762,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
         }
     }
     __syncwarp();
-    if (cluster != 1) cluster_sync();        // no CTA's shared memory goes while another may read it
+    // No CTA's shared memory goes while another may read it.  (Relaxed: this is not to wait for the stores of D.)
+    if (cluster != 1)
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 int slot_bytes(int mode, int K) {
