@@ -797,13 +797,13 @@ MatvecShape search_shape(int M, int N, int K, bool scaled_x, int slot, const int
             s.held = turns < fit ? turns : fit;
             s.smem = base + s.held * part;
             s.grid = clusters * c;
-            // Microseconds, fitted to 3000 measured products (all shapes of 125 sizes of 1 to 16 rows; the shape taken is
-            // within 1.6% of the best one on average, 16% at worst): a warp's steps, at the rate of its weights or of
+            // Microseconds, fitted to 3170 measured products (all shapes of 123 sizes of 1 to 16 rows; the shape taken is
+            // within 1.1% of the best one on average, 13% at worst): a warp's steps, at the rate of its weights or of
             // its arithmetic; the turns' ends; a warp's share of X; the joins.
             const int joins = (turns + s.held - 1) / s.held;
-            const double copy = WARPS * slot / std::min(45e3, 6.37e6 / s.grid);
-            const double step = form == 16 ? std::max(copy, 1.0) : form == 8 ? std::max(copy, 0.87) : copy;
-            const double turn = form == 16 ? 1.9 : form == 8 ? 0.45 : 0.25, join = c == 1 ? 0.5 : 0.8 + 0.5 * c;
+            const double copy = WARPS * slot / std::min(46e3, 6.63e6 / s.grid);
+            const double step = form == 16 ? std::max(copy, 1.15) : form == 8 ? std::max(copy, 0.84) : copy;
+            const double turn = form == 16 ? 0.5 : form == 8 ? 0.09 : 0.14, join = c == 1 ? 0.58 : 1.22 + 0.16 * c;
             const double cost = turns * ((chunks + c * S - 1) / (c * S) * step + turn) + 0.32 * x_rows(form, M) * room / WARPS +
                                 joins * join;
             if (best.grid == 0 || cost < best_cost) {
