@@ -92,6 +92,9 @@ struct NormParams {
 };
 
 // One row per group of threads (threadIdx.y): all of its loads are requested before the first is used.
+// Bound by memory: x and r in, h, y and the scales out, once each.  8192 x 8192, bf16 with residual to e4m3: 72.3 us,
+// 6525 GB/s (96% of a copy's rate); with the rows ahead in a ring in shared memory it took longer.  1 x 4096: 2.1 us, a
+// launch, a trip to memory, the row's sum and a trip for w.
 template <typename XT, typename HT, typename YT, int U>
 __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int N = UNIT, PX = PIECES<XT, N>, PH = PIECES<HT, N>;
@@ -227,7 +230,10 @@ __device__ __forceinline__ float published_sum(const float *red, uint64_t *bar, 
     return __any_sync(0xFFFFFFFFu, lost) ? __uint_as_float(0x7FC00000u) : v;
 }
 
-// A CTA walks rows (rpc at a time) with w and dw in registers; a row costs one barrier, that of its sum.  SPLIT: a row
+// A CTA walks rows (rpc at a time) with w and dw in registers; a row costs one barrier, that of its sum.
+// Bound by memory: dy, h and dh in, dx (and y) out, once each; then dw's join, 3.5 us that no row's bytes overlap.
+// 4096 x 8192, bf16 with y again: 57.2 us, 5870 GB/s (87% of a copy's rate; the rows alone at 98%).  333 x 2064, fp32:
+// 7.2 - 7.8 us, two kernels one after the other with a trip to memory each.  SPLIT: a row
 // is the work of a cluster, a share of its columns each.  Its sum then takes longer than a row's bytes should, so the
 // row before is finished meanwhile, for which dy and h are read from the ring once more.
 template <typename GT, typename HT, typename YT, int U, bool SPLIT>
