@@ -39,11 +39,13 @@ struct GateParams {
 template <typename ZT, typename AT>
 __global__ void __launch_bounds__(256, 4) gate_kernel(const __grid_constant__ GateParams p) {
     constexpr int N = 16;
+    let_next_launch();
     const int blocks = (p.F + BLOCK - 1) / BLOCK;
     int64_t row;
     int u;
     const bool on = p.units.place(blockIdx.x * 256 + threadIdx.x, row, u) && u * N < p.F;
     float g[N], v[N], a[N];
+    wait_for_previous();
     {
         uint4 gq[PIECES<ZT, N>], vq[PIECES<ZT, N>];
         const ZT *z = static_cast<const ZT *>(p.z) + row * 2 * p.F + u * N;
@@ -84,9 +86,11 @@ struct GateBackParams {
 template <typename GT, typename ZT, typename AT>
 __global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ GateBackParams p) {
     constexpr int N = 8;             // no block is shared: the smaller unit keeps each access of a warp contiguous
+    let_next_launch();
     const int blocks = (p.F + BLOCK - 1) / BLOCK;
     int64_t row;
     int u;
+    wait_for_previous();
     if (!p.units.place(blockIdx.x * 256 + threadIdx.x, row, u)) return;
     const uint8_t *ck = p.ck + row * 2 * p.F + u * N, *sf = p.sfck + row * 2 * blocks + u / 4;
     float g[N], v[N], d[N], a[N];
@@ -108,16 +112,14 @@ __global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ 
 
 template <typename ZT>
 cudaError_t gate_launch(gemm_dtype a, unsigned n, const GateParams &p, cudaStream_t stream) {
-    if (a == GEMM_E4M3) gate_kernel<ZT, uint8_t><<<n, 256, 0, stream>>>(p);
-    else if (a == GEMM_BF16) gate_kernel<ZT, __nv_bfloat16><<<n, 256, 0, stream>>>(p);
-    else gate_kernel<ZT, __half><<<n, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (a == GEMM_E4M3) return launch(gate_kernel<ZT, uint8_t>, (int)n, 256, 0, stream, p);
+    if (a == GEMM_BF16) return launch(gate_kernel<ZT, __nv_bfloat16>, (int)n, 256, 0, stream, p);
+    return launch(gate_kernel<ZT, __half>, (int)n, 256, 0, stream, p);
 }
 template <typename GT, typename ZT>
 cudaError_t back_launch(gemm_dtype a, unsigned n, const GateBackParams &p, cudaStream_t stream) {
-    if (a == GEMM_F16) gate_back_kernel<GT, ZT, __half><<<n, 256, 0, stream>>>(p);
-    else gate_back_kernel<GT, ZT, __nv_bfloat16><<<n, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return a == GEMM_F16 ? launch(gate_back_kernel<GT, ZT, __half>, (int)n, 256, 0, stream, p)
+                         : launch(gate_back_kernel<GT, ZT, __nv_bfloat16>, (int)n, 256, 0, stream, p);
 }
 
 bool real(gemm_dtype t) { return t == GEMM_F32 || t == GEMM_BF16; }

@@ -437,6 +437,7 @@ __device__ __forceinline__ void join_slices(const MatvecParams &p, float *parts,
 
 template <typename XT, int MODE, int FORM, bool ALIGNED>
 __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_constant__ MatvecParams p) {
+    rows::let_next_launch();
     constexpr bool SCALED_X = !std::is_same<XT, __half>::value;
     constexpr bool FEW = FORM <= 4;
     constexpr int NT = FORM == 16 ? 2 : 1;               // MMAs' columns of eight rows of X
@@ -529,6 +530,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
         copies_commit();
     };
     enter_tile();
+    rows::wait_for_previous();
     // X's first loads go out before the weights', which take longer
     stage_x<XT, FORM == 16 ? 8 : FORM == 8 ? 4 : 2>(p, lo, hi, FORM, UNBIAS, xf, xscale, [&]() {
 #pragma unroll 1
@@ -838,20 +840,6 @@ MatvecShape matvec_shape(int M, int N, int K, bool scaled_x, int slot, const int
     return s;
 }
 
-void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, int grid, int cluster, int smem, cudaStream_t stream) {
-    cfg = cudaLaunchConfig_t{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(WARPS * 32);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    attr = cudaLaunchAttribute{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-}
-
 constexpr int MAX_DEVICES = 64;
 
 template <typename XT, int MODE, int FORM, bool ALIGNED>
@@ -865,10 +853,8 @@ cudaError_t launch(const MatvecShape &s, const MatvecParams &p, cudaStream_t str
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
-    cluster_config(cfg, attr, s.grid, s.cluster, s.smem, stream);
-    return cudaLaunchKernelEx(&cfg, matvec_kernel<XT, MODE, FORM, ALIGNED>, p);
+    const rows::Launch l(s.grid, WARPS * 32, s.smem, s.cluster, stream);
+    return cudaLaunchKernelEx(&l.config, matvec_kernel<XT, MODE, FORM, ALIGNED>, p);
 }
 
 // How many clusters of 1 .. 8 CTAs run at once on the current device (asked once: one CTA fills an SM whatever
@@ -885,11 +871,8 @@ cudaError_t resident_clusters(const int **out) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SMEM);
         int found[MOST_CLUSTER + 1] = {};
         for (int c = 1; c <= MOST_CLUSTER && e == cudaSuccess; ++c) {
-            cudaLaunchConfig_t cfg;
-            cudaLaunchAttribute attr;
-            cluster_config(cfg, attr, c, c, MOST_SMEM, nullptr);
-            cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&found[c], kernel, &cfg);
+            const rows::Launch l(c, WARPS * 32, MOST_SMEM, c, nullptr, false);
+            e = cudaOccupancyMaxActiveClusters(&found[c], kernel, &l.config);
         }
         if (e != cudaSuccess) return e;
         for (int c = 1; c <= MOST_CLUSTER; ++c) known[dev][c] = found[c];

@@ -99,6 +99,7 @@ template <typename XT, typename HT, typename YT, int U>
 __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int N = UNIT, PX = PIECES<XT, N>, PH = PIECES<HT, N>;
     __shared__ float red[MAX_WARPS];
+    let_next_launch();
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int units = p.K / N, tpr = blockDim.x;
     const XT *x = static_cast<const XT *>(p.x) + row * p.K;
@@ -107,6 +108,7 @@ __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_
 
     uint4 xq[U][PX], rq[U][PH];
     bool on[U];
+    wait_for_previous();
 #pragma unroll
     for (int j = 0; j < U; ++j) {
         const int u = threadIdx.x + j * tpr;
@@ -265,6 +267,8 @@ __global__ void __launch_bounds__(BACK_THREADS, U == 1 ? 2 : 1) norm_back_kernel
         __syncwarp();
         cluster_arrive();
     }
+    let_next_launch();
+    wait_for_previous();
     auto request = [&](int64_t row, int slot) {
         if (PG + PH > 2) __syncwarp();                 // a warp shares its copies: all of it has read what lay there
         if (row < p.M) {
@@ -415,7 +419,6 @@ __global__ void __launch_bounds__(BACK_THREADS, U == 1 ? 2 : 1) norm_back_kernel
             slot = slot + 1 >= p.stages ? 0 : slot + 1;
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!p.parts) return;
 
     // the CTA's sums in a fixed order: rows of threads first, then (norm_dw_kernel) CTAs
@@ -443,13 +446,13 @@ __global__ void __launch_bounds__(BACK_THREADS, U == 1 ? 2 : 1) norm_back_kernel
     }
 }
 
-// dw[k] = sum of the CTAs' rows, in a fixed order: 32 columns per CTA, its warps share the rows out.  Starts early
-// (programmatic launch) and waits for the kernel above.
+// dw[k] = sum of the CTAs' rows, in a fixed order: 32 columns per CTA, its warps share the rows out.
 constexpr int DW_WARPS = 32;
 __global__ void __launch_bounds__(DW_WARPS * 32) norm_dw_kernel(const float *parts, int n, int K, float *__restrict__ dw) {
     __shared__ float s[DW_WARPS][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, k = blockIdx.x * 32 + lane;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next_launch();
+    wait_for_previous();
     float sum = 0.f;
     if (k < K) {
 #pragma unroll 10
@@ -465,16 +468,7 @@ __global__ void __launch_bounds__(DW_WARPS * 32) norm_dw_kernel(const float *par
     }
 }
 cudaError_t dw_launch(const float *parts, int n, int K, float *dw, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((K + 31) / 32));
-    cfg.blockDim = dim3(DW_WARPS * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = n > 0 ? 1 : 0;                        // n = 0: nothing came before it
-    return cudaLaunchKernelEx(&cfg, norm_dw_kernel, parts, n, K, dw);
+    return launch(norm_dw_kernel, (K + 31) / 32, DW_WARPS * 32, 0, stream, parts, n, K, dw);
 }
 
 constexpr int RING_SMEM = 220 * 1024;        // of an SM, for the CTAs that share it
@@ -520,11 +514,10 @@ cudaError_t norm_launch(int sms, const NormParams &p, cudaStream_t stream) {
     const int units = p.K / UNIT;
     const RowShape s = row_shape(units, units <= (p.M <= 2 * sms ? 512 : 128) ? 1 : units <= 1024 ? 2 : 4);
     const dim3 block(s.tpr, s.rpc);
-    const unsigned ctas = (unsigned)((p.M + s.rpc - 1) / s.rpc);
-    if (s.u == 1) norm_kernel<XT, HT, YT, 1><<<ctas, block, 0, stream>>>(p);
-    else if (s.u == 2) norm_kernel<XT, HT, YT, 2><<<ctas, block, 0, stream>>>(p);
-    else norm_kernel<XT, HT, YT, 4><<<ctas, block, 0, stream>>>(p);
-    return cudaGetLastError();
+    const int ctas = (int)((p.M + s.rpc - 1) / s.rpc);
+    if (s.u == 1) return launch(norm_kernel<XT, HT, YT, 1>, ctas, block, 0, stream, p);
+    if (s.u == 2) return launch(norm_kernel<XT, HT, YT, 2>, ctas, block, 0, stream, p);
+    return launch(norm_kernel<XT, HT, YT, 4>, ctas, block, 0, stream, p);
 }
 template <typename XT, typename HT>
 cudaError_t norm_launch(gemm_dtype y, int sms, const NormParams &p, cudaStream_t stream) {
@@ -537,19 +530,6 @@ cudaError_t norm_launch(gemm_dtype h, gemm_dtype y, int sms, const NormParams &p
     return h == GEMM_F32 ? norm_launch<XT, float>(y, sms, p, stream) : norm_launch<XT, __nv_bfloat16>(y, sms, p, stream);
 }
 
-cudaLaunchConfig_t back_config(int ctas, dim3 block, int smem, int cluster, cudaLaunchAttribute *attr, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = (unsigned)cluster;
-    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cfg;
-}
 // How many clusters of `cluster` CTAs run at once, each CTA with an SM's shared memory to itself
 template <auto KERNEL>
 cudaError_t resident_clusters(int cluster, int *out) {
@@ -561,9 +541,8 @@ cudaError_t resident_clusters(int cluster, int *out) {
     std::lock_guard<std::mutex> lock(mu);
     int &n = known[dev][cluster];
     if (n == 0) {
-        cudaLaunchAttribute attr{};
-        const cudaLaunchConfig_t cfg = back_config(cluster, dim3(BACK_THREADS), RING_SMEM, cluster, &attr, nullptr);
-        e = cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg);
+        const Launch l(cluster, BACK_THREADS, RING_SMEM, cluster, nullptr, false);
+        e = cudaOccupancyMaxActiveClusters(&n, KERNEL, &l.config);
         if (e == cudaSuccess && n <= 0) e = cudaErrorInvalidConfiguration;
     }
     *out = n;
@@ -620,10 +599,8 @@ cudaError_t back_launch(const BackShape &b, NormBackParams p, float *dw, int sms
     if (dw && l.groups == 1) p.parts = dw;               // a lone group's sums are dw itself
     *parts = l.groups;
     const int joined = b.s.rpc > 1 ? b.s.rpc * p.K * (int)sizeof(float) : 0;
-    cudaLaunchAttribute attr{};
-    const cudaLaunchConfig_t cfg = back_config(l.groups * b.cluster, dim3(b.s.tpr, b.s.rpc), l.smem > joined ? l.smem : joined,
-                                               b.cluster, &attr, stream);
-    return cudaLaunchKernelEx(&cfg, KERNEL, p);
+    const Launch run(l.groups * b.cluster, dim3(b.s.tpr, b.s.rpc), l.smem > joined ? l.smem : joined, b.cluster, stream);
+    return cudaLaunchKernelEx(&run.config, KERNEL, p);
 }
 template <typename GT, typename HT, typename YT>
 cudaError_t back_launch(const NormBackParams &p, float *dw, int sms, int *parts, cudaStream_t stream) {

@@ -16,6 +16,44 @@ namespace rows {
 
 constexpr int BLOCK = 32;         // elements per scale
 
+// ------------------------------------------------------------------ launches
+
+// Every kernel of these operators may begin while the one before it in the stream ends (a programmatic launch): it lets
+// the next one do so at once, and touches memory only after its own wait, which is for the whole of what came before.
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A launch's configuration: programmatic, and with a cluster where there is one; a query's has the cluster alone
+struct Launch {
+    cudaLaunchAttribute attributes[2];
+    cudaLaunchConfig_t config;
+    Launch(int ctas, dim3 block, int smem, int cluster, cudaStream_t stream, bool programmatic = true) : attributes{}, config{} {
+        unsigned n = 0;
+        if (programmatic) {
+            attributes[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attributes[n++].val.programmaticStreamSerializationAllowed = 1;
+        }
+        if (cluster > 1 || !programmatic) {
+            attributes[n].id = cudaLaunchAttributeClusterDimension;
+            attributes[n].val.clusterDim.x = (unsigned)cluster;
+            attributes[n].val.clusterDim.y = attributes[n].val.clusterDim.z = 1;
+            ++n;
+        }
+        config.gridDim = dim3((unsigned)ctas);
+        config.blockDim = block;
+        config.dynamicSmemBytes = (size_t)smem;
+        config.stream = stream;
+        config.attrs = attributes;
+        config.numAttrs = n;
+    }
+    Launch(const Launch &) = delete;
+};
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), int ctas, dim3 block, int smem, cudaStream_t stream, const Args &...args) {
+    const Launch l(ctas, block, smem, 1, stream);
+    return cudaLaunchKernelEx(&l.config, kernel, args...);
+}
+
 // ------------------------------------------------------------------ elements
 
 // 16-byte pieces of N elements
