@@ -39,13 +39,13 @@ struct GateParams {
 template <typename ZT, typename AT>
 __global__ void __launch_bounds__(256, 4) gate_kernel(const __grid_constant__ GateParams p) {
     constexpr int N = 16;
-    let_next_launch();
     const int blocks = (p.F + BLOCK - 1) / BLOCK;
     int64_t row;
     int u;
     const bool on = p.units.place(blockIdx.x * 256 + threadIdx.x, row, u) && u * N < p.F;
     float g[N], v[N], a[N];
     wait_for_previous();
+    let_next_launch();
     {
         uint4 gq[PIECES<ZT, N>], vq[PIECES<ZT, N>];
         const ZT *z = static_cast<const ZT *>(p.z) + row * 2 * p.F + u * N;
@@ -86,11 +86,11 @@ struct GateBackParams {
 template <typename GT, typename ZT, typename AT>
 __global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ GateBackParams p) {
     constexpr int N = 8;             // no block is shared: the smaller unit keeps each access of a warp contiguous
-    let_next_launch();
     const int blocks = (p.F + BLOCK - 1) / BLOCK;
     int64_t row;
     int u;
     wait_for_previous();
+    let_next_launch();
     if (!p.units.place(blockIdx.x * 256 + threadIdx.x, row, u)) return;
     const uint8_t *ck = p.ck + row * 2 * p.F + u * N, *sf = p.sfck + row * 2 * blocks + u / 4;
     float g[N], v[N], d[N], a[N];

@@ -437,7 +437,6 @@ __device__ __forceinline__ void join_slices(const MatvecParams &p, float *parts,
 
 template <typename XT, int MODE, int FORM, bool ALIGNED>
 __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_constant__ MatvecParams p) {
-    rows::let_next_launch();
     constexpr bool SCALED_X = !std::is_same<XT, __half>::value;
     constexpr bool FEW = FORM <= 4;
     constexpr int NT = FORM == 16 ? 2 : 1;               // MMAs' columns of eight rows of X
@@ -531,6 +530,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     };
     enter_tile();
     rows::wait_for_previous();
+    rows::let_next_launch();
     // X's first loads go out before the weights', which take longer
     stage_x<XT, FORM == 16 ? 8 : FORM == 8 ? 4 : 2>(p, lo, hi, FORM, UNBIAS, xf, xscale, [&]() {
 #pragma unroll 1

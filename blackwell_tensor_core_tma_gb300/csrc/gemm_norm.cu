@@ -99,7 +99,6 @@ template <typename XT, typename HT, typename YT, int U>
 __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int N = UNIT, PX = PIECES<XT, N>, PH = PIECES<HT, N>;
     __shared__ float red[MAX_WARPS];
-    let_next_launch();
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int units = p.K / N, tpr = blockDim.x;
     const XT *x = static_cast<const XT *>(p.x) + row * p.K;
@@ -109,6 +108,7 @@ __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_
     uint4 xq[U][PX], rq[U][PH];
     bool on[U];
     wait_for_previous();
+    let_next_launch();
 #pragma unroll
     for (int j = 0; j < U; ++j) {
         const int u = threadIdx.x + j * tpr;
@@ -267,7 +267,6 @@ __global__ void __launch_bounds__(BACK_THREADS, U == 1 ? 2 : 1) norm_back_kernel
         __syncwarp();
         cluster_arrive();
     }
-    let_next_launch();
     wait_for_previous();
     auto request = [&](int64_t row, int slot) {
         if (PG + PH > 2) __syncwarp();                 // a warp shares its copies: all of it has read what lay there
@@ -419,6 +418,7 @@ __global__ void __launch_bounds__(BACK_THREADS, U == 1 ? 2 : 1) norm_back_kernel
             slot = slot + 1 >= p.stages ? 0 : slot + 1;
         }
     }
+    let_next_launch();
     if (!p.parts) return;
 
     // the CTA's sums in a fixed order: rows of threads first, then (norm_dw_kernel) CTAs
@@ -451,8 +451,8 @@ constexpr int DW_WARPS = 32;
 __global__ void __launch_bounds__(DW_WARPS * 32) norm_dw_kernel(const float *parts, int n, int K, float *__restrict__ dw) {
     __shared__ float s[DW_WARPS][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, k = blockIdx.x * 32 + lane;
-    let_next_launch();
     wait_for_previous();
+    let_next_launch();
     float sum = 0.f;
     if (k < K) {
 #pragma unroll 10

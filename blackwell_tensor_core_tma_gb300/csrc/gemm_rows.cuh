@@ -18,8 +18,11 @@ constexpr int BLOCK = 32;         // elements per scale
 
 // ------------------------------------------------------------------ launches
 
-// Every kernel of these operators may begin while the one before it in the stream ends (a programmatic launch): it lets
-// the next one do so at once, and touches memory only after its own wait, which is for the whole of what came before.
+// Every kernel of these operators may begin while the one before it in the stream ends (a programmatic launch).  It
+// touches memory only after its own wait, which is for the whole of what came before, and then (the norm's gradient when
+// its rows are done) lets the next one begin.
+// Doing so before the wait has kernels queue up on the SMs: a row of small calls then takes longer (the norm of
+// 333 x 2048 3.8 us instead of 2.3, the gate of it 2.7 instead of 2.0; of one row 0.3 us less).
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
