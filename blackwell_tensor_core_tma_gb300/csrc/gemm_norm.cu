@@ -92,8 +92,8 @@ struct NormParams {
 };
 
 // One row per group of threads (threadIdx.y): all of its loads are requested before the first is used.
-// Bound by memory: x and r in, h, y and the scales out, once each.  8192 x 8192, bf16 with residual to e4m3: 72.3 us,
-// 6525 GB/s (96% of a copy's rate); with the rows ahead in a ring in shared memory it took longer.  1 x 4096: 2.1 us, a
+// Bound by memory: x and r in, h, y and the scales out, once each.  8192 x 8192, bf16 with residual to e4m3: 71.9 us,
+// 6565 GB/s (97% of a copy's rate); with the rows ahead in a ring in shared memory it took longer.  1 x 4096: 1.8 us, a
 // launch, a trip to memory, the row's sum and a trip for w.
 template <typename XT, typename HT, typename YT, int U>
 __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormParams p) {
@@ -234,8 +234,8 @@ __device__ __forceinline__ float published_sum(const float *red, uint64_t *bar, 
 
 // A CTA walks rows (rpc at a time) with w and dw in registers; a row costs one barrier, that of its sum.
 // Bound by memory: dy, h and dh in, dx (and y) out, once each; then dw's join, 3.5 us that no row's bytes overlap.
-// 4096 x 8192, bf16 with y again: 57.2 us, 5870 GB/s (87% of a copy's rate; the rows alone at 98%).  333 x 2064, fp32:
-// 7.2 - 7.8 us, two kernels one after the other with a trip to memory each.  SPLIT: a row
+// 4096 x 8192, bf16 with y again: 56.9 us, 5895 GB/s (87% of a copy's rate; the rows alone at 97%).  333 x 2064, fp32:
+// 7.1 us, two kernels one after the other with a trip to memory each.  SPLIT: a row
 // is the work of a cluster, a share of its columns each.  Its sum then takes longer than a row's bytes should, so the
 // row before is finished meanwhile, for which dy and h are read from the ring once more.
 template <typename GT, typename HT, typename YT, int U, bool SPLIT>
@@ -558,10 +558,10 @@ struct BackShape {
     int cluster, share;
 };
 // Few rows: as many threads as there are units.  Many: two units per thread with everything in registers, 512 threads
-// per SM and the ring as deep as fits (4096 x 8192, bf16: 57.2 us; with 64 registers, twice the threads and g and n
+// per SM and the ring as deep as fits (4096 x 8192, bf16: 56.9 us; with 64 registers, twice the threads and g and n
 // read again from the ring 67.6).
 // Rows of more than 8192 elements, and those of which an SM's shared memory does not hold three, are split over 2, 4 or
-// 8 CTAs.  2048 x 16384, bf16: 60.5 us with two CTAs per row; by one CTA with four units per thread, and w read again
+// 8 CTAs.  2048 x 16384, bf16: 60.0 us with two CTAs per row; by one CTA with four units per thread, and w read again
 // for every row, 88.3.  4096 x 8192, all fp32: 96.9 us with two, 106.6 with one and a ring of two rows.
 constexpr int LINE = 16;                     // units of 256 bytes
 BackShape back_shape(int64_t M, int K, int sms, int unit_bytes) {
