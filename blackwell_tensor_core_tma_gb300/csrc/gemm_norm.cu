@@ -51,7 +51,7 @@ constexpr int MAX_WARPS = 32;
 struct RowShape {
     int u, tpr, rpc;
 };
-RowShape row_shape(int units, int u) {
+RowShape row_shape(int units, int u, int threads = 256) {      // threads: of a CTA, at least a row's
     RowShape s;
     s.u = u;
     const int need = (units + s.u - 1) / s.u;
@@ -61,20 +61,23 @@ RowShape row_shape(int units, int u) {
     } else {
         s.tpr = (need + 31) / 32 * 32;
     }
-    s.rpc = s.tpr >= 256 ? 1 : 256 / s.tpr;
+    s.rpc = s.tpr >= threads ? 1 : threads / s.tpr;
     return s;
 }
 
 // Sum over the threads of a row (threadIdx.y), the same in each of them and in a fixed order: within a warp,
 // then each warp over the row's warps.  Every thread of the CTA takes part.  `red` holds one float per warp; it may
-// be written again after the next __syncthreads.
+// be written again after the row's next sum in another place.  OWN: a row's warps wait at a barrier of their own (there
+// are fifteen, and at most eight rows of whole warps in a CTA), not for the CTA's other rows.
+template <bool OWN>
 __device__ __forceinline__ float row_sum(float v, float *red) {
     const int tpr = blockDim.x;
     for (int o = min(tpr, 32) / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (tpr <= 32) return v;
     const int lane = threadIdx.x & 31, warps = tpr / 32;
     if (lane == 0) red[threadIdx.y * warps + threadIdx.x / 32] = v;
-    __syncthreads();
+    if (OWN) asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(tpr) : "memory");
+    else __syncthreads();
     v = lane < warps ? red[threadIdx.y * warps + lane] : 0.f;
     for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_
 #pragma unroll
         for (int i = 0; i < N; ++i) sum = fmaf(v[j][i], v[j][i], sum);
     }
-    sum = row_sum(sum, red);
+    sum = row_sum<false>(sum, red);
     const float rstd = __frsqrt_rn(sum / (float)p.K + p.eps);
     if (row < p.M && threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
 
@@ -235,8 +238,8 @@ __device__ __forceinline__ float published_sum(const float *red, uint64_t *bar, 
 // A CTA walks rows (rpc at a time) with w and dw in registers; a row costs one barrier, that of its sum.
 // Bound by memory: dy, h and dh in, dx (and y) out, once each; then dw's join, 3.5 us that no row's bytes overlap.
 // 4096 x 8192, bf16 with y again: 56.9 us, 5895 GB/s (87% of a copy's rate; the rows alone at 97%).  333 x 2064, fp32:
-// 7.1 us, two kernels one after the other with a trip to memory each.  SPLIT: a row
-// is the work of a cluster, a share of its columns each.  Its sum then takes longer than a row's bytes should, so the
+// 7.1 us, two kernels one after the other with a trip to memory each.
+// SPLIT: a row is the work of a cluster, a share of its columns each.  Its sum then takes longer than a row's bytes should, so the
 // row before is finished meanwhile, for which dy and h are read from the ring once more.
 template <typename GT, typename HT, typename YT, int U, bool SPLIT>
 __global__ void __launch_bounds__(BACK_THREADS, U == 1 ? 2 : 1) norm_back_kernel(const __grid_constant__ NormBackParams p) {
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(BACK_THREADS, U == 1 ? 2 : 1) norm_back_kernel
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (live && threadIdx.x + j * tpr < units) first_pass(row, j, rstd, g[j], n[j], sum);
-            const float c = row_sum(sum[0] + sum[1], red[turn]) * p.inverse_k;
+            const float c = row_sum<true>(sum[0] + sum[1], red[turn]) * p.inverse_k;
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (live && threadIdx.x + j * tpr < units) second_pass(row, slot, j, rstd, c, g[j], n[j]);
@@ -446,29 +449,39 @@ __global__ void __launch_bounds__(BACK_THREADS, U == 1 ? 2 : 1) norm_back_kernel
     }
 }
 
-// dw[k] = sum of the CTAs' rows, in a fixed order: 32 columns per CTA, its warps share the rows out.
+// dw[k] = sum of the CTAs' rows, in a fixed order: COLUMNS columns per CTA, its warps share the rows out, 32 / COLUMNS of
+// them at a time.  Few columns for small K and many rows, so that all SMs take part: 1000 x 2048, bf16 9.9 us
+// with eight columns, 11.2 with 32 (`spread`; 333 x 2064, fp32, a row per CTA: 7.5 and 7.1).
 constexpr int DW_WARPS = 32;
+template <int COLUMNS>
 __global__ void __launch_bounds__(DW_WARPS * 32) norm_dw_kernel(const float *parts, int n, int K, float *__restrict__ dw) {
-    __shared__ float s[DW_WARPS][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, k = blockIdx.x * 32 + lane;
+    constexpr int ROWS = 32 / COLUMNS;
+    __shared__ float s[DW_WARPS][COLUMNS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = lane % COLUMNS, k = blockIdx.x * COLUMNS + c;
     wait_for_previous();
     let_next_launch();
     float sum = 0.f;
     if (k < K) {
 #pragma unroll 10
-        for (int i = warp; i < n; i += DW_WARPS) sum += parts[(int64_t)i * K + k];
+        for (int i = warp * ROWS + lane / COLUMNS; i < n; i += DW_WARPS * ROWS) sum += parts[(int64_t)i * K + k];
     }
-    s[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && k < K) {
-        float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < DW_WARPS; ++i) t += s[i][lane];
-        dw[k] = t;
-    }
+    for (int o = COLUMNS; o < 32; o *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane < COLUMNS) s[warp][c] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < DW_WARPS; i += ROWS) t += s[i + lane / COLUMNS][c];
+#pragma unroll
+    for (int o = COLUMNS; o < 32; o *= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if (lane < COLUMNS && k < K) dw[k] = t;
 }
-cudaError_t dw_launch(const float *parts, int n, int K, float *dw, cudaStream_t stream) {
-    return launch(norm_dw_kernel, (K + 31) / 32, DW_WARPS * 32, 0, stream, parts, n, K, dw);
+cudaError_t dw_launch(const float *parts, int n, int K, float *dw, int sms, bool spread, cudaStream_t stream) {
+    const int at_once = spread ? 2 * sms : 0;            // CTAs
+    if (K <= 8 * at_once) return launch(norm_dw_kernel<8>, (K + 7) / 8, DW_WARPS * 32, 0, stream, parts, n, K, dw);
+    if (K <= 16 * at_once) return launch(norm_dw_kernel<16>, (K + 15) / 16, DW_WARPS * 32, 0, stream, parts, n, K, dw);
+    return launch(norm_dw_kernel<32>, (K + 31) / 32, DW_WARPS * 32, 0, stream, parts, n, K, dw);
 }
 
 constexpr int RING_SMEM = 220 * 1024;        // of an SM, for the CTAs that share it
@@ -573,6 +586,11 @@ BackShape back_shape(int64_t M, int K, int sms, int unit_bytes) {
         if (b.cluster == 1) {
             b.share = units;
             b.s = row_shape(units, units <= (M <= 3 * sms ? BACK_THREADS : 128) ? 1 : 2);
+            // With several rows for every CTA, large CTAs, of which there are fewer partial sums of dw: 16384 x 1024, bf16
+            // 33.9 us, 41.5 with CTAs of 256 threads.
+            const RowShape large = row_shape(units, b.s.u, BACK_THREADS);
+            const int row = large.tpr * large.rpc * large.u * unit_bytes;
+            if (M >= (int64_t)4 * sms * large.rpc && row * 3 * (large.u == 1 ? 2 : 1) <= RING_SMEM) b.s = large;
         } else {
             b.share = (units + LINE * b.cluster - 1) / (LINE * b.cluster) * LINE;        // whole lines of memory
             b.s = row_shape(b.share, 2);
@@ -682,7 +700,7 @@ extern "C" gemm_status gemm_norm_backward(int64_t M, int64_t K, gemm_dtype dy, g
                                              : back_launch<__nv_bfloat16>(h, y, p, DW, sms, &parts, stream);
         if (e != cudaSuccess) return GEMM_ERR_CUDA;
     }
-    if (DW && parts != 1 && dw_launch(static_cast<const float *>(workspace), parts, (int)K, DW, stream) != cudaSuccess)
+    if (DW && parts != 1 && dw_launch(static_cast<const float *>(workspace), parts, (int)K, DW, sms, M > parts, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
     return GEMM_OK;
 }

@@ -260,6 +260,20 @@ def test_backward_of_shared_rows(M, K, dy, h):
     assert torch.equal(lone[0], got[0])
 
 
+# several rows for every CTA, with as many rows at a time as a CTA takes: row groups of part of a warp, of whole warps and
+# of warps with idle lanes, and the widths where the last sum of dw changes
+@pytest.mark.parametrize("M,K,dy,h", [(20000, 112, "bf16", "bf16"), (10000, 256, "f32", "f32"), (5000, 1024, "bf16", "bf16"),
+                                      (3100, 528, "bf16", "f32"), (3100, 2064, "bf16", "bf16"), (1300, 4096, "f32", "bf16"),
+                                      (1300, 2432, "bf16", "bf16"), (1300, 2448, "bf16", "bf16"), (700, 4864, "bf16", "bf16"),
+                                      (700, 4880, "f32", "f32")])
+def test_backward_of_many_row_groups(M, K, dy, h):
+    t = back_inputs(M, K, dy, h, seed=M + K)
+    got = run_backward(M, K, dy, h, "bf16", *t)
+    check_backward(M, dy, h, "bf16", got, *t)
+    again = run_backward(M, K, dy, h, "bf16", *t, in_place=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
 def test_backward_optional_parts_and_repeatability():
     M, K = 333, 2064
     DY, DH, H, RS, W = back_inputs(M, K, "bf16", "bf16", 5)
