@@ -96,8 +96,8 @@ struct NormParams {
 
 // One row per group of threads (threadIdx.y): all of its loads are requested before the first is used.
 // Bound by memory: x and r in, h, y and the scales out, once each.  8192 x 8192, bf16 with residual to e4m3: 71.9 us,
-// 6565 GB/s (97% of a copy's rate); with the rows ahead in a ring in shared memory it took longer.  1 x 4096: 1.8 us, a
-// launch, a trip to memory, the row's sum and a trip for w.
+// 6565 GB/s (97% of a copy's rate); with the rows ahead in a ring in shared memory it took longer.  1 x 4096: 1.7 us, a
+// launch, a trip to memory and the row's sum.
 template <typename XT, typename HT, typename YT, int U>
 __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int N = UNIT, PX = PIECES<XT, N>, PH = PIECES<HT, N>;
@@ -119,6 +119,14 @@ __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_
         load_pieces(x + u * N, on[j], xq[j]);
         load_pieces(r + u * N, on[j] && p.r, rq[j]);
     }
+    // w with the row, where registers allow it, or behind the row's sum: with two units only if both inputs are fp32,
+    // whose occupancy is no lower for it (4096 x 8192: 66.4 us, 71.4 behind the sum; bf16 x and fp32 h 62.4 and 57.1).
+    constexpr bool EARLY_W = U == 1 || (U == 2 && PX + PH == 4);
+    float w[U][N];
+    if (EARLY_W)
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (on[j]) load(p.w + (threadIdx.x + j * tpr) * N, w[j]);
     float v[U][N];
     float sum = 0.f;
 #pragma unroll
@@ -142,10 +150,9 @@ __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_
     for (int j = 0; j < U; ++j) {
         const int u = threadIdx.x + j * tpr;
         if (on[j]) {
-            float w[N];
-            load(p.w + u * N, w);
+            if (!EARLY_W) load(p.w + u * N, w[j]);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[j][i] = v[j][i] * rstd * w[i];
+            for (int i = 0; i < N; ++i) v[j][i] = v[j][i] * rstd * w[j][i];
         }
         if constexpr (sizeof(YT) == 1) {
             const uint32_t code = quantise(v[j], static_cast<uint8_t *>(p.y) + row * p.K + u * N, on[j]);
