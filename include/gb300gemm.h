@@ -321,7 +321,9 @@ gemm_status gemm_chain_run_host(gemm_plan_t p, const void *A, const void *B, con
  *
  * None takes a plan or allocates: the caller owns and passes every buffer, calls on different
  * streams are independent, and each may be captured into a graph.  They enqueue on cuda_stream
- * (a cudaStream_t of the current device, which must be compute capability 10.3) and return.
+ * (a cudaStream_t of the current device, which must be compute capability 10.3) and return.  Their
+ * kernels may be set up while what came before them in the stream ends, and wait for the whole of
+ * it before they touch memory.
  * M counts rows (tokens); M = 0 is allowed and does nothing (gemm_norm_backward then sets DW to
  * zero).  Buffers are packed and row-major, and every pointer but the scale codes' and RSTD's must be
  * 16-byte aligned (GEMM_ERR_ALIGNMENT).  Outputs must not overlap inputs except where said.
@@ -364,7 +366,7 @@ gemm_status gemm_norm_run(int64_t M, int64_t K, gemm_dtype x, gemm_dtype h, gemm
  * again for the weight's gradient, GEMM_BF16 or GEMM_F16; y is ignored without it) may be NULL.
  * With DW the call needs a workspace of min(M, GEMM_NORM_PARTS) * K fp32 values (smaller:
  * GEMM_ERR_INVALID_ARG), whose contents do not matter before or after.  DW is summed in fp32 in an order
- * that depends on M, K and the GPU's SM count alone.
+ * that depends on M, K, the types and the GPU's SM count alone.
  */
 #define GEMM_NORM_PARTS 512
 gemm_status gemm_norm_backward(int64_t M, int64_t K, gemm_dtype dy, gemm_dtype h, gemm_dtype y, const void *DY,
