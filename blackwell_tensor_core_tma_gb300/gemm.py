@@ -30,7 +30,8 @@ EXPORTS = ["gemm_plan_create", "gemm_run", "gemm_run_host", "gemm_plan_last_stat
            "gemm_testing_pair_tile_n", "gemm_plan_set_clock_meter", "gemm_plan_read_clock_meter",
            "gemm_testing_trace_slots", "gemm_testing_set_trace", "gemm_testing_tmem_ld_probe",
            "gemm_testing_staging_probe", "gemm_testing_schedule", "gemm_testing_e4m3_pair_tile_n",
-           "gemm_norm_run", "gemm_norm_backward", "gemm_gate_run", "gemm_gate_backward", "gemm_matvec_run"]
+           "gemm_norm_run", "gemm_norm_backward", "gemm_gate_run", "gemm_gate_backward", "gemm_matvec_run",
+           "gemm_testing_set_norm_fault"]
 
 # the per-role trace counters of one CTA, in slot order (a GB300_TRACE=1 library:
 # gemm_testing_set_trace); SM clock cycles unless the name says otherwise
@@ -97,6 +98,8 @@ def lib():
         L.gemm_status_string.restype = ctypes.c_char_p
         L.gemm_testing_set_fault.argtypes = [vp, st]
         L.gemm_testing_set_fault.restype = st
+        L.gemm_testing_set_norm_fault.argtypes = [st]
+        L.gemm_testing_set_norm_fault.restype = st
         L.gemm_plan_set_split_k.argtypes = [vp, st]
         L.gemm_plan_set_split_k.restype = st
         L.gemm_plan_set_stream_k.argtypes = [vp, st]
@@ -273,6 +276,10 @@ def gemm_plan_destroy(plan: int):
 
 def gemm_testing_set_fault(plan: int, fault: int):
     _check(lib().gemm_testing_set_fault(plan, fault), "gemm_testing_set_fault")
+
+
+def gemm_testing_set_norm_fault(limit: int):
+    _check(lib().gemm_testing_set_norm_fault(limit), "gemm_testing_set_norm_fault")
 
 
 def gemm_run_noalloc(M: int, N: int, K: int, ab, d, A, B, C, D, stream=None, wait: int = 0) -> int:

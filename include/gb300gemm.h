@@ -367,6 +367,10 @@ gemm_status gemm_norm_run(int64_t M, int64_t K, gemm_dtype x, gemm_dtype h, gemm
  * With DW the call needs a workspace of min(M, GEMM_NORM_PARTS) * K fp32 values (smaller:
  * GEMM_ERR_INVALID_ARG), whose contents do not matter before or after.  DW is summed in fp32 in an order
  * that depends on M, K, the types and the GPU's SM count alone.
+ *
+ * Rows that are split over several CTAs (those of more than 8192 elements, and some of fp32) wait for one another's
+ * sums with a limit of seconds.  Were it ever to run out, DX of that row and of rows behind it would be NaN and the
+ * call would end as usual.
  */
 #define GEMM_NORM_PARTS 512
 gemm_status gemm_norm_backward(int64_t M, int64_t K, gemm_dtype dy, gemm_dtype h, gemm_dtype y, const void *DY,

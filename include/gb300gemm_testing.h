@@ -107,6 +107,16 @@ gemm_status gemm_testing_schedule(int chain, int tiles_m, int tiles_n, int group
                                   int sk_dp_tiles, int sk_units, int unit, int units, int *out, int max_pieces,
                                   int *n_pieces);
 
+/*
+ * gemm_norm_backward's wait for the sums of a row that several CTAs share, made to run out without
+ * faulting a GPU: with limit > 0 one warp of each cluster withholds the sum of the cluster's first
+ * row in this host thread's later calls, and the other warps give up after `limit` looks for it.  Such
+ * a call ends by itself: DX of that row and of the cluster's later ones is NaN, DW and Y are as ever.
+ * limit = 0 restores normal calls (a limit of seconds); calls whose rows are not split are not touched.
+ * GEMM_ERR_INVALID_ARG for a negative limit.
+ */
+gemm_status gemm_testing_set_norm_fault(int limit);
+
 #ifdef __cplusplus
 }
 #endif

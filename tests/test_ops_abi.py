@@ -96,3 +96,8 @@ def test_no_rows_is_no_work():
     assert gemm.gemm_gate_run(0, 64, "bf16", "e4m3", None, None) == gemm.GEMM_OK
     assert gemm.gemm_gate_backward(0, 64, "bf16", "bf16", "bf16", None, None, None, None) == gemm.GEMM_OK
     assert gemm.gemm_matvec_run(0, 64, 64, "bf16", "bf16", 1, None, None, None, None, None) == gemm.GEMM_OK
+
+
+def test_norm_fault_refuses_a_negative_limit():
+    refused(INVALID, gemm.gemm_testing_set_norm_fault, -1)
+    gemm.gemm_testing_set_norm_fault(0)
