@@ -50,6 +50,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "gb300gemm_testing.h"
 #include "gemm_rows.cuh"
 #include "ptx.cuh"
 
@@ -925,42 +926,47 @@ extern "C" gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dty
     if (st != GEMM_OK) return st;
     const int *resident = nullptr;
     if (resident_clusters(&resident) != cudaSuccess) return GEMM_ERR_CUDA;
-    const int slot = slot_bytes(block_scaled, (int)K);
-    // rows whose activations fit no cluster's shared memory (16 of them from K about 18000 on, 8 from about 31000)
-    // go in several passes
-    int most = (int)M;
-    MatvecShape s = matvec_shape(most, (int)N, (int)K, x == GEMM_BF16, slot, resident);
-    while (s.grid == 0 && most > 1) {
-        most = (most + 1) / 2;
-        s = matvec_shape(most, (int)N, (int)K, x == GEMM_BF16, slot, resident);
-    }
-    for (int m = 0; m < (int)M; m += most) {
-        const int rows = (int)M - m < most ? (int)M - m : most;
-        if (rows != most) s = matvec_shape(rows, (int)N, (int)K, x == GEMM_BF16, slot, resident);
-        if (s.grid == 0) return GEMM_ERR_CUDA;
-        const int64_t out = (int64_t)m * N;
-        const MatvecParams p{static_cast<const uint8_t *>(X) + (int64_t)m * K * 2,
-                             static_cast<const uint8_t *>(B),
-                             SFB,
-                             C ? C + out : nullptr,
-                             static_cast<uint8_t *>(D) + out * (d == GEMM_BF16 ? 2 : 4),
-                             rows,
-                             (int)N,
-                             (int)K,
-                             inverse16(rows),
-                             inverse16(x_rows(form_of(rows), rows)),
-                             inverse16(s.cluster),
-                             s.cluster << s.log_slices == 1 ? 0u : inverse32(s.cluster << s.log_slices),
-                             d == GEMM_BF16,
-                             s.cluster,
-                             s.grid / s.cluster,
-                             s.log_slices,
-                             s.x_stride,
-                             s.held};
-        cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
-        const cudaError_t e = x == GEMM_F16 ? launch<__half>(block_scaled, s, p, stream)
-                                            : launch<__nv_bfloat16>(block_scaled, s, p, stream);
-        if (e != cudaSuccess) return GEMM_ERR_CUDA;
-    }
+    const MatvecShape s = matvec_shape((int)M, (int)N, (int)K, x == GEMM_BF16, slot_bytes(block_scaled, (int)K), resident);
+    if (s.grid == 0) return GEMM_ERR_UNSUPPORTED;        // (clusters of eight hold the activations of every M and K)
+    const int T = s.cluster << s.log_slices;
+    const MatvecParams p{X,
+                         static_cast<const uint8_t *>(B),
+                         SFB,
+                         C,
+                         D,
+                         (int)M,
+                         (int)N,
+                         (int)K,
+                         inverse16((int)M),
+                         inverse16(x_rows(form_of((int)M), (int)M)),
+                         inverse16(s.cluster),
+                         T == 1 ? 0u : inverse32(T),
+                         d == GEMM_BF16,
+                         s.cluster,
+                         s.grid / s.cluster,
+                         s.log_slices,
+                         s.x_stride,
+                         s.held};
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
+    const cudaError_t e = x == GEMM_F16 ? launch<__half>(block_scaled, s, p, stream)
+                                        : launch<__nv_bfloat16>(block_scaled, s, p, stream);
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// Test hook (declared in include/gb300gemm_testing.h): the launch's shape.
+extern "C" gemm_status gemm_testing_matvec_shape(int64_t M, int64_t N, int64_t K, gemm_dtype x, int block_scaled,
+                                                 int largest_cluster, int *out) {
+    if (!out || M < 1 || M > MAX_M || N < 1 || N > INT32_MAX / 16 || K < 32 || K > MAX_K || K % 32 != 0 || largest_cluster < 1 ||
+        largest_cluster > MOST_CLUSTER || (x != GEMM_F16 && x != GEMM_BF16) ||
+        (block_scaled != GEMM_SCALE_UE8M0_32 && block_scaled != GEMM_SCALE_UE4M3_16))
+        return GEMM_ERR_INVALID_ARG;
+    int resident[MOST_CLUSTER + 1] = {};
+    for (int c = 1; c <= largest_cluster; ++c) resident[c] = 152 / c;
+    const MatvecShape s = search_shape((int)M, (int)N, (int)K, x == GEMM_BF16, slot_bytes(block_scaled, (int)K), resident);
+    if (s.grid == 0) return GEMM_ERR_UNSUPPORTED;
+    out[0] = s.grid;
+    out[1] = s.cluster;
+    out[2] = 1 << s.log_slices;
+    out[3] = s.smem;
     return GEMM_OK;
 }

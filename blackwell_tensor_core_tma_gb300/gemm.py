@@ -31,7 +31,7 @@ EXPORTS = ["gemm_plan_create", "gemm_run", "gemm_run_host", "gemm_plan_last_stat
            "gemm_testing_trace_slots", "gemm_testing_set_trace", "gemm_testing_tmem_ld_probe",
            "gemm_testing_staging_probe", "gemm_testing_schedule", "gemm_testing_e4m3_pair_tile_n",
            "gemm_norm_run", "gemm_norm_backward", "gemm_gate_run", "gemm_gate_backward", "gemm_matvec_run",
-           "gemm_testing_set_norm_fault"]
+           "gemm_testing_set_norm_fault", "gemm_testing_matvec_shape"]
 
 # the per-role trace counters of one CTA, in slot order (a GB300_TRACE=1 library:
 # gemm_testing_set_trace); SM clock cycles unless the name says otherwise
@@ -100,6 +100,8 @@ def lib():
         L.gemm_testing_set_fault.restype = st
         L.gemm_testing_set_norm_fault.argtypes = [st]
         L.gemm_testing_set_norm_fault.restype = st
+        L.gemm_testing_matvec_shape.argtypes = [i64, i64, i64, st, st, st, ctypes.POINTER(ctypes.c_int)]
+        L.gemm_testing_matvec_shape.restype = st
         L.gemm_plan_set_split_k.argtypes = [vp, st]
         L.gemm_plan_set_split_k.restype = st
         L.gemm_plan_set_stream_k.argtypes = [vp, st]
@@ -280,6 +282,14 @@ def gemm_testing_set_fault(plan: int, fault: int):
 
 def gemm_testing_set_norm_fault(limit: int):
     _check(lib().gemm_testing_set_norm_fault(limit), "gemm_testing_set_norm_fault")
+
+
+def gemm_testing_matvec_shape(M: int, N: int, K: int, x, block_scaled: int, largest_cluster: int = 8):
+    """(CTAs, CTAs per cluster, slices of K per CTA, bytes of shared memory) of a matrix-vector product's launch."""
+    out = (ctypes.c_int * 4)()
+    _check(lib().gemm_testing_matvec_shape(M, N, K, DTYPE.get(x, x), int(block_scaled), largest_cluster, out),
+           "gemm_testing_matvec_shape")
+    return tuple(out)
 
 
 def gemm_run_noalloc(M: int, N: int, K: int, ab, d, A, B, C, D, stream=None, wait: int = 0) -> int:

@@ -117,6 +117,15 @@ gemm_status gemm_testing_schedule(int chain, int tiles_m, int tiles_n, int group
  */
 gemm_status gemm_testing_set_norm_fault(int limit);
 
+/*
+ * gemm_matvec_run's launch for a size, worked out on the host for 152 multiprocessors of which clusters of
+ * up to largest_cluster (1..8) CTAs run at once: out[0] CTAs, out[1] CTAs per cluster, out[2] slices of K per
+ * CTA, out[3] bytes of shared memory.  GEMM_ERR_UNSUPPORTED where the activations fit no such cluster (none of 8);
+ * GEMM_ERR_INVALID_ARG for NULL out or what gemm_matvec_run refuses.
+ */
+gemm_status gemm_testing_matvec_shape(int64_t M, int64_t N, int64_t K, gemm_dtype x, int block_scaled,
+                                      int largest_cluster, int *out);
+
 #ifdef __cplusplus
 }
 #endif
