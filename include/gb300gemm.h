@@ -325,8 +325,9 @@ gemm_status gemm_chain_run_host(gemm_plan_t p, const void *A, const void *B, con
  * kernels may be set up while what came before them in the stream ends, and wait for the whole of
  * it before they touch memory.
  * M counts rows (tokens); M = 0 is allowed and does nothing (gemm_norm_backward then sets DW to
- * zero).  Buffers are packed and row-major, and every pointer but the scale codes' and RSTD's must be
- * 16-byte aligned (GEMM_ERR_ALIGNMENT).  Outputs must not overlap inputs except where said.
+ * zero); it is at most 2^31 - 1 (GEMM_ERR_INVALID_ARG).  Buffers are packed and row-major, and every pointer must be
+ * 16-byte aligned (GEMM_ERR_ALIGNMENT) except RSTD and the scale codes of the norm and the gate (SFY, SFA, SFCK):
+ * gemm_matvec_run's SFB must be.  Outputs must not overlap inputs except where said.
  *
  * Where an output is GEMM_E4M3, it is the A operand of a GEMM_SCALE_UE8M0_32 plan and its scale
  * codes are that plan's SFA: per row, each 32 consecutive elements (the last block of a row may be
@@ -366,7 +367,7 @@ gemm_status gemm_norm_run(int64_t M, int64_t K, gemm_dtype x, gemm_dtype h, gemm
  * again for the weight's gradient, GEMM_BF16 or GEMM_F16; y is ignored without it) may be NULL.
  * With DW the call needs a workspace of min(M, GEMM_NORM_PARTS) * K fp32 values (smaller:
  * GEMM_ERR_INVALID_ARG), whose contents do not matter before or after.  DW is summed in fp32 in an order
- * that depends on M, K, the types and the GPU's SM count alone.
+ * that depends on M, K, the types, the GPU's SM count and (rows split over CTAs) how many clusters the GPU runs at once.
  *
  * Rows that are split over several CTAs (those of more than 8192 elements, and some of fp32) wait for one another's
  * sums with a limit of seconds.  Were it ever to run out, DX of that row and of rows behind it would be NaN and the
@@ -406,8 +407,9 @@ gemm_status gemm_gate_backward(int64_t M, int64_t F, gemm_dtype da, gemm_dtype d
  * D = A·B + C for 1 to 16 rows of 16-bit activations and 4-bit weights: one token, or a few, through
  * a matrix whose other uses run as a GEMM_E2M1 plan.  X (A above): M x K, GEMM_F16 or GEMM_BF16; B and
  * SFB: the plan's own buffers (N x K packed e2m1, N x K/32 UE8M0 or N x K/16 UE4M3 codes by
- * block_scaled); C: M x N fp32 or NULL; D: M x N, GEMM_F32 or GEMM_BF16.  Sums in fp32.  Any N >= 1;
- * K % 32 == 0 (GEMM_ERR_ALIGNMENT); M > 16 or K > 32768: GEMM_ERR_UNSUPPORTED.
+ * block_scaled), SFB 16-byte aligned here as B is; C: M x N fp32 or NULL; D: M x N, GEMM_F32 or GEMM_BF16.
+ * Sums in fp32, in an order that depends on M, N, K, the types and how many clusters the GPU runs at once.  Any N from 1 to
+ * (2^31 - 1) / 16 (GEMM_ERR_INVALID_ARG); K % 32 == 0 (GEMM_ERR_ALIGNMENT); M > 16 or K > 32768: GEMM_ERR_UNSUPPORTED.
  */
 gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dtype x, gemm_dtype d, int block_scaled,
                             const void *X, const void *B, const uint8_t *SFB, const float *C, void *D,
