@@ -398,7 +398,7 @@ gemm_status gemm_gate_run(int64_t M, int64_t F, gemm_dtype z, gemm_dtype a, cons
  *     dz = [ da * u * s * (1 + g * (1 - s)) | da * g * s ],    a = g * s * u
  *
  * da and dz: GEMM_F32 or GEMM_BF16; A (the second product's operand again, for its weight's gradient,
- * GEMM_BF16 or GEMM_F16; a is ignored without it) may be NULL.
+ * GEMM_BF16 or GEMM_F16; a is ignored without it) may be NULL, or DA itself where both are GEMM_BF16.
  */
 gemm_status gemm_gate_backward(int64_t M, int64_t F, gemm_dtype da, gemm_dtype dz, gemm_dtype a, const void *DA,
                                const uint8_t *CK, const uint8_t *SFCK, void *DZ, void *A, void *cuda_stream);
