@@ -16,12 +16,18 @@ namespace {
 
 using namespace rows;
 
-// 1 / (1 + exp(-g)), with the fast exponential and reciprocal (2 + 1.173 |g| and 1 units in the last place): the
-// outputs are rounded to 8 or 16 bits or compared at 1e-6.  exp(-g) infinite gives 0.
-__device__ __forceinline__ float sigmoid(float g) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
-    return r;
+// s = 1 / (1 + exp(-g)) and t = 1 - s = exp(-g) s, which a subtraction would leave few digits of.  With p = 2^-16 exp(-g / 2)
+// both come from r = 1 / (p^2 + 2^-32) = 2^32 s, which is a normal number wherever s is not zero: s goes down to fp32's
+// smallest number, at g = -103, and t to 2^-117.  (Where s is zero t is no matter, but has to be finite.)  The fast
+// exponential and reciprocal (p^2: 4 + 1.173 |g| units in the last place, r: 1) are what the outputs' 8 or 16 bits, or a
+// comparison at 1e-6, have room for.
+__device__ __forceinline__ void sigmoid(float g, float &s, float &t) {
+    float p, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(g * -0.72134752f));                     // log2(e) / 2
+    p *= 0x1p-16f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(p, p, 0x1p-32f)));
+    s = r * 0x1p-32f;
+    t = fminf(p * p, 0x1p126f) * r;
 }
 
 struct GateParams {
@@ -34,7 +40,7 @@ struct GateParams {
 
 // Bound by memory: z in, a and the checkpoint out, once each.  A thread takes half a scale's block, so that two lanes
 // settle its largest magnitude and the units are as wide as 64 registers allow: four CTAs per SM.  4096 x 8192, bf16 to
-// e4m3 with checkpoint: 37.8 us, 6290 GB/s (93% of a copy's rate); three CTAs per SM take 41.0 us, five spill: 46.7.
+// e4m3 with checkpoint: 37.7 us, 6320 GB/s (93% of a copy's rate); three CTAs per SM take 41.0 us, five spill: 46.7.
 // 1 x 8192: 1.5 us, a launch and one trip to memory.
 template <typename ZT, typename AT>
 __global__ void __launch_bounds__(256, 4) gate_kernel(const __grid_constant__ GateParams p) {
@@ -55,7 +61,11 @@ __global__ void __launch_bounds__(256, 4) gate_kernel(const __grid_constant__ Ga
         unpack(z, vq, v);
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) a[i] = g[i] * sigmoid(g[i]) * v[i];
+    for (int i = 0; i < N; ++i) {
+        float s, t;
+        sigmoid(g[i], s, t);
+        a[i] = g[i] * s * v[i];
+    }
     const bool first = on && (u & 1) == 0;           // of its block
     uint32_t code;
     if constexpr (sizeof(AT) == 1) {
@@ -99,7 +109,9 @@ __global__ void __launch_bounds__(256) gate_back_kernel(const __grid_constant__ 
     decode(*reinterpret_cast<const uint2 *>(ck + p.F), scale_value(sf[blocks]), v);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float s = sigmoid(g[i]), gs = g[i] * s, dgs = s * (1.f + g[i] * (1.f - s));
+        float s, t;
+        sigmoid(g[i], s, t);
+        const float gs = g[i] * s, dgs = s * (1.f + g[i] * t);
         a[i] = gs * v[i];
         g[i] = d[i] * v[i] * dgs;
         d[i] *= gs;

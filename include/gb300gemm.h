@@ -384,6 +384,8 @@ gemm_status gemm_norm_backward(int64_t M, int64_t K, gemm_dtype dy, gemm_dtype h
  *
  *     a[m][f] = g[m][f] * s * u[m][f],   s = 1 / (1 + exp(-g[m][f]))
  *
+ * s is within 9 + 1.2 |g| units in the last place where it is a normal fp32 number (g > -87.3), here and in the gradient, as is
+ * 1 - s there for g < 80; below that both lose digits as subnormal numbers do.
  * z: GEMM_F32 or GEMM_BF16; a: GEMM_E4M3 (M x ceil(F/32) scale codes in SFA), GEMM_BF16 or GEMM_F16.  With
  * CK != NULL the call also keeps g and u for the backward pass in 8 bits: CK is M x 2F e4m3 codes in Z's
  * order and SFCK M x 2 ceil(F/32) scale codes (g's blocks of the row, then u's).  F % 16 == 0
