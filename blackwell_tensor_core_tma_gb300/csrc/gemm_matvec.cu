@@ -31,8 +31,7 @@
 // Activations.  fp16 goes in as it is.  bf16 is multiplied per row and chunk by the power of two that brings
 // the largest magnitude to 2^15 .. 2^16, which is exact in fp16 for elements down to 2^-29 of it.
 // What these rules do not hold (bf16 activations too far apart within a chunk, outside 2^-50 .. 2^40, infinite or
-// NaN; UE8M0 scales from 2^33, NaN among them) takes products_64 for that chunk: the same sums in 64 bits from
-// the original values.
+// NaN; UE8M0 scales from 2^33, NaN among them) takes products_by_band for that chunk.
 //
 // A CTA (one per SM) is 16 warps: R tiles of 16 columns by S slices of K, and `c` CTAs of a cluster split K
 // further; the partial sums are joined in a fixed order through shared memory, the cluster's through
@@ -231,61 +230,6 @@ __device__ __forceinline__ void add4(float4 &a, float4 b) {
 // so that neither the MMAs' layout of them nor rows of them meet in the banks more than twice
 __device__ __forceinline__ int quad_of(int m, int quad) { return m * 16 + ((quad ^ (m >> 1)) & 3) * 4; }
 
-__device__ __forceinline__ float2 pair_of(const __nv_bfloat16 *, uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-__device__ __forceinline__ float2 pair_of(const __half *, uint32_t w) { return halves(w); }
-
-// One chunk's products in 64 bits from the original values, for eight rows of X from m0: what lane (g, t) adds to its
-// accumulators (columns n0 + g, n0 + g, n0 + g + 8, n0 + g + 8 by rows 2t, 2t + 1; with FEW row t in x and z).  The
-// four lanes of a column take every fourth 32-block.  64 bits hold every product of the formats' extremes (an activation
-// of 2^127 under a scale of 2^-120), and this is off the path of ordinary data.
-template <typename XT, int MODE, bool FEW>
-__device__ __noinline__ float4 products_64(const MatvecParams &p, int n0, int chunk, int m0) {
-    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3, blocks = p.K / 32;
-    float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int m = 0; m < 8; ++m) {
-        if (m0 + m >= p.M) break;
-        const uint32_t *x = reinterpret_cast<const uint32_t *>(static_cast<const XT *>(p.x) + (int64_t)(m0 + m) * p.K);
-        double sum[2] = {0., 0.};
-        for (int col = 0; col < 2; ++col) {
-            const int n = n0 + g + 8 * col;
-            for (int block = chunk * BLOCKS + t; n < p.N && block < min((chunk + 1) * BLOCKS, blocks); block += 4) {
-                const int64_t at = (int64_t)n * blocks + block;
-                const uint32_t *w = reinterpret_cast<const uint32_t *>(p.b + at * 16);
-                double part[2] = {0., 0.};               // the block's halves
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t h[4];
-                    e2m1x8(w[i], h);
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 v = halves(h[j]), xv = pair_of((const XT *)nullptr, x[block * 16 + 4 * i + j]);
-                        part[i / 2] += (double)v.x * xv.x + (double)v.y * xv.y;
-                    }
-                }
-                if (MODE == GEMM_SCALE_UE8M0_32) {
-                    const int code = p.sfb[at];
-                    sum[col] += code == 255 ? (double)__uint_as_float(0x7FC00000u) : ldexp(part[0] + part[1], code - 127);
-                } else {
-                    const float2 s = halves(ue4m3x2(reinterpret_cast<const uint16_t *>(p.sfb)[at] & 0x7F7Fu));
-                    sum[col] += part[0] * s.x + part[1] * s.y;
-                }
-            }
-        }
-        for (int col = 0; col < 2; ++col) {
-            sum[col] += __shfl_xor_sync(0xFFFFFFFFu, sum[col], 1);
-            sum[col] += __shfl_xor_sync(0xFFFFFFFFu, sum[col], 2);
-        }
-        if (FEW ? m == t : m / 2 == t) {
-            (!FEW && m & 1 ? out.y : out.x) = (float)sum[0];
-            (!FEW && m & 1 ? out.w : out.z) = (float)sum[1];
-        }
-    }
-    return out;
-}
-
-// Rows of X in shared memory: forms 8 and 16 have zeros where X has no row
-__host__ __device__ constexpr int x_rows(int form, int M) { return form > 4 ? form : M; }
-
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -296,6 +240,125 @@ __device__ __forceinline__ uint32_t min_s16x2(uint32_t a, uint32_t b) {
     asm("min.s16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+
+// 0xFFFF where a half of a is less than b's, as bf16 numbers that are not negative
+__device__ __forceinline__ uint32_t less2(uint32_t a, uint32_t b) {
+    return __hlt2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+}
+
+// v * 2^e for e of -240 .. 254 (and what is above: infinity either way), in two steps that are factors of fp32
+__device__ __forceinline__ float times_power(float v, int e) {
+    e = min(e, 254);
+    const int half = e >> 1;
+    return v * __uint_as_float((uint32_t)(half + 127) << 23) * __uint_as_float((uint32_t)(e - half + 127) << 23);
+}
+
+// One chunk's products for eight rows of X from m0, where the chunk's one power of two per row does not hold them or a
+// scale code is from 160 on: what lane (g, t) adds to its accumulators (columns n0 + g, n0 + g, n0 + g + 8, n0 + g + 8
+// by rows 2t, 2t + 1; with FEW row t in x and z).  `w` is the chunk's slot, `shift` the columns' bits within the first words
+// of their codes.
+//
+// bf16: X is read again and taken in bands of thirty exponents, the lowest first: band b holds biased exponents 30 b + 1 ..
+// 30 b + 30 (band 0 also 0, the subnormal numbers), which are fp16's with 30 b subtracted, exactly.  Each band that
+// the chunk spans runs through the MMAs as above, the rest being zeros, and its sums are scaled back in fp32.  Infinities and
+// NaN go with the first band.  A gated unit's output spans two or three bands when its gates are far apart, and a
+// chunk then takes about ten times as long: 16 x 8192 x 16384 (UE8M0) with gates of deviation 8 297 us instead of 28.1,
+// 1 x 32768 x 8192 (UE4M3) 205 instead of 24.9 (with the sums in 64 bits on the CUDA cores 17164 and 1636).
+template <typename XT, int MODE, bool FEW, bool ALIGNED>
+__device__ __noinline__ float4 products_by_band(const MatvecParams &p, uint32_t w, uint2 shift, int chunk, int m0) {
+    constexpr bool BF16 = !std::is_same<XT, __half>::value;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, m = m0 + g;
+    const XT *x = static_cast<const XT *>(p.x) + (int64_t)m * p.K + chunk * CHUNK + t * 8;
+    // the lane's eight values of block i
+    auto load_x = [&](int i) {
+        return m < p.M && chunk * CHUNK + i * 32 < p.K ? *reinterpret_cast<const uint4 *>(x + i * 32) : make_uint4(0, 0, 0, 0);
+    };
+    int band = 0, last = 0;
+    bool special = false;                                // infinities or NaN
+    if (BF16) {
+        uint32_t low = 0x7FFF7FFFu, high = 0;
+#pragma unroll
+        for (int i = 0; i < BLOCKS; ++i) {
+            const uint4 v = load_x(i);
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                low = min_s16x2(low, (q[k] | 0x80008000u) - 0x00010001u);       // |x| - 1 - 2^15, of zeros 2^15 - 1
+                high = max_u16x2(high, q[k] & 0x7FFF7FFFu);
+            }
+        }
+        const int top = (int)__reduce_max_sync(0xFFFFFFFFu, max(high >> 16, high & 0xFFFFu));
+        const int least = __reduce_min_sync(0xFFFFFFFFu, min((int)low >> 16, (int)(int16_t)low)) + 32769;
+        special = top >= 0x7F80;
+        last = (max(min(top >> 7, 254), 1) - 1) / 30;
+        band = min(max((least >> 7) - 1, 0) / 30, last);             // (a chunk of zeros meets its scale codes all the same)
+    }
+    float out[4] = {0.f, 0.f, 0.f, 0.f};
+    for (; band <= last; ++band) {
+        const uint32_t base = (uint32_t)(30 * band) * 0x00800080u, from = base + 0x00800080u, to = base + 31 * 0x00800080u;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int i = 0; i < BLOCKS; ++i) {
+            const uint4 v = load_x(i);
+            uint32_t b[4] = {v.x, v.y, v.z, v.w};
+            if (BF16) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a = b[k] & 0x7FFF7FFFu, sign = b[k] & 0x80008000u;
+                    uint32_t in = band == 8 ? less2(a, 0x7F807F80u) : less2(a, to);
+                    if (band != 0) in &= ~less2(a, from);
+                    b[k] = sign | ((max_u16x2(a, base) - base) & in) << 3;
+                    if (special) {
+                        if ((a >> 16) >= 0x7F80u) b[k] |= (a >> 16) > 0x7F80u ? 0x7E000000u : 0x7C000000u;
+                        if ((a & 0xFFFFu) >= 0x7F80u) b[k] |= (a & 0xFFFFu) > 0x7F80u ? 0x7E00u : 0x7C00u;
+                    }
+                }
+            }
+            uint32_t q[4], h[2][4];                      // words of columns g and g + 8 in the even block, then the odd one
+            matrices(w + (lane & 15) * 128 + ((((i & ~1) + (lane >> 4)) ^ lane) & 7) * 16, q);
+            int code[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                e2m1x8(i & 1 ? q[2 + r] : q[r], h[r]);
+                const uint32_t at = w + W_BYTES + (g + 8 * r) * SF_STRIDE<MODE, ALIGNED> + (ALIGNED ? 0 : (r ? shift.y : shift.x) / 8);
+                if (MODE == GEMM_SCALE_UE8M0_32) {
+                    code[r] = (int)load_shared_u8(at + i);
+                } else {
+                    const uint32_t c = load_shared_u8(at + 2 * i + t / 2) & 0x7Fu, f = ue4m3x2(c * 0x0101u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[r][e] = mul2(h[r][e], f);
+                }
+            }
+            if (MODE == GEMM_SCALE_UE8M0_32) {
+                float acc[4];
+                mma_16816_zero(acc, h[0][0], h[1][0], h[0][1], h[1][1], b[0], b[1]);
+                mma_16816(acc, h[0][2], h[1][2], h[0][3], h[1][3], b[2], b[3]);
+                const int e = (BF16 ? 30 * band - 112 : 0) - 127;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    out[k] += code[k / 2] == 255 ? __uint_as_float(0x7FC00000u) : times_power(acc[k], e + code[k / 2]);
+            } else {
+                mma_16816(sum, h[0][0], h[1][0], h[0][1], h[1][1], b[0], b[1]);
+                mma_16816(sum, h[0][2], h[1][2], h[0][3], h[1][3], b[2], b[3]);
+            }
+        }
+        special = false;
+        if (MODE != GEMM_SCALE_UE8M0_32)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) out[k] += times_power(sum[k], BF16 ? 30 * band - 112 : 0);
+    }
+    if (!FEW) return make_float4(out[0], out[1], out[2], out[3]);
+    float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {                        // row t is lane t / 2's
+        const float v = __shfl_sync(0xFFFFFFFFu, out[k], g * 4 + t / 2);
+        if (t < p.M && (t & 1) == (k & 1)) (k < 2 ? d.x : d.z) = v;
+    }
+    return d;
+}
+
+// Rows of X in shared memory: forms 8 and 16 have zeros where X has no row
+__host__ __device__ constexpr int x_rows(int form, int M) { return form > 4 ? form : M; }
 
 // The CTA's chunks [lo, hi) of X into shared memory as the MMA's B operand: row by row, k ascending; lane (g, t) reads
 // the eight k of 32 i + 8 t as one 128-bit word.  A row's stride is 64 bytes past a multiple of 128, so that two rows'
@@ -640,7 +703,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             if ((SCALED_X || MODE == GEMM_SCALE_UE8M0_32) && !__all_sync(0xFFFFFFFFu, fine)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float4 add = products_64<XT, MODE, FEW>(p, n0, ch, nt * 8);
+                    const float4 add = products_by_band<XT, MODE, FEW, ALIGNED>(p, w, make_uint2(shift[0], shift[1]), ch, nt * 8);
                     total[nt][0] += add.x;
                     total[nt][1] += add.y;
                     total[nt][2] += add.z;
