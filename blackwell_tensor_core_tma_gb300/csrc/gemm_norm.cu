@@ -98,7 +98,8 @@ struct NormParams {
 // One row per group of threads (threadIdx.y): all of its loads are requested before the first is used.
 // Bound by memory: x and r in, h, y and the scales out, once each.  8192 x 8192, bf16 with residual to e4m3: 71.9 us,
 // 6565 GB/s (97% of a copy's rate); with the rows ahead in a ring in shared memory it took longer.  1 x 4096: 1.7 us, a
-// launch, a trip to memory and the row's sum.
+// launch, a trip to memory and the row's sum.  Without residual and h an element moves half the bytes, and issue slots bound
+// it (86%): 32768 x 2048, bf16 to e4m3 52.5 us, 3880 GB/s (57%).
 template <typename XT, typename HT, typename YT, int U>
 __global__ void __launch_bounds__(U == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int N = UNIT, PX = PIECES<XT, N>, PH = PIECES<HT, N>;
@@ -260,7 +261,9 @@ __device__ __forceinline__ float published_sum(const uint64_t *sums, uint32_t ro
 // A CTA walks rows (rpc at a time) with w and dw in registers; a row costs one barrier, that of its sum.
 // Bound by memory: dy, h and dh in, dx (and y) out, once each; then dw's join, 3.5 us that no row's bytes overlap.
 // 4096 x 8192, bf16 with y again: 56.9 us, 5895 GB/s (87% of a copy's rate; the rows alone at 97%).  333 x 2064, fp32:
-// 7.1 us, two kernels one after the other with a trip to memory each.
+// 7.1 us, two kernels one after the other with a trip to memory each.  Rows of few elements run at a copy's rate, behind
+// 5.8 us for the first rows' trip and the last rows' outputs: 16384 x 512, bf16 with y again 20.7 us (18.0 without dw, floor
+// 12.4), 65536 x 512 56.9 us (54.4, floor 49.5).
 // SPLIT: a row is the work of a cluster, a share of its columns each.  Its sum then takes longer than a row's bytes should, so the
 // row before is finished meanwhile, for which dy and h are read from the ring once more.
 template <typename GT, typename HT, typename YT, int U, bool SPLIT>
@@ -545,7 +548,8 @@ template <typename XT, typename HT, typename YT>
 cudaError_t norm_launch(int sms, const NormParams &p, cudaStream_t stream) {
     // Few rows: as many threads as there are units, for the shortest chain.  Many: two units per thread, so that
     // a thread has twice the bytes in flight and half as many warps meet at the barrier (16384 x 4096, bf16 to e4m3: 70.0 us
-    // with two, 79.8 with one; 8192 x 2048 without residual: 15.8 and 18.6; at 1024 columns and below the two are equal).
+    // with two, 79.8 with one; bf16 to e4m3 without residual at 8192 x 2048: 15.4 and 18.3; at 1024 columns and below the two
+    // are equal).
     const int units = p.K / UNIT;
     const RowShape s = row_shape(units, units <= (p.M <= 2 * sms ? 512 : 128) ? 1 : units <= 1024 ? 2 : 4);
     const dim3 block(s.tpr, s.rpc);

@@ -332,7 +332,8 @@ gemm_status gemm_chain_run_host(gemm_plan_t p, const void *A, const void *B, con
  * Where an output is GEMM_E4M3, it is the A operand of a GEMM_SCALE_UE8M0_32 plan and its scale
  * codes are that plan's SFA: per row, each 32 consecutive elements (the last block of a row may be
  * short) share the code c = the smallest c >= 0 with max |v| <= 448 * 2^(c - 127), and an
- * element is v / 2^(c - 127) rounded to nearest even.  No finite element saturates.  An infinite
+ * element is v / 2^(c - 127) rounded to nearest even.  No finite element saturates (from 248 * 2^120 on it rounds to 2^128,
+ * which is past fp32 when decoded there).  An infinite
  * element makes its block decode to infinity at that element (448 * 2^120 exceeds fp32) and to zero at
  * finite ones below 2^110; a NaN element becomes the NaN code and does not touch its block's scale.
  */
