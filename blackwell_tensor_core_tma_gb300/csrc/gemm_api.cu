@@ -135,6 +135,10 @@ const ScaledFamily &scaled_family(int family) {
     return family == KIND_MXF4 ? family_mxf4() : (family == KIND_NVF4 ? family_nvf4() : family_mxf8());
 }
 
+// gemm_run's own plans; the chain's and the gated product's have entry points of their own
+bool is_product(const gemm_plan *p) { return p->family <= KIND_NVF4; }
+bool is_gated(const gemm_plan *p) { return p->family == FAMILY_GATED || p->family == FAMILY_GATED_BACK; }
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // 2-D row-major tensor [outer][inner] with a box of box_outer x box_inner elements; `promo`
@@ -149,6 +153,21 @@ bool encode_2d(CUtensorMap *m, CUtensorMapDataType dt, int ebytes, const void *p
     cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(m, dt, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           sw, promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// 3-D tensor [outer][planes][inner], rows of `inner` elements one behind the other in the order of
+// strides given in bytes; a box of box_inner elements of box_planes planes and box_outer rows
+bool encode_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *ptr, uint64_t inner, uint64_t mid, uint64_t outer,
+               uint64_t mid_stride, uint64_t outer_stride, uint32_t box_inner, uint32_t box_mid, uint32_t box_outer,
+               CUtensorMapSwizzle sw) {
+    if (!encoder()) return false;
+    cuuint64_t dims[3] = {inner, mid, outer};
+    cuuint64_t strides[2] = {mid_stride, outer_stride};
+    cuuint32_t box[3] = {box_inner, box_mid, box_outer};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(m, dt, 3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
@@ -544,7 +563,7 @@ gemm_status gemm_plan_create(gemm_plan_t *out, int64_t M, int64_t N, int64_t K, 
 
 gemm_status gemm_run(gemm_plan_t p, const void *A, const void *B, const void *C, void *D, const uint8_t *SFA,
                      const uint8_t *SFB, void *cuda_stream) {
-    if (!p || !A || !B || !D || p->family == FAMILY_CHAIN) return GEMM_ERR_INVALID_ARG;
+    if (!p || !A || !B || !D || !is_product(p)) return GEMM_ERR_INVALID_ARG;
     if (p->family != KIND_F16 && (!SFA || !SFB)) return GEMM_ERR_INVALID_ARG;
     if (!aligned16(A) || !aligned16(B) || !aligned16(D) || (C && !aligned16(C))) return GEMM_ERR_ALIGNMENT;
     gemm_status st = encode_maps(p, A, B, C, D);
@@ -746,7 +765,7 @@ gemm_status run_host_pipelined(gemm_plan *p, const void *A, const void *B, const
 
 gemm_status gemm_run_host(gemm_plan_t p, const void *A, const void *B, const void *C, void *D, const uint8_t *SFA,
                           const uint8_t *SFB, void *cuda_stream) {
-    if (!p || !A || !B || !D || p->family == FAMILY_CHAIN) return GEMM_ERR_INVALID_ARG;
+    if (!p || !A || !B || !D || !is_product(p)) return GEMM_ERR_INVALID_ARG;
     const size_t a_bytes = bytes_of(p->ab, p->M * p->K);
     const size_t b_bytes = bytes_of(p->ab, p->K * p->N);
     const size_t c_bytes = (size_t)p->M * p->N * 4;
@@ -812,7 +831,7 @@ gemm_status gemm_plan_get_info(gemm_plan_t p, gemm_plan_info *info) {
     info->tiles = p->tiles;
     info->smem_bytes = p->smem;
     // block-scaled plans also launch the scale-packing kernel, split-K plans the D = C kernel
-    const bool scaled = p->family != KIND_F16 && p->family != FAMILY_CHAIN;
+    const bool scaled = p->block_scaled != GEMM_SCALE_NONE;
     info->launches_per_run = (scaled ? 2 : 1) + (p->splits > 1 ? 1 : 0);
     info->splits = p->splits;
     info->stream_k = p->sk;
@@ -828,7 +847,7 @@ gemm_status gemm_plan_set_timeout(gemm_plan_t p, uint64_t ns) {
 
 gemm_status gemm_plan_set_split_k(gemm_plan_t p, int splits) {
     if (!p || splits < 0) return GEMM_ERR_INVALID_ARG;
-    if (p->family == FAMILY_CHAIN) return splits > 1 ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
+    if (!is_product(p)) return splits > 1 ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
     if (splits > 1 && (p->d != GEMM_F32 || (p->flags & GEMM_FLAG_DETERMINISTIC))) return GEMM_ERR_UNSUPPORTED;
     p->split_request = splits;
     return choose_splits(p);
@@ -836,6 +855,7 @@ gemm_status gemm_plan_set_split_k(gemm_plan_t p, int splits) {
 
 gemm_status gemm_plan_set_stream_k(gemm_plan_t p, int enable) {
     if (!p || enable < 0 || enable > 1) return GEMM_ERR_INVALID_ARG;
+    if (is_gated(p)) return enable ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
     p->sk_request = enable;
     if (p->family == FAMILY_CHAIN) return choose_chain_schedule(p);
     return choose_splits(p);
@@ -1041,6 +1061,204 @@ gemm_status gemm_chain_run_host(gemm_plan_t p, const void *A, const void *B, con
     return gemm_plan_last_status(p);
 }
 
+// --------------------------------------------------- the product with the gated unit
+
+namespace {
+
+GatedForm gated_form(const gemm_plan *p) {
+    return p->family == FAMILY_GATED_BACK ? GATED_BACK : (p->block_scaled ? GATED_MXF8 : GATED_F16);
+}
+
+// The plan of either direction: A is M x F, the product's sums run over K
+gemm_status gated_plan_create(gemm_plan_t *out, int family, int64_t M, int64_t F, int64_t K, gemm_dtype ab, gemm_dtype a,
+                              int block_scaled, unsigned flags) {
+    int dev = 0;
+    cudaDeviceProp prop;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaGetDeviceProperties(&prop, dev) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    if (prop.major != 10 || prop.minor != 3) return GEMM_ERR_UNSUPPORTED;
+
+    gemm_plan *p = new (std::nothrow) gemm_plan();
+    if (!p) return GEMM_ERR_CUDA;
+    p->M = M;
+    p->N = F;
+    p->K = K;
+    p->ab = ab;
+    p->c = GEMM_F32;
+    p->d = a;
+    p->block_scaled = block_scaled;
+    p->b_mn = family == FAMILY_GATED_BACK;
+    p->flags = flags;
+    p->device = dev;
+    p->sm_count = prop.multiProcessorCount;
+    p->timeout_ns = 1000000000ull;
+    p->family = family;
+    p->splits = 1;
+    const GatedForm form = gated_form(p);
+    int cg = M >= 1024 && F >= 512 ? 2 : 1;
+    if (flags & GEMM_FLAG_FORCE_1CTA) cg = 1;
+    if (flags & GEMM_FLAG_FORCE_2CTA) cg = 2;
+    int units = 0;
+    if (gated_prepare(form, cg, &units) != cudaSuccess || units <= 0) {
+        delete p;
+        return GEMM_ERR_CUDA;
+    }
+    const GatedShape sh = gated_shape(form, cg);
+    p->cta_group = cg;
+    p->stages = sh.stages;
+    p->smem = sh.smem;
+    p->tile_n = sh.tile_n;
+    p->tile_k = sh.bk;
+    p->num_kb = (int)((K + sh.bk - 1) / sh.bk);
+    p->tiles_m = (int)((M + TILE_M * cg - 1) / (TILE_M * cg));
+    p->tiles_n = (int)((F + sh.tile_n - 1) / sh.tile_n);
+    p->tiles = p->tiles_m * p->tiles_n;
+    p->capacity = units;
+    p->grid = cg * (p->tiles < units ? p->tiles : units);
+    p->group_m = cg == 2 ? GB300_GROUP_M_PAIRS : GB300_GROUP_M_SINGLE;
+    bool ok = cudaMalloc(&p->status, sizeof(int)) == cudaSuccess &&
+              cudaMemset(p->status, 0, sizeof(int)) == cudaSuccess;
+    if (ok && block_scaled) {             // the packed scales of every (128 rows, stage) and (tile column, stage)
+        const size_t a_bytes = (size_t)p->tiles_m * cg * p->num_kb * sh.sfa_bytes;
+        const size_t b_bytes = (size_t)p->tiles_n * p->num_kb * sh.sfb_bytes;
+        ok = cudaMalloc(&p->ws_a, a_bytes) == cudaSuccess && cudaMalloc(&p->ws_b, b_bytes) == cudaSuccess &&
+             encode_2d(&p->maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p->ws_a, 128, a_bytes / 128, 128,
+                       (uint32_t)(sh.sfa_bytes / 128), CU_TENSOR_MAP_SWIZZLE_NONE) &&
+             encode_2d(&p->maps[3], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p->ws_b, 128, b_bytes / 128, 128,
+                       (uint32_t)(sh.sfb_bytes / 128), CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
+    if (!ok) {
+        gemm_plan_destroy(p);
+        return GEMM_ERR_CUDA;
+    }
+    *out = p;
+    return GEMM_OK;
+}
+
+// Tensor maps of a run: X, W, A and the checkpoint; backward DY, W2, A and DZ
+gemm_status encode_gated_maps(gemm_plan *p, const void *X, const void *W, const void *A, const void *Z) {
+    if (p->maps_valid && X == p->lastA && W == p->lastB && A == p->lastD && Z == p->lastC) return GEMM_OK;
+    p->maps_valid = false;
+    const bool back = p->family == FAMILY_GATED_BACK;
+    const CUtensorMapDataType ab = tma_dtype(p->ab);
+    const uint64_t eb = (uint64_t)elem_bits(p->ab) / 8, M = (uint64_t)p->M, F = (uint64_t)p->N, K = (uint64_t)p->K;
+    const uint32_t bk = 128u / (uint32_t)eb, hn = (uint32_t)p->tile_n;
+    bool ok = encode_2d(&p->maps[0], ab, (int)eb, X, K, M, bk, TILE_M, CU_TENSOR_MAP_SWIZZLE_128B);
+    ok = ok && (back ? encode_2d(&p->maps[1], ab, (int)eb, W, F, K, bk, bk, CU_TENSOR_MAP_SWIZZLE_128B)
+                     : encode_3d(&p->maps[1], ab, W, K, F, 2, K * eb, F * K * eb, bk, hn, 1, CU_TENSOR_MAP_SWIZZLE_128B));
+    // outputs leave by boxes of 32 x 32, rows of 64 (16-bit) or 32 (8-bit) bytes swizzled over the row
+    const int a_bytes = elem_bits(p->d) / 8;
+    const CUtensorMapSwizzle sw = a_bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+    if (ok && A) ok = encode_2d(&p->maps[4], tma_dtype(p->d), a_bytes, A, F, M, EPI_COLS, 32, sw);
+    const uint64_t zb = back ? 2 : 1;
+    if (ok && Z)
+        ok = encode_3d(&p->maps[5], back ? ab : CU_TENSOR_MAP_DATA_TYPE_UINT8, Z, F, 2, M, F * zb, 2 * F * zb, EPI_COLS, 1, 32,
+                       back ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+    if (!ok) return GEMM_ERR_CUDA;
+    p->lastA = X;
+    p->lastB = W;
+    p->lastD = A;
+    p->lastC = Z;
+    p->maps_valid = true;
+    return GEMM_OK;
+}
+
+gemm_status gated_launch_plan(gemm_plan *p, GatedParams &gp, cudaStream_t stream) {
+    const GatedForm form = gated_form(p);
+    gp.M = (int)p->M;
+    gp.F = (int)p->N;
+    gp.tiles_m = p->tiles_m;
+    gp.tiles_n = p->tiles_n;
+    gp.num_tiles = p->tiles;
+    gp.num_kb = p->num_kb;
+    gp.group_m = p->group_m;
+    gp.out16 = p->d;
+    const uint32_t m = (uint32_t)(TILE_M * p->cta_group), n = (uint32_t)(form == GATED_BACK ? p->tile_n : 2 * p->tile_n);
+    gp.idesc = form == GATED_MXF8 ? idesc_mxf8(m, n, 0, 0)
+                                  : idesc_f16(p->ab == GEMM_BF16 ? 1u : 0u, m, n) | ((uint32_t)p->b_mn << 16);
+    gp.status = p->status;
+    gp.timeout_ns = p->timeout_ns;
+    gp.fault = p->fault;
+    if (gated_launch(form, p->cta_group, p->grid, p->maps, gp, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+    if (p->flags & GEMM_FLAG_SYNC) {
+        if (cudaStreamSynchronize(stream) != cudaSuccess) return GEMM_ERR_CUDA;
+        return gemm_plan_last_status(p);
+    }
+    return GEMM_OK;
+}
+
+gemm_status gated_sizes(gemm_plan_t *out, int64_t M, int64_t F, int64_t K, unsigned flags) {
+    if (!out || M <= 0 || F <= 0 || K <= 0) return GEMM_ERR_INVALID_ARG;
+    if (M > INT32_MAX || F > (1 << 20) || K > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+    // tiles and the rows of packed scales are counted in 32 bits
+    if ((M + TILE_M) / TILE_M * ((F + 63) / 64) > INT32_MAX || (M + TILE_M) / TILE_M * (K / 32 + 1) > INT32_MAX)
+        return GEMM_ERR_INVALID_ARG;
+    if ((flags & GEMM_FLAG_FORCE_1CTA) && (flags & GEMM_FLAG_FORCE_2CTA)) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+}  // namespace
+
+gemm_status gemm_gated_plan_create(gemm_plan_t *out, int64_t M, int64_t F, int64_t K, gemm_dtype ab, gemm_dtype a,
+                                   int block_scaled, unsigned flags) {
+    gemm_status st = gated_sizes(out, M, F, K, flags);
+    if (st != GEMM_OK) return st;
+    if ((unsigned)ab > GEMM_E2M1 || (unsigned)a > GEMM_E2M1) return GEMM_ERR_INVALID_ARG;
+    if (block_scaled < GEMM_SCALE_NONE || block_scaled > GEMM_SCALE_UE4M3_16) return GEMM_ERR_INVALID_ARG;
+    const bool plain = (ab == GEMM_F16 || ab == GEMM_BF16) && block_scaled == GEMM_SCALE_NONE;
+    if (!plain && !(ab == GEMM_E4M3 && block_scaled == GEMM_SCALE_UE8M0_32)) return GEMM_ERR_UNSUPPORTED;
+    if (a != GEMM_E4M3 && a != GEMM_BF16 && a != GEMM_F16) return GEMM_ERR_UNSUPPORTED;
+    if (F % 16 != 0 || K * elem_bits(ab) % 128 != 0) return GEMM_ERR_ALIGNMENT;
+    return gated_plan_create(out, FAMILY_GATED, M, F, K, ab, a, block_scaled, flags);
+}
+
+gemm_status gemm_gated_run(gemm_plan_t p, const void *X, const void *W, const uint8_t *SFX, const uint8_t *SFW, void *A,
+                           uint8_t *SFA, uint8_t *CK, uint8_t *SFCK, void *cuda_stream) {
+    if (!p || p->family != FAMILY_GATED || !X || !W || !A) return GEMM_ERR_INVALID_ARG;
+    if ((p->block_scaled && (!SFX || !SFW)) || (p->d == GEMM_E4M3 && !SFA) || (CK && !SFCK)) return GEMM_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(W) || !aligned16(A) || (CK && !aligned16(CK))) return GEMM_ERR_ALIGNMENT;
+    gemm_status st = encode_gated_maps(p, X, W, A, CK);
+    if (st != GEMM_OK) return st;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
+    if (p->block_scaled) {
+        const int sfk = (int)((p->K + 31) / 32);
+        if (sf_pack(SFX, SFW, p->ws_a, p->ws_b, (int)p->M, (int)(2 * p->N), sfk, p->tiles_m * p->cta_group, p->tiles_n,
+                    2 * p->tile_n, p->num_kb, unit_scale(KIND_MXF8), stream, p->tile_n, (int)p->N) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+    }
+    GatedParams gp{};
+    gp.has_a = 1;
+    gp.has_z = CK != nullptr;
+    gp.a_8bit = p->d == GEMM_E4M3;
+    gp.sfa = SFA;
+    gp.sfck = SFCK;
+    return gated_launch_plan(p, gp, stream);
+}
+
+gemm_status gemm_gated_back_plan_create(gemm_plan_t *out, int64_t M, int64_t F, int64_t N, gemm_dtype ab, unsigned flags) {
+    gemm_status st = gated_sizes(out, M, F, N, flags);
+    if (st != GEMM_OK) return st;
+    if ((unsigned)ab > GEMM_E2M1) return GEMM_ERR_INVALID_ARG;
+    if (ab != GEMM_F16 && ab != GEMM_BF16) return GEMM_ERR_UNSUPPORTED;
+    if (F % 16 != 0 || N % 8 != 0) return GEMM_ERR_ALIGNMENT;
+    return gated_plan_create(out, FAMILY_GATED_BACK, M, F, N, ab, ab, GEMM_SCALE_NONE, flags);
+}
+
+gemm_status gemm_gated_back_run(gemm_plan_t p, const void *DY, const void *W2, const uint8_t *CK, const uint8_t *SFCK,
+                                void *DZ, void *A, void *cuda_stream) {
+    if (!p || p->family != FAMILY_GATED_BACK || !DY || !W2 || !CK || !SFCK || !DZ) return GEMM_ERR_INVALID_ARG;
+    if (!aligned16(DY) || !aligned16(W2) || !aligned16(CK) || !aligned16(DZ) || (A && !aligned16(A)))
+        return GEMM_ERR_ALIGNMENT;
+    gemm_status st = encode_gated_maps(p, DY, W2, A, DZ);
+    if (st != GEMM_OK) return st;
+    GatedParams gp{};
+    gp.has_a = A != nullptr;
+    gp.has_z = 1;
+    gp.ck = CK;
+    gp.sfck_in = SFCK;
+    return gated_launch_plan(p, gp, reinterpret_cast<cudaStream_t>(cuda_stream));
+}
+
 // Test hook (declared in include/gb300gemm_testing.h): the pair tile-width rule alone.
 gemm_status gemm_testing_pair_tile_n(int64_t M, int64_t N, int64_t K, gemm_dtype d, int units, int *tile_n) {
     if (!tile_n || M <= 0 || N <= 0 || K <= 0 || units <= 0 || (d != GEMM_F32 && d != GEMM_BF16))
@@ -1059,7 +1277,7 @@ gemm_status gemm_testing_e4m3_pair_tile_n(int64_t M, int64_t N, int64_t K, gemm_
 
 gemm_status gemm_plan_set_clock_meter(gemm_plan_t p, int enable) {
     if (!p || enable < 0 || enable > 1) return GEMM_ERR_INVALID_ARG;
-    if (p->family == FAMILY_CHAIN) return GEMM_ERR_UNSUPPORTED;
+    if (!is_product(p)) return GEMM_ERR_UNSUPPORTED;
     if (enable) {
         if (!p->clk_meter && cudaMalloc(&p->clk_meter, 2 * sizeof(unsigned long long)) != cudaSuccess) {
             p->clk_meter = nullptr;
@@ -1097,7 +1315,7 @@ int gemm_testing_trace_slots(void) { return GB300_TRACE ? (int)TRACE_SLOTS : 0; 
 
 gemm_status gemm_testing_set_trace(gemm_plan_t p, void *dev_buffer, int64_t bytes) {
     if (!p) return GEMM_ERR_INVALID_ARG;
-    if (!GB300_TRACE || p->family == FAMILY_CHAIN) return GEMM_ERR_UNSUPPORTED;
+    if (!GB300_TRACE || !is_product(p)) return GEMM_ERR_UNSUPPORTED;
     if (dev_buffer && bytes < (int64_t)p->grid * TRACE_SLOTS * (int64_t)sizeof(unsigned long long))
         return GEMM_ERR_INVALID_ARG;
     p->trace = static_cast<unsigned long long *>(dev_buffer);
@@ -1108,7 +1326,7 @@ gemm_status gemm_testing_set_trace(gemm_plan_t p, void *dev_buffer, int64_t byte
 // producer withhold one arrival so that a bounded wait runs out (1), or shift its A
 // rows past the tiled extent (2).
 gemm_status gemm_testing_set_fault(gemm_plan_t p, int fault) {
-    if (!p || fault < 0 || fault > 2 || (fault == 2 && p->family == FAMILY_CHAIN)) return GEMM_ERR_INVALID_ARG;
+    if (!p || fault < 0 || fault > 2 || (fault == 2 && !is_product(p))) return GEMM_ERR_INVALID_ARG;
     p->fault = fault;
     return GEMM_OK;
 }

@@ -1,0 +1,563 @@
+// The first product of a feed-forward block with its gated unit in one kernel, and the product
+// that enters the unit from behind with the unit's gradient (gemm_gated_run, gemm_gated_back_run
+// in include/gb300gemm.h):
+//
+//   forward    z = X·[Wg; Wu]ᵀ = [g | u],  a = g / (1 + exp(-g)) * u,  g and u kept in 8 bits
+//   backward   da = DY·W2,  [dg | du] from da and the kept g, u,  a again
+//
+// The roles are those of gemm_tc_kernel (gemm_kernel.cuh): a TMA producer warp, a warp with the
+// MMA issuing thread, scale-copying warps for block-scaled operands, epilogue warps.  What differs
+// is what a tile is and what its epilogue does:
+//
+//   * Forward: a tile's HN columns of A take 2 HN columns of the product, g's and then u's.  The
+//     weights are mapped as [2][F][K], so that a box of HN rows of either half is zero past F.  In a
+//     CTA pair the leader's half of the MMA's N is g's rows and its peer's u's, so that each CTA
+//     loads one box as in the plain product.  Both accumulators of an element are then in the
+//     same lane of tensor memory, HN columns apart: the unit needs no exchange between threads.
+//   * A thread owns a row; its chunk of 32 columns is one scale block of e4m3, so that a block's
+//     maximum is a thread's own.
+//   * Backward: B is N-contiguous (W2 as the forward product has it), g and u come as 8-bit codes
+//     straight from memory, one chunk ahead of their use, and dz and a leave through TMA boxes.
+//
+// No split-K: sums would meet before the unit.  Every wait is bounded as in gemm_tc_kernel.
+#pragma once
+
+#include "gemm_kernel.cuh"
+#include "gemm_rows.cuh"
+
+namespace gb300 {
+
+// Compile-time shape of one kernel instance: HN columns of A per tile; the rest as in TileCfg.
+template <int CG_, int KIND_, bool BACK_, int HN_, int STAGES_, int ACC_BUFS_, int EPI_WARPS_, int COPIERS_ = 0>
+struct GatedCfg {
+    static constexpr int CG = CG_;
+    static constexpr int KIND = KIND_;
+    static constexpr bool SCALED = KIND != KIND_F16;
+    static constexpr bool BACK = BACK_;
+    static constexpr int HN = HN_;
+    static constexpr int BN = BACK ? HN : 2 * HN;               // columns of the MMA
+    static constexpr int STAGES = STAGES_;
+    static constexpr int ACC_BUFS = ACC_BUFS_;
+    static constexpr int EPI_WARPS = EPI_WARPS_;
+    static constexpr int COPIERS = COPIERS_;
+    static constexpr bool COPIER = COPIERS > 0;
+    static constexpr int COPY_WARP = 2 + EPI_WARPS;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS + 32 * COPIERS;
+    static constexpr int WCOLS = HN * 4 / EPI_WARPS;            // columns of A one epilogue warp handles
+    static constexpr int WCHUNKS = WCOLS / EPI_COLS;
+    static constexpr int ELEM_BITS = KIND == KIND_F16 ? 16 : 8;
+    static constexpr int ELEM_BYTES = ELEM_BITS / 8;
+    static constexpr int BK = 1024 / ELEM_BITS;                 // K elements per stage: one 128-byte row
+    static constexpr int MMA_K = 256 / ELEM_BITS;
+    static constexpr int ATOM_MN = 1024 / ELEM_BITS;            // N elements of an N-contiguous operand's atom
+    static constexpr int ATOM_BYTES = BK * 128;
+    static constexpr int A_BYTES = TILE_M * 128;
+    static constexpr int B_ROWS = BN / CG;                      // B rows held by one CTA
+    static constexpr int B_BYTES = B_ROWS * 128;
+    static constexpr int SF_WORDS = SCALED ? BK / 32 / 4 : 0;
+    static constexpr int SF_PER_MMA = 1;
+    static constexpr int HALVES = (BN + 127) / 128;
+    static constexpr int SFA_BYTES = 512 * SF_WORDS;
+    static constexpr int SFB_BYTES = 512 * SF_WORDS * HALVES;
+    static constexpr int TX_AB = CG * (A_BYTES + B_BYTES);
+    static constexpr int TX_SF = CG * (SFA_BYTES + SFB_BYTES);
+    // an epilogue warp's staging: 32 rows of a chunk of each output (16-bit: 2 KiB, 8-bit: 1 KiB)
+    static constexpr int EPI_BUF = BACK ? 3 * 2048 : 2048 + 2 * 1024;
+    static constexpr int align1k(int x) { return (x + 1023) / 1024 * 1024; }
+    static constexpr int OFF_A = 0;
+    static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
+    static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
+    static constexpr int OFF_EPI = align1k(OFF_SF + STAGES * (SFA_BYTES + SFB_BYTES));
+    static constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_BUF;
+    // full[STAGES], empty[STAGES], tfull[2], tempty[2], drain, then with COPIER: cdrain, sffull[STAGES]
+    static constexpr int NBAR = 2 * STAGES + 5 + (COPIER ? STAGES + 1 : 0);
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;         // tmem base slot, abort flag
+    static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;     // + alignment slack
+    static constexpr int SF_SLOT = 4 * SF_WORDS * (1 + HALVES);
+    static constexpr int SF_COL0 = ACC_BUFS * BN;
+    static_assert(CG == 1 || CG == 2, "CTA group");
+    static_assert(KIND == KIND_F16 || KIND == KIND_MXF8, "operand kind");
+    static_assert(!BACK || KIND == KIND_F16, "the backward product has 16-bit operands");
+    static_assert(COPIER == SCALED, "block-scaled instances have copier warps");
+    static_assert(ACC_BUFS * BN + STAGES * SF_SLOT <= 512, "TMEM budget");
+    static_assert(SMEM_BYTES <= 232448, "shared-memory budget");
+    static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && EPI_BUF % 1024 == 0, "1024-byte regions");
+    static_assert(EPI_WARPS == 4 || EPI_WARPS == 8, "epilogue warps");
+    static_assert(WCOLS % EPI_COLS == 0 && HN % 64 == 0 && BN <= 256, "tile columns");
+    static_assert(ACC_BUFS == 1 || ACC_BUFS == 2, "accumulator buffers");
+};
+
+// 32 values of a row quantised as one scale block: codes to shared memory (32-byte row `lane` of a
+// 32-byte-swizzled box), the block's scale code returned
+__device__ __forceinline__ uint32_t quantise_chunk(const float (&v)[32], uint32_t box, int lane) {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));      // fmaxf drops NaN
+    const uint32_t code = rows::scale_code(amax);
+    const float inv = rows::scale_inverse(code);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float *x = v + 16 * c + 4 * i;
+            w[i] = rows::e4m3x2(x[0] * inv, x[1] * inv) | rows::e4m3x2(x[2] * inv, x[3] * inv) << 16;
+        }
+        st_shared_v4(box + swz_off<32>(lane, c), w[0], w[1], w[2], w[3]);
+    }
+    return code;
+}
+
+// 32 values of a row rounded to 16 bits: 64-byte row `lane` of a 64-byte-swizzled box
+__device__ __forceinline__ void round_chunk(const float (&v)[32], bool bf16, uint32_t box, int lane) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint4 q = bf16 ? rows::pack8(static_cast<const __nv_bfloat16 *>(nullptr), v + 8 * c)
+                             : rows::pack8(static_cast<const __half *>(nullptr), v + 8 * c);
+        st_shared_v4(box + swz_off<64>(lane, c), q.x, q.y, q.z, q.w);
+    }
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    gated_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ CUtensorMap tmSFX, const __grid_constant__ CUtensorMap tmSFW,
+                 const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmZ,
+                 const GatedParams p) {
+    constexpr int CG = Cfg::CG;
+    constexpr int STAGES = Cfg::STAGES;
+    constexpr int BN = Cfg::BN;
+    constexpr int HN = Cfg::HN;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR);
+    uint64_t *empty = full + STAGES;
+    uint64_t *tfull = empty + STAGES;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *drain = tempty + 2;
+    uint64_t *cdrain = drain + 1;                         // COPIER only
+    uint64_t *sffull = cdrain + 1;                        // COPIER only
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Cfg::OFF_MISC + 4);
+    const Waiter W{abort_flag, p.status, p.timeout_ns};
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tmX);
+        prefetch_tensormap(&tmW);
+        if constexpr (Cfg::SCALED) {
+            prefetch_tensormap(&tmSFX);
+            prefetch_tensormap(&tmSFW);
+        }
+        if (p.has_a) prefetch_tensormap(&tmA);
+        if (p.has_z) prefetch_tensormap(&tmZ);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1 + Cfg::COPIERS);        // the producer's arrival and each copier warp's commit
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], Cfg::EPI_WARPS * CG);
+        }
+        mbar_init(drain, 1);
+        if constexpr (Cfg::COPIER) {
+            for (int i = 0; i < STAGES; ++i) mbar_init(&sffull[i], 1);
+            mbar_init(cdrain, Cfg::COPIERS);
+        }
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(smem_addr(tmem_slot), 512);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before_sync();
+    if constexpr (CG == 2) cluster_sync(); else __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int tile0 = blockIdx.x / CG;
+    const int tile_step = gridDim.x / CG;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, round = 0;
+            bool ok = true;
+            for (int t = tile0; ok && t < p.num_tiles; t += tile_step, ++round) {
+                int tm, tn;
+                tile_coords(t, p.tiles_m, p.group_m, tm, tn, p.tiles_n);
+                const int m0 = (tm * CG + (int)rank) * TILE_M;
+                const int f0 = tn * HN;
+                for (int j = 0; j < p.num_kb; ++j) {
+                    const int kb = kb_at(j, 0, p.num_kb, round);
+                    if (!W.wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+                    const bool withhold = p.fault == 1 && round == 0 && j == 0;
+                    const uint32_t fb = smem_addr(&full[s]);
+                    const uint32_t bar = CG == 1 ? fb : mapa_shared(fb, 0);      // the leader's
+                    if constexpr (Cfg::SCALED) {          // the scales first: the copier warps start on them
+                        if (rank == 0) mbar_arrive_expect_tx(&sffull[s], Cfg::TX_SF);
+                        const uint32_t sb = smem_addr(&sffull[s]);
+                        const uint32_t sbar = CG == 1 ? sb : mapa_shared(sb, 0);
+                        const uint32_t dst = smem_addr(smem + Cfg::OFF_SF + s * (Cfg::SFA_BYTES + Cfg::SFB_BYTES));
+                        const int xr = checked_y(p.status, ((tm * CG + (int)rank) * p.num_kb + kb) * (Cfg::SFA_BYTES / 128),
+                                                 p.tiles_m * CG * p.num_kb * (Cfg::SFA_BYTES / 128));
+                        const int wr = checked_y(p.status, (tn * p.num_kb + kb) * (Cfg::SFB_BYTES / 128),
+                                                 p.tiles_n * p.num_kb * (Cfg::SFB_BYTES / 128));
+                        if constexpr (CG == 1) {
+                            tma_load_2d(dst, &tmSFX, sbar, 0, xr);
+                            tma_load_2d(dst + Cfg::SFA_BYTES, &tmSFW, sbar, 0, wr);
+                        } else {
+                            tma_load_2d_pair(dst, &tmSFX, sbar, 0, xr);
+                            tma_load_2d_pair(dst + Cfg::SFA_BYTES, &tmSFW, sbar, 0, wr);
+                        }
+                    }
+                    if (rank == 0 && !withhold) mbar_arrive_expect_tx(&full[s], Cfg::TX_AB);
+                    const uint32_t a_dst = smem_addr(smem + Cfg::OFF_A + s * Cfg::A_BYTES);
+                    const uint32_t b_dst = smem_addr(smem + Cfg::OFF_B + s * Cfg::B_BYTES);
+                    const int kx = checked_x<Cfg::ELEM_BYTES>(p.status, kb * Cfg::BK, p.num_kb * Cfg::BK);
+                    const int my = checked_y(p.status, m0, p.tiles_m * CG * TILE_M);
+                    if constexpr (CG == 1) tma_load_2d(a_dst, &tmX, bar, kx, my);
+                    else tma_load_2d_pair(a_dst, &tmX, bar, kx, my);
+                    if constexpr (Cfg::BACK) {            // W2 [N][F]: a box of 64 F x 64 N per atom column
+                        const int n0 = f0 + (int)rank * Cfg::B_ROWS;
+#pragma unroll
+                        for (int i = 0; i < Cfg::B_ROWS / Cfg::ATOM_MN; ++i) {
+                            const int x = checked_x<2>(p.status, n0 + i * Cfg::ATOM_MN, p.tiles_n * HN);
+                            const int y = checked_y(p.status, kb * Cfg::BK, p.num_kb * Cfg::BK);
+                            if constexpr (CG == 1) tma_load_2d(b_dst + i * Cfg::ATOM_BYTES, &tmW, bar, x, y);
+                            else tma_load_2d_pair(b_dst + i * Cfg::ATOM_BYTES, &tmW, bar, x, y);
+                        }
+                    } else {                              // W [2][F][K]: HN rows of each half
+                        const int fy = checked_y(p.status, f0, p.tiles_n * HN);
+                        if constexpr (CG == 1) {
+                            tma_load_3d(b_dst, &tmW, bar, kx, fy, 0);
+                            tma_load_3d(b_dst + HN * 128, &tmW, bar, kx, fy, 1);
+                        } else {
+                            tma_load_3d_pair(b_dst, &tmW, bar, kx, fy, (int)rank);
+                        }
+                    }
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ----------------------------------------------------------- MMA issue
+        if (rank == 0 && lane == 0) {
+            // descriptors as in gemm_tc_kernel: K-major operands step 32 bytes per MMA, an
+            // N-contiguous B MMA_K rows of 128 bytes
+            constexpr uint32_t B_LBO = Cfg::BACK ? Cfg::ATOM_BYTES : 16;
+            constexpr uint32_t B_STEP = Cfg::BACK ? (Cfg::MMA_K * 128) >> 4 : 2;
+            int s = 0;
+            uint32_t ph = 0, acc_it = 0;
+            bool ok = true;
+            for (int t = tile0; ok && t < p.num_tiles; t += tile_step, ++acc_it) {
+                const uint32_t b = Cfg::ACC_BUFS == 2 ? (acc_it & 1u) : 0u;
+                const uint32_t aph = Cfg::ACC_BUFS == 2 ? ((acc_it >> 1) & 1u) : (acc_it & 1u);
+                if (!W.wait<CG == 2>(&tempty[b], aph ^ 1u)) { ok = false; break; }
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + b * BN;
+                for (int j = 0; j < p.num_kb; ++j) {
+                    if (!W.wait(&full[s], ph)) { ok = false; break; }
+                    tc_fence_after_sync();
+                    const uint64_t ad = smem_desc(smem_addr(smem + Cfg::OFF_A + s * Cfg::A_BYTES), 16, 1024, SWZ_128B);
+                    const uint64_t bd = smem_desc(smem_addr(smem + Cfg::OFF_B + s * Cfg::B_BYTES), B_LBO, 1024, SWZ_128B);
+                    if constexpr (Cfg::SCALED) {
+                        const uint32_t sfa_t = tmem_base + Cfg::SF_COL0 + s * Cfg::SF_SLOT;
+                        const uint32_t sfb_t = sfa_t + 4 * Cfg::SF_WORDS;
+#pragma unroll
+                        for (int k = 0; k < Cfg::BK / Cfg::MMA_K; ++k) {
+                            const uint32_t w = (uint32_t)k / 4u, id = (uint32_t)k % 4u;
+                            mma_scaled<Cfg::KIND, CG>(d_tmem, ad + 2 * k, bd + 2 * k, p.idesc | (id << 4) | (id << 29),
+                                                      sfa_t + 4 * w, sfb_t + 4 * Cfg::HALVES * w, (j != 0) | (k != 0));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < Cfg::BK / Cfg::MMA_K; ++k)
+                            mma_f16<CG>(d_tmem, ad + 2 * k, bd + B_STEP * k, p.idesc, (j != 0) | (k != 0));
+                    }
+                    if constexpr (CG == 1) tc_commit<1>(smem_addr(&empty[s]));
+                    else tc_commit_pair(smem_addr(&empty[s]), 0x3);
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
+                }
+                if (!ok) break;
+                if constexpr (CG == 1) tc_commit<1>(smem_addr(&tfull[b]));
+                else tc_commit_pair(smem_addr(&tfull[b]), 0x3);
+            }
+            // every MMA this thread issued has finished before teardown
+            tc_commit<CG>(smem_addr(drain));
+            W.wait(drain, 0, false);
+        }
+    } else if (Cfg::COPIER && warp >= Cfg::COPY_WARP) {
+        // ---------------------------------------------------------- scale copies
+        if constexpr (Cfg::COPIER) {
+            if (rank == 0 && lane == 0) {
+                int s = 0;
+                uint32_t ph = 0;
+                bool ok = true;
+                for (int t = tile0; ok && t < p.num_tiles; t += tile_step) {
+                    for (int j = 0; j < p.num_kb; ++j) {
+                        if (!W.wait(&sffull[s], ph)) { ok = false; break; }
+                        tc_fence_after_sync();
+                        const uint32_t sfa_t = tmem_base + Cfg::SF_COL0 + s * Cfg::SF_SLOT;
+                        copy_scales<Cfg, Cfg::COPIERS>(smem, s, sfa_t, sfa_t + 4 * Cfg::SF_WORDS, warp - Cfg::COPY_WARP);
+                        if constexpr (CG == 1) tc_commit<1>(smem_addr(&full[s]));
+                        else tc_commit_pair(smem_addr(&full[s]), 0x1);
+                        if (++s == STAGES) { s = 0; ph ^= 1u; }
+                    }
+                }
+                if constexpr (CG == 1) tc_commit<1>(smem_addr(cdrain));
+                else tc_commit_pair(smem_addr(cdrain), 0x1);
+                W.wait(cdrain, 0, false);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int e = warp - 2;
+        const int q = warp & 3;                           // TMEM lane window of this warp
+        const int h = e / 4;                              // which WCOLS-wide slice of the tile's columns
+        const uint32_t box = smem_addr(smem + Cfg::OFF_EPI + e * Cfg::EPI_BUF);
+        const uint64_t stream_pol = l2_policy_evict_first();
+        const int blocks = (p.F + rows::BLOCK - 1) / rows::BLOCK;
+        const bool bf16 = p.out16 == GEMM_BF16;
+        uint32_t acc_it = 0;
+        // hand accumulator b back to the MMA (all 32 lanes have read it)
+        auto release = [&](uint32_t b) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 1) mbar_arrive(&tempty[b]);
+                else mbar_arrive_remote(mapa_shared(smem_addr(&tempty[b]), 0));
+            }
+        };
+        for (int t = tile0; t < p.num_tiles; t += tile_step, ++acc_it) {
+            int tm, tn;
+            tile_coords(t, p.tiles_m, p.group_m, tm, tn, p.tiles_n);
+            const uint32_t b = Cfg::ACC_BUFS == 2 ? (acc_it & 1u) : 0u;
+            const uint32_t aph = Cfg::ACC_BUFS == 2 ? ((acc_it >> 1) & 1u) : (acc_it & 1u);
+            const int m_warp = (tm * CG + (int)rank) * TILE_M + 32 * q;
+            const int f_warp = tn * HN + h * Cfg::WCOLS;
+            const int row = m_warp + lane;
+            const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + b * BN + h * Cfg::WCOLS;
+            // chunks with a column of the matrix; none where the warp's rows are all past M
+            const int chunks = m_warp < p.M ? max(0, min(Cfg::WCHUNKS, (p.F - f_warp + EPI_COLS - 1) / EPI_COLS)) : 0;
+
+            // the staging is free again once the last chunk's boxes have been read
+            auto begin_boxes = [&]() {
+                if (lane == 0) bulk_wait_group_read0();
+                __syncwarp();
+            };
+            auto end_boxes = [&]() {
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+
+            if constexpr (!Cfg::BACK) {
+                auto finish = [&](int c, const uint32_t (&gr)[32], const uint32_t (&ur)[32]) {
+                    if (c >= chunks) return;
+                    const int f = f_warp + EPI_COLS * c;
+                    float g[32], u[32], a[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        g[i] = __uint_as_float(gr[i]);
+                        u[i] = __uint_as_float(ur[i]);
+                        float s1, s0;
+                        rows::sigmoid(g[i], s1, s0);
+                        a[i] = g[i] * s1 * u[i];
+                    }
+                    begin_boxes();
+                    const int64_t block = (int64_t)row * blocks + f / rows::BLOCK;
+                    if (p.a_8bit) {
+                        const uint32_t code = quantise_chunk(a, box, lane);
+                        if (row < p.M) p.sfa[block] = (uint8_t)code;
+                    } else {
+                        round_chunk(a, bf16, box, lane);
+                    }
+                    if (p.has_z) {
+                        const uint32_t cg = quantise_chunk(g, box + 2048, lane), cu = quantise_chunk(u, box + 3072, lane);
+                        if (row < p.M) {
+                            uint8_t *sf = p.sfck + (block + (int64_t)row * blocks);
+                            sf[0] = (uint8_t)cg;
+                            sf[blocks] = (uint8_t)cu;
+                        }
+                    }
+                    end_boxes();
+                    if (lane == 0) {
+                        const int x = checked_x<1>(p.status, f, p.F), y = checked_y(p.status, m_warp, p.M);
+                        tma_store_2d_hint(&tmA, box, x, y, stream_pol);
+                        if (p.has_z) {
+                            tma_store_3d_hint(&tmZ, box + 2048, x, 0, y, stream_pol);
+                            tma_store_3d_hint(&tmZ, box + 3072, x, 1, y, stream_pol);
+                        }
+                        bulk_commit_group();
+                    }
+                };
+                if (!__all_sync(0xffffffffu, W.wait(&tfull[b], aph))) break;
+                tc_fence_after_sync();
+                if constexpr (Cfg::ACC_BUFS == 1) {
+                    // the whole slice to registers first, so that the MMA can start the next tile
+                    uint32_t g[Cfg::WCHUNKS][32], u[Cfg::WCHUNKS][32];
+#pragma unroll
+                    for (int c = 0; c < Cfg::WCHUNKS; ++c) {
+                        tmem_ld_32x32b_x32(taddr + EPI_COLS * c, g[c]);
+                        tmem_ld_32x32b_x32(taddr + HN + EPI_COLS * c, u[c]);
+                    }
+                    tmem_ld_wait_all();
+#pragma unroll
+                    for (int c = 0; c < Cfg::WCHUNKS; ++c) {
+                        tie_registers(g[c]);
+                        tie_registers(u[c]);
+                    }
+                    release(b);
+#pragma unroll
+                    for (int c = 0; c < Cfg::WCHUNKS; ++c) finish(c, g[c], u[c]);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < Cfg::WCHUNKS; ++c) {
+                        uint32_t g[32], u[32];
+                        tmem_ld_32x32b_x32(taddr + EPI_COLS * c, g);
+                        tmem_ld_32x32b_x32(taddr + HN + EPI_COLS * c, u);
+                        tmem_ld_wait(g);
+                        tie_registers(u);
+                        if (c == Cfg::WCHUNKS - 1) release(b);
+                        finish(c, g, u);
+                    }
+                }
+            } else {
+                // codes and scales of a chunk's g and u; zeros past the matrix
+                struct Kept {
+                    uint4 g[2], u[2];
+                    uint32_t sg, su;
+                };
+                auto fetch = [&](int c) {
+                    Kept k{};
+                    const int f = f_warp + EPI_COLS * c;
+                    if (c < chunks && row < p.M) {
+                        const uint8_t *ck = p.ck + (int64_t)row * 2 * p.F + f;
+                        const uint8_t *sf = p.sfck_in + (int64_t)row * 2 * blocks + f / rows::BLOCK;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (f + 16 * i < p.F) {
+                                k.g[i] = *reinterpret_cast<const uint4 *>(ck + 16 * i);
+                                k.u[i] = *reinterpret_cast<const uint4 *>(ck + p.F + 16 * i);
+                            }
+                        k.sg = sf[0];
+                        k.su = sf[blocks];
+                    }
+                    return k;
+                };
+                Kept next = fetch(0);
+                if (!__all_sync(0xffffffffu, W.wait(&tfull[b], aph))) break;
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int c = 0; c < Cfg::WCHUNKS; ++c) {
+                    const Kept k = next;
+                    if (c + 1 < Cfg::WCHUNKS) next = fetch(c + 1);
+                    uint32_t d[32];
+                    tmem_ld_32x32b_x32(taddr + EPI_COLS * c, d);
+                    tmem_ld_wait(d);
+                    if (c == Cfg::WCHUNKS - 1) release(b);
+                    if (c >= chunks) continue;
+                    begin_boxes();
+                    const float sg = rows::scale_value(k.sg), su = rows::scale_value(k.su);
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) {         // eight columns at a time
+                        const uint4 gq = k.g[o / 2], uq = k.u[o / 2];
+                        float g[8], u[8], dg[8], du[8], a[8];
+                        rows::decode(o % 2 ? make_uint2(gq.z, gq.w) : make_uint2(gq.x, gq.y), sg, g);
+                        rows::decode(o % 2 ? make_uint2(uq.z, uq.w) : make_uint2(uq.x, uq.y), su, u);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float da = __uint_as_float(d[8 * o + i]);
+                            float s1, s0;
+                            rows::sigmoid(g[i], s1, s0);
+                            const float gs = g[i] * s1;
+                            a[i] = gs * u[i];
+                            dg[i] = da * u[i] * (s1 * (1.f + g[i] * s0));
+                            du[i] = da * gs;
+                        }
+                        auto put = [&](uint32_t to, const float (&v)[8]) {
+                            const uint4 w = bf16 ? rows::pack8(static_cast<const __nv_bfloat16 *>(nullptr), v)
+                                                 : rows::pack8(static_cast<const __half *>(nullptr), v);
+                            st_shared_v4(to + swz_off<64>(lane, o), w.x, w.y, w.z, w.w);
+                        };
+                        put(box, dg);
+                        put(box + 2048, du);
+                        if (p.has_a) put(box + 4096, a);
+                    }
+                    end_boxes();
+                    if (lane == 0) {
+                        const int x = checked_x<2>(p.status, f_warp + EPI_COLS * c, p.F), y = checked_y(p.status, m_warp, p.M);
+                        tma_store_3d_hint(&tmZ, box, x, 0, y, stream_pol);
+                        tma_store_3d_hint(&tmZ, box + 2048, x, 1, y, stream_pol);
+                        if (p.has_a) tma_store_2d_hint(&tmA, box + 4096, x, y, stream_pol);
+                        bulk_commit_group();
+                    }
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_group0();
+    }
+
+    // ----------------------------------------------------------------- teardown
+    __syncwarp();
+    if (*abort_flag) {
+        // give copies that were already in flight time to land before the
+        // shared memory they target is released
+        for (int i = 0; i < 64; ++i) __nanosleep(1000);
+    }
+    tc_fence_before_sync();
+    if constexpr (CG == 2) cluster_sync(); else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<CG>(tmem_base, 512);
+    }
+}
+
+// What the host does with an instance
+template <class Cfg>
+struct GatedInstance {
+    static GatedShape shape() { return {Cfg::HN, Cfg::STAGES, Cfg::SMEM_BYTES, Cfg::BK, Cfg::SFA_BYTES, Cfg::SFB_BYTES}; }
+    static cudaError_t prepare(int *clusters) {
+        const void *f = reinterpret_cast<const void *>(&gated_kernel<Cfg>);
+        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t lc = config(2 * 1024, nullptr);
+        cudaLaunchAttribute attr = cluster();
+        lc.attrs = &attr;
+        lc.numAttrs = 1;
+        return cudaOccupancyMaxActiveClusters(clusters, f, &lc);
+    }
+    static cudaError_t launch(int grid, const CUtensorMap *maps, const GatedParams &p, cudaStream_t stream) {
+        cudaLaunchConfig_t lc = config(grid, stream);
+        cudaLaunchAttribute attr = cluster();
+        lc.attrs = &attr;
+        lc.numAttrs = 1;
+        return cudaLaunchKernelEx(&lc, gated_kernel<Cfg>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);
+    }
+
+private:
+    static cudaLaunchConfig_t config(int grid, cudaStream_t stream) {
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3((unsigned)grid);
+        lc.blockDim = dim3(Cfg::THREADS);
+        lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+        lc.stream = stream;
+        return lc;
+    }
+    static cudaLaunchAttribute cluster() {
+        cudaLaunchAttribute a = {};
+        a.id = cudaLaunchAttributeClusterDimension;
+        a.val.clusterDim.x = Cfg::CG;
+        a.val.clusterDim.y = a.val.clusterDim.z = 1;
+        return a;
+    }
+};
+
+}  // namespace gb300

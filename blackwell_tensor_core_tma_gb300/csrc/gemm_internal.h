@@ -144,9 +144,11 @@ const ScaledFamily &family_nvf4();   // gemm_nvf4.cu
 // Pack row-major scale factors SFA (M x sfk) and SFB (N x sfk) into the kernels'
 // 512-byte TMEM-order blocks (gemm_sfpack.cu).  n_wg: groups of four scale columns
 // per row of the packed layout (stages x scale words per stage); scales outside the
-// matrices read as `pad` (the format's 1.0).
+// matrices read as `pad` (the format's 1.0).  With plane_w > 0 SFB is two planes of plane_n rows and a tile
+// column takes plane_w rows of each (tile_n = 2 plane_w).
 cudaError_t sf_pack(const uint8_t *sfa, const uint8_t *sfb, uint8_t *out_a, uint8_t *out_b, int M, int N, int sfk,
-                    int row_blocks, int tiles_n, int tile_n, int n_wg, uint8_t pad, cudaStream_t stream);
+                    int row_blocks, int tiles_n, int tile_n, int n_wg, uint8_t pad, cudaStream_t stream, int plane_w = 0,
+                    int plane_n = 0);
 
 // Two chained products D = C + round(A·B)·E (gemm_chain.cu): parameters of one launch
 struct ChainParams {
@@ -179,6 +181,40 @@ cudaError_t chain_prepare(int out_bf16, int cta_group);
 cudaError_t chain_max_active_clusters(int out_bf16, int cta_group, int *clusters);
 // grid: CTAs (a multiple of cta_group); tiles of 128 * cta_group rows
 cudaError_t chain_launch(int out_bf16, int cta_group, int grid, const CUtensorMap *maps, const ChainParams &p,
+                         cudaStream_t stream);
+
+// The product with the gated unit (gemm_gated.cu): parameters of one launch
+struct GatedParams {
+    int M, F;
+    int tiles_m, tiles_n, num_tiles;
+    int num_kb;
+    int group_m;
+    int has_a;               // A is written (always, forward)
+    int has_z;               // forward: the checkpoint is kept; backward: always
+    int a_8bit;              // forward: A in e4m3 with scales
+    int out16;               // gemm_dtype of 16-bit outputs
+    uint32_t idesc;
+    int *status;
+    uint64_t timeout_ns;
+    int fault;
+    uint8_t *sfa, *sfck;                 // forward: scale codes out
+    const uint8_t *ck, *sfck_in;         // backward: the checkpoint
+};
+enum GatedForm { GATED_F16 = 0, GATED_MXF8 = 1, GATED_BACK = 2 };
+// plan families: forward plans and backward ones
+constexpr int FAMILY_GATED = 5;
+constexpr int FAMILY_GATED_BACK = 6;
+struct GatedShape {
+    int tile_n;              // columns of A per tile
+    int stages, smem;
+    int bk;                  // K elements per stage
+    int sfa_bytes, sfb_bytes;
+};
+GatedShape gated_shape(GatedForm form, int cta_group);
+// set the kernel's shared-memory limit; CTAs (or CTA pairs) that run at once
+cudaError_t gated_prepare(GatedForm form, int cta_group, int *clusters);
+// maps: X, W, packed SFX, packed SFW, A, checkpoint (backward: DY, W2, -, -, A, DZ)
+cudaError_t gated_launch(GatedForm form, int cta_group, int grid, const CUtensorMap *maps, const GatedParams &p,
                          cudaStream_t stream);
 
 constexpr int EPI_COLS = 32;  // epilogue chunk width (columns)

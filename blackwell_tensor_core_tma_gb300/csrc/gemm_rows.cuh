@@ -144,6 +144,22 @@ __device__ __forceinline__ void round_store(__nv_bfloat16 *p, bool on, float (&v
     unpack(p, q, v);
 }
 
+// ------------------------------------------------------------- the gated unit
+
+// s = 1 / (1 + exp(-g)) and t = 1 - s = exp(-g) s, which a subtraction would leave few digits of.  With p = 2^-16 exp(-g / 2)
+// both come from r = 1 / (p^2 + 2^-32) = 2^32 s, which is a normal number wherever s is not zero: s goes down to fp32's
+// smallest number, at g = -103, and t to 2^-117.  (Where s is zero t is no matter, but has to be finite.)  The fast
+// exponential and reciprocal (p^2: 4 + 1.173 |g| units in the last place, r: 1) are what the outputs' 8 or 16 bits, or a
+// comparison at 1e-6, have room for.
+__device__ __forceinline__ void sigmoid(float g, float &s, float &t) {
+    float p, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(g * -0.72134752f));                     // log2(e) / 2
+    p *= 0x1p-16f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(p, p, 0x1p-32f)));
+    s = r * 0x1p-32f;
+    t = fminf(p * p, 0x1p126f) * r;
+}
+
 // ------------------------------------------------------------- e4m3 with UE8M0
 
 // Scale code of a block with maximum magnitude amax: s = 2^(code - 127) is the smallest power of two

@@ -39,7 +39,7 @@ constexpr int PACK_COLS = PACK_WG * 4;      // scale bytes per row per CTA
 __global__ void __launch_bounds__(256) sf_pack_kernel(const uint8_t *__restrict__ sfa, const uint8_t *__restrict__ sfb,
                                                       uint8_t *__restrict__ out_a, uint8_t *__restrict__ out_b, int M,
                                                       int N, int sfk, int row_blocks, int tiles_n, int n_wg,
-                                                      int tile_n, uint8_t pad) {
+                                                      int tile_n, uint8_t pad, int plane_w, int plane_n) {
     __shared__ __align__(16) uint8_t slab[128][PACK_COLS];
     const int wg_groups = (n_wg + PACK_WG - 1) / PACK_WG;
     const int halves = (tile_n + 127) / 128;
@@ -60,19 +60,27 @@ __global__ void __launch_bounds__(256) sf_pack_kernel(const uint8_t *__restrict_
         row0 = tn * tile_n + h * 128;
         valid = min(min(128, tile_n - h * 128), N - row0);
     }
+    // two planes: the block's rows are those of both at the tile column's place (plane_w = 64 or 128)
+    const int p0 = plane_w && !is_a ? (blk_row / halves) * plane_w : 0, h0 = (blk_row % halves) * 128;
+    auto place = [&](int r) -> int {                // row r of the block in the scale matrix, or -1
+        if (!plane_w || is_a) return r < valid ? row0 + r : -1;
+        const int n = h0 + r, f = p0 + n % plane_w;
+        return n < tile_n && f < plane_n ? n / plane_w * plane_n + f : -1;
+    };
     const int col0 = g * PACK_COLS;
     const bool vec = (sfk % 16 == 0) && ((reinterpret_cast<uintptr_t>(src) & 15) == 0) && col0 + PACK_COLS <= sfk;
     // load: 128 rows x 64 bytes = 512 chunks of 16 bytes, two per thread
     for (int c = threadIdx.x; c < 128 * (PACK_COLS / 16); c += blockDim.x) {
         const int r = c / (PACK_COLS / 16), q = c % (PACK_COLS / 16);
+        const int row = place(r);
         uint4 v;
-        if (r < valid && vec) {
-            v = *reinterpret_cast<const uint4 *>(src + (int64_t)(row0 + r) * sfk + col0 + 16 * q);
+        if (row >= 0 && vec) {
+            v = *reinterpret_cast<const uint4 *>(src + (int64_t)row * sfk + col0 + 16 * q);
         } else {
             uint8_t b[16];
             for (int e = 0; e < 16; ++e) {
                 const int col = col0 + 16 * q + e;
-                b[e] = (r < valid && col < sfk) ? src[(int64_t)(row0 + r) * sfk + col] : pad;
+                b[e] = (row >= 0 && col < sfk) ? src[(int64_t)row * sfk + col] : pad;
             }
             memcpy(&v, b, 16);
         }
@@ -101,11 +109,12 @@ __global__ void __launch_bounds__(256) sf_pack_kernel(const uint8_t *__restrict_
 }  // namespace
 
 cudaError_t sf_pack(const uint8_t *sfa, const uint8_t *sfb, uint8_t *out_a, uint8_t *out_b, int M, int N, int sfk,
-                    int row_blocks, int tiles_n, int tile_n, int n_wg, uint8_t pad, cudaStream_t stream) {
+                    int row_blocks, int tiles_n, int tile_n, int n_wg, uint8_t pad, cudaStream_t stream, int plane_w,
+                    int plane_n) {
     const int wg_groups = (n_wg + PACK_WG - 1) / PACK_WG;
     const int64_t ctas = (int64_t)(row_blocks + tiles_n * ((tile_n + 127) / 128)) * wg_groups;
     sf_pack_kernel<<<(unsigned)ctas, 256, 0, stream>>>(sfa, sfb, out_a, out_b, M, N, sfk, row_blocks, tiles_n, n_wg,
-                                                       tile_n, pad);
+                                                       tile_n, pad, plane_w, plane_n);
     return cudaGetLastError();
 }
 

@@ -130,6 +130,24 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// The same for three dimensions
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t mbar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(m), "r"(mbar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *m, uint32_t mbar, int32_t c0,
+                                                 int32_t c1, int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(m), "r"(mbar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
 // 1-D bulk copy GMEM -> own SMEM (16-byte aligned addresses, size % 16 == 0)
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar) {
     asm volatile(
@@ -162,6 +180,15 @@ __device__ __forceinline__ void tma_store_2d_hint(const CUtensorMap *m, uint32_t
                      m),
                  "r"(src), "r"(c0), "r"(c1), "l"(pol)
                  : "memory");
+}
+
+// 3-D tiled store with an L2 cache policy
+__device__ __forceinline__ void tma_store_3d_hint(const CUtensorMap *m, uint32_t src, int32_t c0, int32_t c1, int32_t c2,
+                                                  uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(m),
+        "r"(src), "r"(c0), "r"(c1), "r"(c2), "l"(pol)
+        : "memory");
 }
 
 // 2-D tiled store own SMEM -> GMEM (clipped to the tensor bounds), bulk-group completion

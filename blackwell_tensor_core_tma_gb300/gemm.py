@@ -18,6 +18,7 @@ GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_ALIGNMENT, GEMM_ER
 GEMM_F16, GEMM_BF16, GEMM_E4M3, GEMM_F32, GEMM_E2M1 = range(5)
 GEMM_SCALE_NONE, GEMM_SCALE_UE8M0_32, GEMM_SCALE_UE4M3_16 = range(3)
 GEMM_NORM_PARTS = 512          # most rows of K fp32 that gemm_norm_backward's workspace needs
+GEMM_CLIP_WORKSPACE = 16384    # bytes of gemm_clip_run's workspace
 GEMM_FLAG_SYNC, GEMM_FLAG_FORCE_1CTA, GEMM_FLAG_FORCE_2CTA, GEMM_FLAG_DETERMINISTIC = 0x1, 0x2, 0x4, 0x8
 
 DTYPE = {"f16": GEMM_F16, "bf16": GEMM_BF16, "e4m3": GEMM_E4M3, "f32": GEMM_F32, "e2m1": GEMM_E2M1}
@@ -31,6 +32,8 @@ EXPORTS = ["gemm_plan_create", "gemm_run", "gemm_run_host", "gemm_plan_last_stat
            "gemm_testing_trace_slots", "gemm_testing_set_trace", "gemm_testing_tmem_ld_probe",
            "gemm_testing_staging_probe", "gemm_testing_schedule", "gemm_testing_e4m3_pair_tile_n",
            "gemm_norm_run", "gemm_norm_backward", "gemm_gate_run", "gemm_gate_backward", "gemm_matvec_run",
+           "gemm_gated_plan_create", "gemm_gated_run", "gemm_gated_back_plan_create", "gemm_gated_back_run",
+           "gemm_gated_matvec_run", "gemm_clip_run",
            "gemm_testing_set_norm_fault", "gemm_testing_matvec_shape"]
 
 # the per-role trace counters of one CTA, in slot order (a GB300_TRACE=1 library:
@@ -56,6 +59,10 @@ class PlanInfo(ctypes.Structure):
 class TensorRate(ctypes.Structure):
     _fields_ = [("flop_per_clk_per_sm", ctypes.c_double), ("sm_mhz", ctypes.c_double), ("tflops", ctypes.c_double),
                 ("ms", ctypes.c_double), ("sms", ctypes.c_int)]
+
+
+class ClipTensor(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("c", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int)]
 
 
 _lib = None
@@ -140,6 +147,15 @@ def lib():
         L.gemm_gate_run.argtypes = [i64, i64, st, st, vp, vp, vp, vp, vp, vp]
         L.gemm_gate_backward.argtypes = [i64, i64, st, st, st, vp, vp, vp, vp, vp, vp]
         L.gemm_matvec_run.argtypes = [i64, i64, i64, st, st, st, vp, vp, vp, vp, vp, vp]
+        L.gemm_gated_plan_create.argtypes = [ctypes.POINTER(vp), i64, i64, i64, st, st, st, ctypes.c_uint]
+        L.gemm_gated_run.argtypes = [vp] * 10
+        L.gemm_gated_back_plan_create.argtypes = [ctypes.POINTER(vp), i64, i64, i64, st, ctypes.c_uint]
+        L.gemm_gated_back_run.argtypes = [vp] * 8
+        L.gemm_gated_matvec_run.argtypes = [i64, i64, i64, st, st, st, vp, vp, vp, vp, vp]
+        L.gemm_clip_run.argtypes = [i64, vp, ctypes.c_float, vp, vp, ctypes.c_size_t, vp]
+        for f in (L.gemm_gated_plan_create, L.gemm_gated_run, L.gemm_gated_back_plan_create, L.gemm_gated_back_run,
+                  L.gemm_gated_matvec_run, L.gemm_clip_run):
+            f.restype = st
         for f in (L.gemm_norm_run, L.gemm_norm_backward, L.gemm_gate_run, L.gemm_gate_backward, L.gemm_matvec_run):
             f.restype = st
         _lib = L
@@ -347,6 +363,80 @@ def gemm_matvec_run(M: int, N: int, K: int, x, d, block_scaled: int, X, B, SFB, 
     return st
 
 
+def gemm_gated_plan_create(M: int, F: int, K: int, ab="bf16", a="bf16", block_scaled: int = 0, flags: int = 0) -> int:
+    out = ctypes.c_void_p()
+    st = lib().gemm_gated_plan_create(ctypes.byref(out), M, F, K, DTYPE.get(ab, ab), DTYPE.get(a, a), int(block_scaled), flags)
+    _check(st, "gemm_gated_plan_create")
+    return out.value
+
+
+def gemm_gated_run(plan: int, X, W, SFX, SFW, A, SFA=None, CK=None, SFCK=None, stream=None) -> int:
+    """A = silu(X·Wgᵀ) * (X·Wuᵀ) of W = [Wg; Wu], optionally the 8-bit checkpoint CK, SFCK of both products."""
+    st = (_lib or lib()).gemm_gated_run(plan, _ptr(X), _ptr(W), _ptr(SFX), _ptr(SFW), _ptr(A), _ptr(SFA), _ptr(CK), _ptr(SFCK),
+                                        _stream(stream))
+    if st:
+        raise GemmError(st, "gemm_gated_run")
+    return st
+
+
+def gemm_gated_back_plan_create(M: int, F: int, N: int, ab="bf16", flags: int = 0) -> int:
+    out = ctypes.c_void_p()
+    st = lib().gemm_gated_back_plan_create(ctypes.byref(out), M, F, N, DTYPE.get(ab, ab), flags)
+    _check(st, "gemm_gated_back_plan_create")
+    return out.value
+
+
+def gemm_gated_back_run(plan: int, DY, W2, CK, SFCK, DZ, A=None, stream=None) -> int:
+    """DZ = the gated unit's gradient at da = DY·W2 and the checkpoint, optionally the 16-bit operand A again."""
+    st = (_lib or lib()).gemm_gated_back_run(plan, _ptr(DY), _ptr(W2), _ptr(CK), _ptr(SFCK), _ptr(DZ), _ptr(A), _stream(stream))
+    if st:
+        raise GemmError(st, "gemm_gated_back_run")
+    return st
+
+
+def gemm_gated_matvec_run(M: int, F: int, K: int, x, w, a, X, W, SFW, A, stream=None) -> int:
+    """The gated product for 1 to 16 rows of 16-bit X and 16-bit or e4m3 (with SFW) weights."""
+    st = (_lib or lib()).gemm_gated_matvec_run(M, F, K, DTYPE.get(x, x), DTYPE.get(w, w), DTYPE.get(a, a), _ptr(X), _ptr(W),
+                                               _ptr(SFW), _ptr(A), _stream(stream))
+    if st:
+        raise GemmError(st, "gemm_gated_matvec_run")
+    return st
+
+
+class ClipTensors:
+    """The list of tensors of gemm_clip_run, laid out once: (g, c, type) with g and c torch tensors (c may be g or None), or
+    (g, c, type, n) with addresses.  Keeps the tensors alive."""
+
+    def __init__(self, tensors):
+        self.tensors = [tuple(t) for t in tensors]
+        self.array = (ClipTensor * max(1, len(self.tensors)))()
+        for entry, (g, c, kind, *n) in zip(self.array, self.tensors):
+            if not n:
+                for x in (g, c):
+                    if x is not None and not (x.is_contiguous() and x.numel() == g.numel() and x.dtype == g.dtype):
+                        raise ValueError("tensors are contiguous, and c has g's size and type")
+                if g.element_size() != (4 if DTYPE.get(kind, kind) == GEMM_F32 else 2):
+                    raise ValueError(f"{g.dtype} is not {kind}")
+            entry.g, entry.c, entry.n, entry.type = _ptr(g), _ptr(c), n[0] if n else g.numel(), DTYPE.get(kind, kind)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def clip_tensors(tensors) -> ClipTensors:
+    return ClipTensors(tensors)
+
+
+def gemm_clip_run(tensors: ClipTensors, limit: float, NORM, workspace, workspace_bytes: int = GEMM_CLIP_WORKSPACE,
+                  stream=None) -> int:
+    """NORM = the Euclidean norm of all g together, c = g * min(1, limit / NORM)."""
+    st = (_lib or lib()).gemm_clip_run(len(tensors.tensors), tensors.array, limit, _ptr(NORM), _ptr(workspace), workspace_bytes,
+                                       _stream(stream))
+    if st:
+        raise GemmError(st, "gemm_clip_run")
+    return st
+
+
 def gemm_measure_tensor_rate(ab, block_scaled: int = GEMM_SCALE_NONE, cta_group: int = 2,
                              iters: int = 4096) -> dict:
     """The tensor-pipe rate probe: FLOP per SM clock of the GEMM's MMA shape, the SM clock
@@ -427,6 +517,36 @@ class ChainPlan(Plan):
 
     def run_host(self, A, B, E, C, D, stream=None):
         return gemm_chain_run_host(self.handle, A, B, E, C, D, stream)
+
+
+class GatedPlan(Plan):
+    """Owning wrapper of a gated product's plan: A = silu(X·Wgᵀ) * (X·Wuᵀ)."""
+
+    def __init__(self, M, F, K, ab="bf16", a="bf16", block_scaled=GEMM_SCALE_NONE, flags=0):
+        self.M, self.F, self.K, self.ab, self.a, self.block_scaled = M, F, K, ab, a, int(block_scaled)
+        self.handle = None
+        self.handle = gemm_gated_plan_create(M, F, K, ab, a, int(block_scaled), flags)
+
+    def run(self, X, W, A, SFX=None, SFW=None, SFA=None, CK=None, SFCK=None, stream=None):
+        return gemm_gated_run(self.handle, X, W, SFX, SFW, A, SFA, CK, SFCK, stream)
+
+    def run_host(self, *_):
+        raise NotImplementedError("a gated plan has no host-buffer form")
+
+
+class GatedBackPlan(Plan):
+    """Owning wrapper of the gated product's gradient's plan: DZ from DY·W2 and the checkpoint."""
+
+    def __init__(self, M, F, N, ab="bf16", flags=0):
+        self.M, self.F, self.N, self.ab = M, F, N, ab
+        self.handle = None
+        self.handle = gemm_gated_back_plan_create(M, F, N, ab, flags)
+
+    def run(self, DY, W2, CK, SFCK, DZ, A=None, stream=None):
+        return gemm_gated_back_run(self.handle, DY, W2, CK, SFCK, DZ, A, stream)
+
+    def run_host(self, *_):
+        raise NotImplementedError("a gated plan has no host-buffer form")
 
 
 def gemm_testing_schedule(chain: bool, tiles_m: int, tiles_n: int, group_m: int, num_kb: int, splits: int,

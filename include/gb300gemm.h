@@ -419,6 +419,82 @@ gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dtype x, gemm_
                             void *cuda_stream);
 
 /*
+ * The block's first product and its gated unit in one kernel:
+ *
+ *     [g | u] = X·Wᵀ                              (W's rows: F of g's weights, then F of u's)
+ *     a[m][f] = g[m][f] * s * u[m][f],   s = 1 / (1 + exp(-g[m][f]))
+ *
+ * X: M x K row-major.  W: 2F x K row-major, the column-major B of a plan with N = 2F.  ab, X, W, SFX and SFW are such
+ * a plan's: GEMM_F16 or GEMM_BF16 with GEMM_SCALE_NONE, or GEMM_E4M3 with GEMM_SCALE_UE8M0_32 (SFX: M x ceil(K/32), SFW:
+ * 2F x ceil(K/32)).  A and, with CK != NULL, the checkpoint of g and u are gemm_gate_run's (a: GEMM_E4M3 with SFA, GEMM_BF16
+ * or GEMM_F16), made from the fp32 sums: no 16-bit z stands between.  F % 16 == 0 and 16-byte rows of X and W
+ * (GEMM_ERR_ALIGNMENT), F <= 2^20.  The sums of an element run in an order that depends on K, and on the tile that it is in.
+ *
+ * A gated plan is a plan: gemm_plan_last_status, gemm_plan_get_info (tile_n: columns of A), gemm_plan_set_timeout,
+ * gemm_plan_destroy and the flags work on it (it takes CTA pairs by the rule that gemm_gated_plan_create documents
+ * in its info); gemm_run and gemm_run_host refuse it (GEMM_ERR_INVALID_ARG), and splits, stream-K and the clock meter
+ * do not apply (GEMM_ERR_UNSUPPORTED).  A block-scaled plan packs SFX and SFW into memory of its own in each run: runs of one
+ * plan must not overlap on the GPU.  Pointers are 16-byte aligned but for the scale codes.  X, W and their codes must not
+ * overlap the outputs.
+ */
+gemm_status gemm_gated_plan_create(gemm_plan_t *out, int64_t M, int64_t F, int64_t K, gemm_dtype ab, gemm_dtype a,
+                                   int block_scaled, unsigned flags);
+gemm_status gemm_gated_run(gemm_plan_t p, const void *X, const void *W, const uint8_t *SFX, const uint8_t *SFW, void *A,
+                           uint8_t *SFA, uint8_t *CK, uint8_t *SFCK, void *cuda_stream);
+
+/*
+ * Its gradient together with the product that the gradient at a comes from, in one kernel:
+ *
+ *     da[m][f] = sum_n DY[m][n] * W2[n][f]        (fp32, not rounded on the way)
+ *     dz = [ da * u * s * (1 + g * (1 - s)) | da * g * s ],    a = g * s * u
+ *
+ * at the checkpoint's values g and u, as gemm_gate_backward has them.  DY: M x N row-major; W2: N x F row-major, the second
+ * product's B (column-major F x N) as the forward product reads it.  DY, W2, DZ (M x 2F) and A (M x F, or
+ * NULL) have the type ab, GEMM_F16 or GEMM_BF16.  F % 16 == 0, N % 8 == 0 (GEMM_ERR_ALIGNMENT), F <= 2^20.  The gradients at
+ * the block's input and at W are then products of DZ, as plans compute them.  Else as for gemm_gated_run.
+ */
+gemm_status gemm_gated_back_plan_create(gemm_plan_t *out, int64_t M, int64_t F, int64_t N, gemm_dtype ab, unsigned flags);
+gemm_status gemm_gated_back_run(gemm_plan_t p, const void *DY, const void *W2, const uint8_t *CK, const uint8_t *SFCK,
+                                void *DZ, void *A, void *cuda_stream);
+
+/*
+ * The gated product for 1 to 16 rows: one token, or a few, through a gated plan's weights.  X: M x K and A: M x F of type
+ * x = a, GEMM_BF16 or GEMM_F16; W: 2F x K of type w = x, or GEMM_E4M3 with SFW as above.  Sums in fp32, in an order that depends on
+ * M, F, K, the types and the GPU's SM count.  fp16 activations meet e4m3 weights as the two bf16 values that they are the sum of;
+ * a scaled e4m3 weight below 2^-126 loses digits as bf16's subnormal numbers do.  Any F from 1 to 2^20 (GEMM_ERR_INVALID_ARG);
+ * K % 8 == 0, for e4m3 K % 16 == 0 (GEMM_ERR_ALIGNMENT); M > 16 or K > 32768: GEMM_ERR_UNSUPPORTED.
+ * It takes no plan, and is otherwise as the operators above.
+ */
+gemm_status gemm_gated_matvec_run(int64_t M, int64_t F, int64_t K, gemm_dtype x, gemm_dtype w, gemm_dtype a, const void *X,
+                                  const void *W, const uint8_t *SFW, void *A, void *cuda_stream);
+
+/*
+ * The Euclidean norm of many tensors together, and the tensors scaled to a largest norm, as a training step does with
+ * its gradients:
+ *
+ *     NORM = sqrt(sum over all tensors of sum_i g[i]^2),     c[i] = g[i] * min(1, limit / NORM)
+ *
+ * Each tensor has n >= 0 consecutive elements of type GEMM_F32, GEMM_BF16 or GEMM_F16, at addresses that are multiples of the element's
+ * size (GEMM_ERR_ALIGNMENT); c has g's type, and is g itself, apart from every g and other c, or NULL (the tensor counts and is not
+ * written).  The list is read before the call returns.  NORM: one fp32 on the device.  limit >= 0; infinity
+ * scales nothing.  Squares neither overflow nor vanish on their way: the sums are exact to fp32's precision over its whole range.  A NaN
+ * among the elements makes NORM and every c NaN; an infinity makes NORM infinite, finite c zero and its own c NaN (unless
+ * limit is infinite).  A c that equals its g is not written where nothing is scaled.  The workspace has GEMM_CLIP_WORKSPACE bytes
+ * (less: GEMM_ERR_INVALID_ARG), 16-byte aligned, whose contents do not matter before or after; calls that may overlap on
+ * the GPU need one each.  Results do not depend on timing, but on the list's order, the alignment of its tensors and
+ * the GPU's SM count.  More than 2 million tensors or 2^46 bytes: GEMM_ERR_UNSUPPORTED.
+ */
+#define GEMM_CLIP_WORKSPACE 16384
+typedef struct {
+    const void *g;
+    void *c;
+    int64_t n;
+    gemm_dtype type;
+} gemm_clip_tensor;
+gemm_status gemm_clip_run(int64_t count, const gemm_clip_tensor *tensors, float limit, float *NORM, void *workspace,
+                          size_t workspace_bytes, void *cuda_stream);
+
+/*
  * Tensor-pipe rate probe (measurement, not part of the GEMM path).  Launches one
  * CTA (cta_group = 1) or CTA pair (cta_group = 2) per SM; in each, one thread
  * issues `iters` groups of four back-to-back tcgen05.mma of the GEMM kernels'
