@@ -78,6 +78,7 @@ struct gemm_plan {
     int *sk_flags;            // stream-K: one flag per (slot, CTA of the group)
     float *sk_part;           // chain stream-K: one partial T per (slot, CTA of the group)
     uint32_t epoch;           // stream-K: runs so far (the value a run's flags carry)
+    int whole;                // gated plans: tiles worked on whole (the others come as two halves)
     int tile_n;
     int epi_box;              // columns of the epilogue's C / D boxes (32 or 16)
     int tile_k;               // K elements per stage
@@ -140,6 +141,14 @@ bool is_product(const gemm_plan *p) { return p->family <= KIND_NVF4; }
 bool is_gated(const gemm_plan *p) { return p->family == FAMILY_GATED || p->family == FAMILY_GATED_BACK; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+GatedForm gated_form(const gemm_plan *p) {
+    return p->family == FAMILY_GATED_BACK ? GATED_BACK : (p->block_scaled ? GATED_MXF8_PACKED : GATED_F16);
+}
+// Single CTAs read the scales as they are where each row of them begins at a multiple of 16 bytes
+bool gated_scales_packed(const gemm_plan *p, const uint8_t *SFX, const uint8_t *SFW) {
+    return p->block_scaled && (p->cta_group == 2 || (p->K + 31) / 32 % 16 != 0 || !aligned16(SFX) || !aligned16(SFW));
+}
 
 // 2-D row-major tensor [outer][inner] with a box of box_outer x box_inner elements; `promo`
 // is the L2 fill granularity of the copies (lines fetched around each box row)
@@ -831,7 +840,8 @@ gemm_status gemm_plan_get_info(gemm_plan_t p, gemm_plan_info *info) {
     info->tiles = p->tiles;
     info->smem_bytes = p->smem;
     // block-scaled plans also launch the scale-packing kernel, split-K plans the D = C kernel
-    const bool scaled = p->block_scaled != GEMM_SCALE_NONE;
+    // (a gated plan: where its scales need packing whatever the pointers)
+    const bool scaled = is_gated(p) ? gated_scales_packed(p, nullptr, nullptr) : p->family != KIND_F16 && is_product(p);
     info->launches_per_run = (scaled ? 2 : 1) + (p->splits > 1 ? 1 : 0);
     info->splits = p->splits;
     info->stream_k = p->sk;
@@ -1065,8 +1075,11 @@ gemm_status gemm_chain_run_host(gemm_plan_t p, const void *A, const void *B, con
 
 namespace {
 
-GatedForm gated_form(const gemm_plan *p) {
-    return p->family == FAMILY_GATED_BACK ? GATED_BACK : (p->block_scaled ? GATED_MXF8 : GATED_F16);
+// Tiles that are worked on whole.  A pair's last round that would keep half of the pairs or fewer busy has its tiles
+// halved, and then takes about half as long.
+int gated_whole_tiles(int tiles, int units, int cg) {
+    const int rest = tiles % units;
+    return cg == 2 && 2 * rest <= units ? tiles - rest : tiles;
 }
 
 // The plan of either direction: A is M x F, the product's sums run over K
@@ -1103,6 +1116,13 @@ gemm_status gated_plan_create(gemm_plan_t *out, int family, int64_t M, int64_t F
         delete p;
         return GEMM_ERR_CUDA;
     }
+    if (block_scaled && cg == 1) {        // the other form's shared-memory limit
+        int same = 0;
+        if (gated_prepare(GATED_MXF8, cg, &same) != cudaSuccess || same != units) {
+            delete p;
+            return GEMM_ERR_CUDA;
+        }
+    }
     const GatedShape sh = gated_shape(form, cg);
     p->cta_group = cg;
     p->stages = sh.stages;
@@ -1114,18 +1134,20 @@ gemm_status gated_plan_create(gemm_plan_t *out, int family, int64_t M, int64_t F
     p->tiles_n = (int)((F + sh.tile_n - 1) / sh.tile_n);
     p->tiles = p->tiles_m * p->tiles_n;
     p->capacity = units;
-    p->grid = cg * (p->tiles < units ? p->tiles : units);
+    p->whole = gated_whole_tiles(p->tiles, units, cg);
+    const int work = 2 * p->tiles - p->whole;
+    p->grid = cg * (work < units ? work : units);
     p->group_m = cg == 2 ? GB300_GROUP_M_PAIRS : GB300_GROUP_M_SINGLE;
     bool ok = cudaMalloc(&p->status, sizeof(int)) == cudaSuccess &&
               cudaMemset(p->status, 0, sizeof(int)) == cudaSuccess;
-    if (ok && block_scaled) {             // the packed scales of every (128 rows, stage) and (tile column, stage)
-        const size_t a_bytes = (size_t)p->tiles_m * cg * p->num_kb * sh.sfa_bytes;
-        const size_t b_bytes = (size_t)p->tiles_n * p->num_kb * sh.sfb_bytes;
+    if (ok && block_scaled) {  // the packed scales of every (128 rows of X, stage) and (64 columns of A, stage)
+        const size_t a_bytes = (size_t)p->tiles_m * cg * p->num_kb * 512;
+        const size_t b_bytes = (size_t)((F + 63) / 64) * p->num_kb * 512;
         ok = cudaMalloc(&p->ws_a, a_bytes) == cudaSuccess && cudaMalloc(&p->ws_b, b_bytes) == cudaSuccess &&
-             encode_2d(&p->maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p->ws_a, 128, a_bytes / 128, 128,
-                       (uint32_t)(sh.sfa_bytes / 128), CU_TENSOR_MAP_SWIZZLE_NONE) &&
-             encode_2d(&p->maps[3], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p->ws_b, 128, b_bytes / 128, 128,
-                       (uint32_t)(sh.sfb_bytes / 128), CU_TENSOR_MAP_SWIZZLE_NONE);
+             encode_2d(&p->maps[4], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p->ws_a, 128, a_bytes / 128, 128, 4,
+                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
+             encode_2d(&p->maps[5], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p->ws_b, 128, b_bytes / 128, 128, 4,
+                       CU_TENSOR_MAP_SWIZZLE_NONE);
     }
     if (!ok) {
         gemm_plan_destroy(p);
@@ -1142,17 +1164,17 @@ gemm_status encode_gated_maps(gemm_plan *p, const void *X, const void *W, const 
     const bool back = p->family == FAMILY_GATED_BACK;
     const CUtensorMapDataType ab = tma_dtype(p->ab);
     const uint64_t eb = (uint64_t)elem_bits(p->ab) / 8, M = (uint64_t)p->M, F = (uint64_t)p->N, K = (uint64_t)p->K;
-    const uint32_t bk = 128u / (uint32_t)eb, hn = (uint32_t)p->tile_n;
+    const uint32_t bk = 128u / (uint32_t)eb;
     bool ok = encode_2d(&p->maps[0], ab, (int)eb, X, K, M, bk, TILE_M, CU_TENSOR_MAP_SWIZZLE_128B);
     ok = ok && (back ? encode_2d(&p->maps[1], ab, (int)eb, W, F, K, bk, bk, CU_TENSOR_MAP_SWIZZLE_128B)
-                     : encode_3d(&p->maps[1], ab, W, K, F, 2, K * eb, F * K * eb, bk, hn, 1, CU_TENSOR_MAP_SWIZZLE_128B));
+                     : encode_3d(&p->maps[1], ab, W, K, F, 2, K * eb, F * K * eb, bk, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B));
     // outputs leave by boxes of 32 x 32, rows of 64 (16-bit) or 32 (8-bit) bytes swizzled over the row
     const int a_bytes = elem_bits(p->d) / 8;
     const CUtensorMapSwizzle sw = a_bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-    if (ok && A) ok = encode_2d(&p->maps[4], tma_dtype(p->d), a_bytes, A, F, M, EPI_COLS, 32, sw);
+    if (ok && A) ok = encode_2d(&p->maps[2], tma_dtype(p->d), a_bytes, A, F, M, EPI_COLS, 32, sw);
     const uint64_t zb = back ? 2 : 1;
     if (ok && Z)
-        ok = encode_3d(&p->maps[5], back ? ab : CU_TENSOR_MAP_DATA_TYPE_UINT8, Z, F, 2, M, F * zb, 2 * F * zb, EPI_COLS, 1, 32,
+        ok = encode_3d(&p->maps[3], back ? ab : CU_TENSOR_MAP_DATA_TYPE_UINT8, Z, F, 2, M, F * zb, 2 * F * zb, EPI_COLS, 1, 32,
                        back ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
     if (!ok) return GEMM_ERR_CUDA;
     p->lastA = X;
@@ -1163,19 +1185,24 @@ gemm_status encode_gated_maps(gemm_plan *p, const void *X, const void *W, const 
     return GEMM_OK;
 }
 
-gemm_status gated_launch_plan(gemm_plan *p, GatedParams &gp, cudaStream_t stream) {
-    const GatedForm form = gated_form(p);
+gemm_status gated_launch_plan(gemm_plan *p, GatedForm form, GatedParams &gp, cudaStream_t stream) {
     gp.M = (int)p->M;
     gp.F = (int)p->N;
+    gp.K = (int)p->K;
     gp.tiles_m = p->tiles_m;
     gp.tiles_n = p->tiles_n;
-    gp.num_tiles = p->tiles;
+    gp.whole = p->whole;
+    gp.units = 2 * p->tiles - p->whole;
     gp.num_kb = p->num_kb;
     gp.group_m = p->group_m;
     gp.out16 = p->d;
     const uint32_t m = (uint32_t)(TILE_M * p->cta_group), n = (uint32_t)(form == GATED_BACK ? p->tile_n : 2 * p->tile_n);
-    gp.idesc = form == GATED_MXF8 ? idesc_mxf8(m, n, 0, 0)
-                                  : idesc_f16(p->ab == GEMM_BF16 ? 1u : 0u, m, n) | ((uint32_t)p->b_mn << 16);
+    auto idesc = [&](uint32_t cols) {
+        return p->block_scaled ? idesc_mxf8(m, cols, 0, 0)
+                                  : idesc_f16(p->ab == GEMM_BF16 ? 1u : 0u, m, cols) | ((uint32_t)p->b_mn << 16);
+    };
+    gp.idesc = idesc(n);
+    gp.idesc_narrow = idesc(128);
     gp.status = p->status;
     gp.timeout_ns = p->timeout_ns;
     gp.fault = p->fault;
@@ -1190,8 +1217,8 @@ gemm_status gated_launch_plan(gemm_plan *p, GatedParams &gp, cudaStream_t stream
 gemm_status gated_sizes(gemm_plan_t *out, int64_t M, int64_t F, int64_t K, unsigned flags) {
     if (!out || M <= 0 || F <= 0 || K <= 0) return GEMM_ERR_INVALID_ARG;
     if (M > INT32_MAX || F > (1 << 20) || K > INT32_MAX) return GEMM_ERR_INVALID_ARG;
-    // tiles and the rows of packed scales are counted in 32 bits
-    if ((M + TILE_M) / TILE_M * ((F + 63) / 64) > INT32_MAX || (M + TILE_M) / TILE_M * (K / 32 + 1) > INT32_MAX)
+    // units of work and rows of packed scales are counted in 32 bits
+    if ((M + TILE_M) / TILE_M * ((F + 63) / 64) > INT32_MAX || ((M + F) / 32 + 16) * (K / 64 + 1) > INT32_MAX)
         return GEMM_ERR_INVALID_ARG;
     if ((flags & GEMM_FLAG_FORCE_1CTA) && (flags & GEMM_FLAG_FORCE_2CTA)) return GEMM_ERR_INVALID_ARG;
     return GEMM_OK;
@@ -1220,19 +1247,19 @@ gemm_status gemm_gated_run(gemm_plan_t p, const void *X, const void *W, const ui
     gemm_status st = encode_gated_maps(p, X, W, A, CK);
     if (st != GEMM_OK) return st;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
-    if (p->block_scaled) {
-        const int sfk = (int)((p->K + 31) / 32);
-        if (sf_pack(SFX, SFW, p->ws_a, p->ws_b, (int)p->M, (int)(2 * p->N), sfk, p->tiles_m * p->cta_group, p->tiles_n,
-                    2 * p->tile_n, p->num_kb, unit_scale(KIND_MXF8), stream, p->tile_n, (int)p->N) != cudaSuccess)
-            return GEMM_ERR_CUDA;
-    }
+    const bool packed = gated_scales_packed(p, SFX, SFW);
+    if (packed && sf_pack(SFX, SFW, p->ws_a, p->ws_b, (int)p->M, (int)(2 * p->N), (int)((p->K + 31) / 32), p->tiles_m * p->cta_group,
+                           (int)((p->N + 63) / 64), 128, p->num_kb, unit_scale(KIND_MXF8), stream, 64, (int)p->N) != cudaSuccess)
+        return GEMM_ERR_CUDA;
     GatedParams gp{};
     gp.has_a = 1;
     gp.has_z = CK != nullptr;
     gp.a_8bit = p->d == GEMM_E4M3;
+    gp.sfx = SFX;
+    gp.sfw = SFW;
     gp.sfa = SFA;
     gp.sfck = SFCK;
-    return gated_launch_plan(p, gp, stream);
+    return gated_launch_plan(p, p->block_scaled && !packed ? GATED_MXF8 : gated_form(p), gp, stream);
 }
 
 gemm_status gemm_gated_back_plan_create(gemm_plan_t *out, int64_t M, int64_t F, int64_t N, gemm_dtype ab, unsigned flags) {
@@ -1256,7 +1283,7 @@ gemm_status gemm_gated_back_run(gemm_plan_t p, const void *DY, const void *W2, c
     gp.has_z = 1;
     gp.ck = CK;
     gp.sfck_in = SFCK;
-    return gated_launch_plan(p, gp, reinterpret_cast<cudaStream_t>(cuda_stream));
+    return gated_launch_plan(p, GATED_BACK, gp, reinterpret_cast<cudaStream_t>(cuda_stream));
 }
 
 // Test hook (declared in include/gb300gemm_testing.h): the pair tile-width rule alone.

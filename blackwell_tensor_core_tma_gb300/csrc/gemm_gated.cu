@@ -11,7 +11,8 @@ namespace {
 using F16Pair = GatedInstance<GatedCfg<2, KIND_F16, false, 128, 6, 2, 8>>;
 using F16Single = GatedInstance<GatedCfg<1, KIND_F16, false, 64, 6, 2, 8>>;
 using Mx8Pair = GatedInstance<GatedCfg<2, KIND_MXF8, false, 128, 5, 1, 8, 2>>;
-using Mx8Single = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 5, 2, 8, 1>>;
+using Mx8Single = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 5, 2, 8, 1, true>>;
+using Mx8SinglePacked = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 5, 2, 8, 1>>;
 using BackPair = GatedInstance<GatedCfg<2, KIND_F16, true, 256, 5, 2, 8>>;
 using BackSingle = GatedInstance<GatedCfg<1, KIND_F16, true, 128, 5, 2, 8>>;
 
@@ -19,7 +20,8 @@ using BackSingle = GatedInstance<GatedCfg<1, KIND_F16, true, 128, 5, 2, 8>>;
 template <typename F>
 auto with(GatedForm form, int cta_group, F f) {
     if (form == GATED_F16) return cta_group == 2 ? f(F16Pair()) : f(F16Single());
-    if (form == GATED_MXF8) return cta_group == 2 ? f(Mx8Pair()) : f(Mx8Single());
+    if (form == GATED_MXF8) return f(Mx8Single());
+    if (form == GATED_MXF8_PACKED) return cta_group == 2 ? f(Mx8Pair()) : f(Mx8SinglePacked());
     return cta_group == 2 ? f(BackPair()) : f(BackSingle());
 }
 

@@ -9,11 +9,20 @@
 // MMA issuing thread, scale-copying warps for block-scaled operands, epilogue warps.  What differs
 // is what a tile is and what its epilogue does:
 //
-//   * Forward: a tile's HN columns of A take 2 HN columns of the product, g's and then u's.  The
-//     weights are mapped as [2][F][K], so that a box of HN rows of either half is zero past F.  In a
-//     CTA pair the leader's half of the MMA's N is g's rows and its peer's u's, so that each CTA
-//     loads one box as in the plain product.  Both accumulators of an element are then in the
-//     same lane of tensor memory, HN columns apart: the unit needs no exchange between threads.
+//   * Forward: 64 columns of A take 128 columns of the product, 64 of g and then the same 64 of u.  The
+//     weights are mapped as [2][F][K], so that a box of 64 rows of either half is zero past F.
+//     Both accumulators of an element are then in the same lane of tensor memory, 64 columns apart:
+//     the unit needs no exchange between threads.  A CTA pair's tile has 128 columns of A, 64 in
+//     each CTA's half of the MMA's N.
+//   * Where a pair's last round of tiles would leave half of the pairs or more without work, its tiles are
+//     halved: 64 columns of A, the leader holding g's rows and its peer u's (backward: 128 columns).
+//   * Block scales are packed by a kernel before (gemm_sfpack.cu) and come by TMA, as in gemm_tc_kernel, or
+//     (GROUPED: single CTAs, whose products are short, where every row of scales begins at a multiple of 16 bytes) are
+//     read as the operands' owners have them: the copying warp loads sixteen bytes of a row (a group of four
+//     k-blocks) ahead of their use, writes the group's words to shared memory in tensor memory's order and copies them
+//     there, into a ring of groups of its own: 64 x 8192 x 4096 takes 18 us, 24.7 with the packing kernel.  (For pairs
+//     the way over both CTAs' warps takes 2 us per group, twice its MMAs' time: 4096 x 8192 x 8192 458 us, 385 with the
+//     packing kernel; rows that begin anywhere cost ten loads for one, 30 us at 64 x 8192 x 4064.)
 //   * A thread owns a row; its chunk of 32 columns is one scale block of e4m3, so that a block's
 //     maximum is a thread's own.
 //   * Backward: B is N-contiguous (W2 as the forward product has it), g and u come as 8-bit codes
@@ -28,7 +37,8 @@
 namespace gb300 {
 
 // Compile-time shape of one kernel instance: HN columns of A per tile; the rest as in TileCfg.
-template <int CG_, int KIND_, bool BACK_, int HN_, int STAGES_, int ACC_BUFS_, int EPI_WARPS_, int COPIERS_ = 0>
+template <int CG_, int KIND_, bool BACK_, int HN_, int STAGES_, int ACC_BUFS_, int EPI_WARPS_, int COPIERS_ = 0,
+          bool GROUPED_ = false>
 struct GatedCfg {
     static constexpr int CG = CG_;
     static constexpr int KIND = KIND_;
@@ -36,6 +46,9 @@ struct GatedCfg {
     static constexpr bool BACK = BACK_;
     static constexpr int HN = HN_;
     static constexpr int BN = BACK ? HN : 2 * HN;               // columns of the MMA
+    // the narrow form of a tile: all that a single CTA has, a pair's halved tile
+    static constexpr int NARROW = BACK ? 128 : 64;              // columns of A
+    static_assert(HN == NARROW * CG_, "a pair's tile is two narrow ones wide");
     static constexpr int STAGES = STAGES_;
     static constexpr int ACC_BUFS = ACC_BUFS_;
     static constexpr int EPI_WARPS = EPI_WARPS_;
@@ -43,8 +56,9 @@ struct GatedCfg {
     static constexpr bool COPIER = COPIERS > 0;
     static constexpr int COPY_WARP = 2 + EPI_WARPS;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS + 32 * COPIERS;
-    static constexpr int WCOLS = HN * 4 / EPI_WARPS;            // columns of A one epilogue warp handles
-    static constexpr int WCHUNKS = WCOLS / EPI_COLS;
+    static_assert(EPI_WARPS == 8, "two epilogue warps per TMEM lane window");
+    // chunks of A's columns one epilogue warp handles
+    static constexpr int WCHUNKS = HN / 2 / EPI_COLS, NARROW_WCHUNKS = NARROW / 2 / EPI_COLS;
     static constexpr int ELEM_BITS = KIND == KIND_F16 ? 16 : 8;
     static constexpr int ELEM_BYTES = ELEM_BITS / 8;
     static constexpr int BK = 1024 / ELEM_BITS;                 // K elements per stage: one 128-byte row
@@ -59,18 +73,31 @@ struct GatedCfg {
     static constexpr int HALVES = (BN + 127) / 128;
     static constexpr int SFA_BYTES = 512 * SF_WORDS;
     static constexpr int SFB_BYTES = 512 * SF_WORDS * HALVES;
+    static constexpr int BOX_BYTES = 64 * 128;                  // a box of B: 64 rows (backward: columns) of 128 bytes
+    static constexpr int BOXES = B_BYTES / BOX_BYTES;
+    static constexpr int NARROW_BOXES = 128 / CG / 64;          // of a narrow tile: 128 columns of the MMA
     static constexpr int TX_AB = CG * (A_BYTES + B_BYTES);
+    static constexpr int NARROW_TX_AB = CG * (A_BYTES + NARROW_BOXES * BOX_BYTES);
+    static constexpr bool GROUPED = GROUPED_;                   // the copying warp packs the scales
+    static constexpr bool PACKED = SCALED && !GROUPED;          // they come packed, a stage's with its operands
+    static_assert(!GROUPED || (SCALED && CG == 1), "scales packed by a single CTA");
     static constexpr int TX_SF = CG * (SFA_BYTES + SFB_BYTES);
+    static constexpr int NARROW_TX_SF = CG * (SFA_BYTES + 512 * SF_WORDS);
+    static constexpr int SF_GROUP = PACKED ? 1 : 4;             // k-blocks of a group of scales
+    static constexpr int SF_RING = PACKED ? STAGES : GROUPED ? 4 : 0;   // groups in shared and in tensor memory
+    static constexpr int SF_BLOCKS = SF_WORDS * (1 + HALVES);   // 512-byte blocks of scales of a stage: X's, W's
+    static constexpr int WARP_SF_BLOCKS = COPIERS ? (SF_BLOCKS + COPIERS - 1) / COPIERS : 0;
     // an epilogue warp's staging: 32 rows of a chunk of each output (16-bit: 2 KiB, 8-bit: 1 KiB)
     static constexpr int EPI_BUF = BACK ? 3 * 2048 : 2048 + 2 * 1024;
     static constexpr int align1k(int x) { return (x + 1023) / 1024 * 1024; }
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
     static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
-    static constexpr int OFF_EPI = align1k(OFF_SF + STAGES * (SFA_BYTES + SFB_BYTES));
+    static constexpr int OFF_EPI = align1k(OFF_SF + SF_RING * SF_GROUP * SF_BLOCKS * 512);
     static constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_BUF;
-    // full[STAGES], empty[STAGES], tfull[2], tempty[2], drain, then with COPIER: cdrain, sffull[STAGES]
-    static constexpr int NBAR = 2 * STAGES + 5 + (COPIER ? STAGES + 1 : 0);
+    // full[STAGES], empty[STAGES], tfull[2], tempty[2], drain, then with COPIER: cdrain and, per group of scales,
+    // sffull (packed ones have landed), sfready (grouped ones are in tensor memory), sfempty (their MMAs are done)
+    static constexpr int NBAR = 2 * STAGES + 5 + (COPIER ? 3 * SF_RING + 1 : 0);
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;         // tmem base slot, abort flag
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;     // + alignment slack
     static constexpr int SF_SLOT = 4 * SF_WORDS * (1 + HALVES);
@@ -79,13 +106,37 @@ struct GatedCfg {
     static_assert(KIND == KIND_F16 || KIND == KIND_MXF8, "operand kind");
     static_assert(!BACK || KIND == KIND_F16, "the backward product has 16-bit operands");
     static_assert(COPIER == SCALED, "block-scaled instances have copier warps");
-    static_assert(ACC_BUFS * BN + STAGES * SF_SLOT <= 512, "TMEM budget");
+    static_assert(ACC_BUFS * BN + SF_RING * SF_GROUP * SF_SLOT <= 512, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared-memory budget");
     static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && EPI_BUF % 1024 == 0, "1024-byte regions");
-    static_assert(EPI_WARPS == 4 || EPI_WARPS == 8, "epilogue warps");
-    static_assert(WCOLS % EPI_COLS == 0 && HN % 64 == 0 && BN <= 256, "tile columns");
+    static_assert(BN <= 256 && SF_WORDS <= 1, "tile columns, one word of scales per stage and row");
     static_assert(ACC_BUFS == 1 || ACC_BUFS == 2, "accumulator buffers");
 };
+
+// A unit of work: rows [128 CG tm, ...) and HN columns of A from f0, or NARROW of them.  The first `whole` units are
+// tiles; the tiles behind them come as two halves each.
+struct GatedUnit {
+    int tm, f0;
+    bool narrow;
+};
+template <class Cfg>
+__device__ __forceinline__ GatedUnit gated_unit(const GatedParams &p, int u) {
+    const bool half = Cfg::CG == 2 && u >= p.whole;
+    const int t = half ? p.whole + (u - p.whole) / 2 : u;
+    GatedUnit w;
+    int tn;
+    tile_coords(t, p.tiles_m, p.group_m, w.tm, tn, p.tiles_n);
+    w.f0 = tn * Cfg::HN + (half ? ((u - p.whole) & 1) * Cfg::NARROW : 0);
+    w.narrow = Cfg::CG == 1 || half;
+    return w;
+}
+
+// k-block kb is the first of its group in the order in which a unit of this round walks K
+template <class Cfg>
+__device__ __forceinline__ bool group_begins(int kb, uint32_t round) {
+    const int edge = GB300_SERPENTINE_K && (round & 1u) ? Cfg::SF_GROUP - 1 : 0;
+    return kb % Cfg::SF_GROUP == edge;
+}
 
 // 32 values of a row quantised as one scale block: codes to shared memory (32-byte row `lane` of a
 // 32-byte-swizzled box), the block's scale code returned
@@ -127,7 +178,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     constexpr int CG = Cfg::CG;
     constexpr int STAGES = Cfg::STAGES;
     constexpr int BN = Cfg::BN;
-    constexpr int HN = Cfg::HN;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -142,7 +192,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
     uint64_t *cdrain = drain + 1;                         // COPIER only
-    uint64_t *sffull = cdrain + 1;                        // COPIER only
+    uint64_t *sffull = cdrain + 1;                        // COPIER only, as the next two
+    uint64_t *sfready = sffull + Cfg::SF_RING;
+    uint64_t *sfempty = sfready + Cfg::SF_RING;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Cfg::OFF_MISC + 4);
     const Waiter W{abort_flag, p.status, p.timeout_ns};
@@ -150,14 +202,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tmX);
         prefetch_tensormap(&tmW);
-        if constexpr (Cfg::SCALED) {
+        if constexpr (Cfg::PACKED) {
             prefetch_tensormap(&tmSFX);
             prefetch_tensormap(&tmSFW);
         }
         if (p.has_a) prefetch_tensormap(&tmA);
         if (p.has_z) prefetch_tensormap(&tmZ);
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1 + Cfg::COPIERS);        // the producer's arrival and each copier warp's commit
+            // the producer's arrival and, with packed scales, each copier warp's commit
+            mbar_init(&full[s], 1 + (Cfg::PACKED ? Cfg::COPIERS : 0));
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -166,7 +219,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
         mbar_init(drain, 1);
         if constexpr (Cfg::COPIER) {
-            for (int i = 0; i < STAGES; ++i) mbar_init(&sffull[i], 1);
+            for (int i = 0; i < Cfg::SF_RING; ++i) {
+                mbar_init(&sffull[i], 1);
+                mbar_init(&sfready[i], Cfg::COPIERS);
+                mbar_init(&sfempty[i], 1);
+            }
             mbar_init(cdrain, Cfg::COPIERS);
         }
         *abort_flag = 0;
@@ -180,9 +237,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     if constexpr (CG == 2) cluster_sync(); else __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
+    rows::wait_for_previous();
+    rows::let_next_launch();
 
-    const int tile0 = blockIdx.x / CG;
-    const int tile_step = gridDim.x / CG;
+    const int unit0 = blockIdx.x / CG;
+    const int unit_step = gridDim.x / CG;
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -190,57 +249,58 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             int s = 0;
             uint32_t ph = 0, round = 0;
             bool ok = true;
-            for (int t = tile0; ok && t < p.num_tiles; t += tile_step, ++round) {
-                int tm, tn;
-                tile_coords(t, p.tiles_m, p.group_m, tm, tn, p.tiles_n);
-                const int m0 = (tm * CG + (int)rank) * TILE_M;
-                const int f0 = tn * HN;
+            for (int n = unit0; ok && n < p.units; n += unit_step, ++round) {
+                const GatedUnit w = gated_unit<Cfg>(p, n);
+                const int m0 = (w.tm * CG + (int)rank) * TILE_M;
                 for (int j = 0; j < p.num_kb; ++j) {
                     const int kb = kb_at(j, 0, p.num_kb, round);
                     if (!W.wait(&empty[s], ph ^ 1u)) { ok = false; break; }
                     const bool withhold = p.fault == 1 && round == 0 && j == 0;
                     const uint32_t fb = smem_addr(&full[s]);
                     const uint32_t bar = CG == 1 ? fb : mapa_shared(fb, 0);      // the leader's
-                    if constexpr (Cfg::SCALED) {          // the scales first: the copier warps start on them
-                        if (rank == 0) mbar_arrive_expect_tx(&sffull[s], Cfg::TX_SF);
+                    if constexpr (Cfg::PACKED) {          // the scales first: the copier warps start on them
+                        if (rank == 0) mbar_arrive_expect_tx(&sffull[s], w.narrow ? Cfg::NARROW_TX_SF : Cfg::TX_SF);
                         const uint32_t sb = smem_addr(&sffull[s]);
                         const uint32_t sbar = CG == 1 ? sb : mapa_shared(sb, 0);
-                        const uint32_t dst = smem_addr(smem + Cfg::OFF_SF + s * (Cfg::SFA_BYTES + Cfg::SFB_BYTES));
-                        const int xr = checked_y(p.status, ((tm * CG + (int)rank) * p.num_kb + kb) * (Cfg::SFA_BYTES / 128),
-                                                 p.tiles_m * CG * p.num_kb * (Cfg::SFA_BYTES / 128));
-                        const int wr = checked_y(p.status, (tn * p.num_kb + kb) * (Cfg::SFB_BYTES / 128),
-                                                 p.tiles_n * p.num_kb * (Cfg::SFB_BYTES / 128));
-                        if constexpr (CG == 1) {
-                            tma_load_2d(dst, &tmSFX, sbar, 0, xr);
-                            tma_load_2d(dst + Cfg::SFA_BYTES, &tmSFW, sbar, 0, wr);
-                        } else {
-                            tma_load_2d_pair(dst, &tmSFX, sbar, 0, xr);
-                            tma_load_2d_pair(dst + Cfg::SFA_BYTES, &tmSFW, sbar, 0, wr);
-                        }
+                        auto load_sf = [&](uint32_t to, const CUtensorMap *m, int row) {
+                            if constexpr (CG == 1) tma_load_2d(to, m, sbar, 0, row);
+                            else tma_load_2d_pair(to, m, sbar, 0, row);
+                        };
+                        const uint32_t dst = smem_addr(smem + Cfg::OFF_SF + s * Cfg::SF_BLOCKS * 512);
+                        // 512-byte blocks, four rows of the packed scales: one per (128 rows of X, k-block) and
+                        // per (64 columns of A, k-block)
+                        load_sf(dst, &tmSFX, checked_y(p.status, ((w.tm * CG + (int)rank) * p.num_kb + kb) * 4,
+                                                       p.tiles_m * CG * p.num_kb * 4));
+#pragma unroll
+                        for (int i = 0; i < Cfg::HALVES; ++i)
+                            if (i == 0 || !w.narrow)      // (HALVES is 1 in a single CTA)
+                                load_sf(dst + 512 * (1 + i), &tmSFW,
+                                        checked_y(p.status, ((w.f0 / 64 + i) * p.num_kb + kb) * 4,
+                                                  p.tiles_n * CG * p.num_kb * 4));
                     }
-                    if (rank == 0 && !withhold) mbar_arrive_expect_tx(&full[s], Cfg::TX_AB);
+                    if (rank == 0 && !withhold) mbar_arrive_expect_tx(&full[s], w.narrow ? Cfg::NARROW_TX_AB : Cfg::TX_AB);
                     const uint32_t a_dst = smem_addr(smem + Cfg::OFF_A + s * Cfg::A_BYTES);
                     const uint32_t b_dst = smem_addr(smem + Cfg::OFF_B + s * Cfg::B_BYTES);
                     const int kx = checked_x<Cfg::ELEM_BYTES>(p.status, kb * Cfg::BK, p.num_kb * Cfg::BK);
                     const int my = checked_y(p.status, m0, p.tiles_m * CG * TILE_M);
                     if constexpr (CG == 1) tma_load_2d(a_dst, &tmX, bar, kx, my);
                     else tma_load_2d_pair(a_dst, &tmX, bar, kx, my);
-                    if constexpr (Cfg::BACK) {            // W2 [N][F]: a box of 64 F x 64 N per atom column
-                        const int n0 = f0 + (int)rank * Cfg::B_ROWS;
 #pragma unroll
-                        for (int i = 0; i < Cfg::B_ROWS / Cfg::ATOM_MN; ++i) {
-                            const int x = checked_x<2>(p.status, n0 + i * Cfg::ATOM_MN, p.tiles_n * HN);
+                    for (int i = 0; i < Cfg::BOXES; ++i) {
+                        if (w.narrow && i >= Cfg::NARROW_BOXES) break;
+                        const uint32_t to = b_dst + i * Cfg::BOX_BYTES;
+                        if constexpr (Cfg::BACK) {        // W2 [N][F]: 64 of F x 64 of N
+                            const int x = checked_x<2>(p.status, w.f0 + ((int)rank * (w.narrow ? Cfg::NARROW_BOXES : Cfg::BOXES) + i) * 64,
+                                                       p.tiles_n * Cfg::HN);
                             const int y = checked_y(p.status, kb * Cfg::BK, p.num_kb * Cfg::BK);
-                            if constexpr (CG == 1) tma_load_2d(b_dst + i * Cfg::ATOM_BYTES, &tmW, bar, x, y);
-                            else tma_load_2d_pair(b_dst + i * Cfg::ATOM_BYTES, &tmW, bar, x, y);
-                        }
-                    } else {                              // W [2][F][K]: HN rows of each half
-                        const int fy = checked_y(p.status, f0, p.tiles_n * HN);
-                        if constexpr (CG == 1) {
-                            tma_load_3d(b_dst, &tmW, bar, kx, fy, 0);
-                            tma_load_3d(b_dst + HN * 128, &tmW, bar, kx, fy, 1);
-                        } else {
-                            tma_load_3d_pair(b_dst, &tmW, bar, kx, fy, (int)rank);
+                            if constexpr (CG == 1) tma_load_2d(to, &tmW, bar, x, y);
+                            else tma_load_2d_pair(to, &tmW, bar, x, y);
+                        } else {                          // W [2][F][K]: 64 rows of one half
+                            const bool split = CG == 2 && w.narrow;       // g's rows in the leader, u's in its peer
+                            const int half = split ? (int)rank : i;
+                            const int y = checked_y(p.status, w.f0 + (split ? 0 : 64 * (int)rank), p.tiles_n * Cfg::HN);
+                            if constexpr (CG == 1) tma_load_3d(to, &tmW, bar, kx, y, half);
+                            else tma_load_3d_pair(to, &tmW, bar, kx, y, half);
                         }
                     }
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
@@ -254,36 +314,49 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             // N-contiguous B MMA_K rows of 128 bytes
             constexpr uint32_t B_LBO = Cfg::BACK ? Cfg::ATOM_BYTES : 16;
             constexpr uint32_t B_STEP = Cfg::BACK ? (Cfg::MMA_K * 128) >> 4 : 2;
-            int s = 0;
-            uint32_t ph = 0, acc_it = 0;
+            int s = 0, sg = 0;
+            uint32_t ph = 0, sgph = 0, acc_it = 0;
             bool ok = true;
-            for (int t = tile0; ok && t < p.num_tiles; t += tile_step, ++acc_it) {
+            for (int n = unit0; ok && n < p.units; n += unit_step, ++acc_it) {
+                const bool narrow = CG == 2 && n >= p.whole;
+                const uint32_t idesc = narrow ? p.idesc_narrow : p.idesc;
                 const uint32_t b = Cfg::ACC_BUFS == 2 ? (acc_it & 1u) : 0u;
                 const uint32_t aph = Cfg::ACC_BUFS == 2 ? ((acc_it >> 1) & 1u) : (acc_it & 1u);
                 if (!W.wait<CG == 2>(&tempty[b], aph ^ 1u)) { ok = false; break; }
                 tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + b * BN;
                 for (int j = 0; j < p.num_kb; ++j) {
+                    [[maybe_unused]] const int kb = kb_at(j, 0, p.num_kb, acc_it);
+                    if constexpr (Cfg::GROUPED) {         // a new group of scales
+                        if (j == 0 || group_begins<Cfg>(kb, acc_it))
+                            if (!W.wait(&sfready[sg], sgph)) { ok = false; break; }
+                    }
                     if (!W.wait(&full[s], ph)) { ok = false; break; }
                     tc_fence_after_sync();
                     const uint64_t ad = smem_desc(smem_addr(smem + Cfg::OFF_A + s * Cfg::A_BYTES), 16, 1024, SWZ_128B);
                     const uint64_t bd = smem_desc(smem_addr(smem + Cfg::OFF_B + s * Cfg::B_BYTES), B_LBO, 1024, SWZ_128B);
                     if constexpr (Cfg::SCALED) {
-                        const uint32_t sfa_t = tmem_base + Cfg::SF_COL0 + s * Cfg::SF_SLOT;
+                        const uint32_t sfa_t = tmem_base + Cfg::SF_COL0 + (Cfg::PACKED ? s : sg * Cfg::SF_GROUP + kb % Cfg::SF_GROUP) * Cfg::SF_SLOT;
                         const uint32_t sfb_t = sfa_t + 4 * Cfg::SF_WORDS;
 #pragma unroll
                         for (int k = 0; k < Cfg::BK / Cfg::MMA_K; ++k) {
                             const uint32_t w = (uint32_t)k / 4u, id = (uint32_t)k % 4u;
-                            mma_scaled<Cfg::KIND, CG>(d_tmem, ad + 2 * k, bd + 2 * k, p.idesc | (id << 4) | (id << 29),
+                            mma_scaled<Cfg::KIND, CG>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29),
                                                       sfa_t + 4 * w, sfb_t + 4 * Cfg::HALVES * w, (j != 0) | (k != 0));
                         }
                     } else {
 #pragma unroll
                         for (int k = 0; k < Cfg::BK / Cfg::MMA_K; ++k)
-                            mma_f16<CG>(d_tmem, ad + 2 * k, bd + B_STEP * k, p.idesc, (j != 0) | (k != 0));
+                            mma_f16<CG>(d_tmem, ad + 2 * k, bd + B_STEP * k, idesc, (j != 0) | (k != 0));
                     }
                     if constexpr (CG == 1) tc_commit<1>(smem_addr(&empty[s]));
                     else tc_commit_pair(smem_addr(&empty[s]), 0x3);
+                    if constexpr (Cfg::GROUPED) {
+                        if (j == p.num_kb - 1 || group_begins<Cfg>(kb_at(j + 1, 0, p.num_kb, acc_it), acc_it)) {
+                            tc_commit<1>(smem_addr(&sfempty[sg]));
+                            if (++sg == Cfg::SF_RING) { sg = 0; sgph ^= 1u; }
+                        }
+                    }
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
                 if (!ok) break;
@@ -296,12 +369,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
     } else if (Cfg::COPIER && warp >= Cfg::COPY_WARP) {
         // ---------------------------------------------------------- scale copies
-        if constexpr (Cfg::COPIER) {
+        if constexpr (Cfg::PACKED) {
             if (rank == 0 && lane == 0) {
+                // (a narrow tile copies what a whole one's second block left in the stage, which no MMA reads)
                 int s = 0;
                 uint32_t ph = 0;
                 bool ok = true;
-                for (int t = tile0; ok && t < p.num_tiles; t += tile_step) {
+                for (int n = unit0; ok && n < p.units; n += unit_step) {
                     for (int j = 0; j < p.num_kb; ++j) {
                         if (!W.wait(&sffull[s], ph)) { ok = false; break; }
                         tc_fence_after_sync();
@@ -312,8 +386,89 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         if (++s == STAGES) { s = 0; ph ^= 1u; }
                     }
                 }
+                // every copy this thread issued has finished before teardown
                 if constexpr (CG == 1) tc_commit<1>(smem_addr(cdrain));
                 else tc_commit_pair(smem_addr(cdrain), 0x1);
+                W.wait(cdrain, 0, false);
+            }
+        }
+        if constexpr (Cfg::GROUPED) {
+            const int part = warp - Cfg::COPY_WARP;       // this warp's blocks: part, part + COPIERS, ...
+            const int sfk = (p.K + rows::BLOCK - 1) / rows::BLOCK;
+            const int groups = (p.num_kb + 3) / 4;
+            // codes of the rows of this warp's blocks, 16 of each row: word i of a block is row 32 i + lane.  1.0
+            // stands for rows past the matrix
+            struct Group {
+                uint4 w[Cfg::WARP_SF_BLOCKS][4];
+            };
+            auto fetch = [&](int n, int g) {
+                Group r;
+                const GatedUnit w = gated_unit<Cfg>(p, n);
+#pragma unroll
+                for (int b = 0; b < Cfg::WARP_SF_BLOCKS; ++b) {
+                    const int block = part + b * Cfg::COPIERS;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        int64_t row = w.tm * TILE_M + 32 * i + lane;                      // 128 rows of X
+                        bool on = row < p.M;
+                        if (block > 0) {                                                  // 64 of g's rows, 64 of u's
+                            const int f = w.f0 + (block - 1) * 64 + 32 * (i % 2) + lane;
+                            row = (int64_t)(i / 2) * p.F + f;
+                            on = block < Cfg::SF_BLOCKS && f < p.F;
+                        }
+                        r.w[b][i] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                        if (on) r.w[b][i] = __ldg(reinterpret_cast<const uint4 *>((block == 0 ? p.sfx : p.sfw) + row * sfk) + g);
+                    }
+                }
+                return r;
+            };
+            int sg = 0;
+            uint32_t ph = 0, round = 0;
+            bool ok = true;
+            Group next = fetch(unit0 < p.units ? unit0 : 0, 0);
+            for (int n = unit0; ok && n < p.units; n += unit_step, ++round) {
+                const bool down = GB300_SERPENTINE_K && (round & 1u);
+                for (int i = 0; i < groups; ++i) {
+                    // the next group, or the next unit's first, is on its way while this one is written
+                    const Group now = next;
+                    const int after = down ? groups - 2 - i : i + 1;
+                    if (i + 1 < groups) next = fetch(n, after);
+                    else if (n + unit_step < p.units) next = fetch(n + unit_step, GB300_SERPENTINE_K && !down ? groups - 1 : 0);
+                    ok = __all_sync(0xffffffffu, W.wait(&sfempty[sg], ph ^ 1u));
+                    if (!ok) break;
+                    const uint32_t from = smem_addr(smem + Cfg::OFF_SF) + sg * Cfg::SF_GROUP * Cfg::SF_BLOCKS * 512;
+#pragma unroll
+                    for (int b = 0; b < Cfg::WARP_SF_BLOCKS; ++b) {
+                        const int block = part + b * Cfg::COPIERS;
+                        if (block >= Cfg::SF_BLOCKS) break;
+                        const uint4 *q = now.w[b];
+                        const uint32_t to = from + 512 * block + 16 * lane;
+                        st_shared_v4(to, q[0].x, q[1].x, q[2].x, q[3].x);
+                        st_shared_v4(to + Cfg::SF_BLOCKS * 512, q[0].y, q[1].y, q[2].y, q[3].y);
+                        st_shared_v4(to + 2 * Cfg::SF_BLOCKS * 512, q[0].z, q[1].z, q[2].z, q[3].z);
+                        st_shared_v4(to + 3 * Cfg::SF_BLOCKS * 512, q[0].w, q[1].w, q[2].w, q[3].w);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int k = 0; k < Cfg::SF_GROUP; ++k)
+#pragma unroll
+                            for (int b = 0; b < Cfg::WARP_SF_BLOCKS; ++b) {
+                                const int block = part + b * Cfg::COPIERS;           // X's, then W's
+                                if (block >= Cfg::SF_BLOCKS) break;
+                                tmem_cp_32x128b_warpx4<CG>(
+                                    tmem_base + Cfg::SF_COL0 + (sg * Cfg::SF_GROUP + k) * Cfg::SF_SLOT + 4 * block,
+                                    smem_desc(from + (k * Cfg::SF_BLOCKS + block) * 512, 512, 128, SWZ_NONE));
+                            }
+                        tc_commit<1>(smem_addr(&sfready[sg]));
+                    }
+                    if (++sg == Cfg::SF_RING) { sg = 0; ph ^= 1u; }
+                }
+            }
+            if (lane == 0) {                              // every copy this thread issued has finished before teardown
+                tc_commit<1>(smem_addr(cdrain));
                 W.wait(cdrain, 0, false);
             }
         }
@@ -336,17 +491,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 else mbar_arrive_remote(mapa_shared(smem_addr(&tempty[b]), 0));
             }
         };
-        for (int t = tile0; t < p.num_tiles; t += tile_step, ++acc_it) {
-            int tm, tn;
-            tile_coords(t, p.tiles_m, p.group_m, tm, tn, p.tiles_n);
+        for (int n = unit0; n < p.units; n += unit_step, ++acc_it) {
+            const GatedUnit w = gated_unit<Cfg>(p, n);
             const uint32_t b = Cfg::ACC_BUFS == 2 ? (acc_it & 1u) : 0u;
             const uint32_t aph = Cfg::ACC_BUFS == 2 ? ((acc_it >> 1) & 1u) : (acc_it & 1u);
-            const int m_warp = (tm * CG + (int)rank) * TILE_M + 32 * q;
-            const int f_warp = tn * HN + h * Cfg::WCOLS;
+            const int m_warp = (w.tm * CG + (int)rank) * TILE_M + 32 * q;
+            const int wchunks = w.narrow ? Cfg::NARROW_WCHUNKS : Cfg::WCHUNKS;
+            const int f_warp = w.f0 + h * wchunks * EPI_COLS;
             const int row = m_warp + lane;
-            const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + b * BN + h * Cfg::WCOLS;
+            // forward: g's columns of the warp's slice, u's are 64 further on; backward: da's
+            const int col = Cfg::BACK ? h * wchunks * EPI_COLS : (w.narrow ? 32 * h : 128 * h);
+            const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + b * BN + col;
             // chunks with a column of the matrix; none where the warp's rows are all past M
-            const int chunks = m_warp < p.M ? max(0, min(Cfg::WCHUNKS, (p.F - f_warp + EPI_COLS - 1) / EPI_COLS)) : 0;
+            const int chunks = m_warp < p.M ? max(0, min(wchunks, (p.F - f_warp + EPI_COLS - 1) / EPI_COLS)) : 0;
 
             // the staging is free again once the last chunk's boxes have been read
             auto begin_boxes = [&]() {
@@ -405,8 +562,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     uint32_t g[Cfg::WCHUNKS][32], u[Cfg::WCHUNKS][32];
 #pragma unroll
                     for (int c = 0; c < Cfg::WCHUNKS; ++c) {
+                        if (c >= wchunks) break;
                         tmem_ld_32x32b_x32(taddr + EPI_COLS * c, g[c]);
-                        tmem_ld_32x32b_x32(taddr + HN + EPI_COLS * c, u[c]);
+                        tmem_ld_32x32b_x32(taddr + 64 + EPI_COLS * c, u[c]);
                     }
                     tmem_ld_wait_all();
 #pragma unroll
@@ -419,13 +577,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     for (int c = 0; c < Cfg::WCHUNKS; ++c) finish(c, g[c], u[c]);
                 } else {
 #pragma unroll 1
-                    for (int c = 0; c < Cfg::WCHUNKS; ++c) {
+                    for (int c = 0; c < wchunks; ++c) {
                         uint32_t g[32], u[32];
                         tmem_ld_32x32b_x32(taddr + EPI_COLS * c, g);
-                        tmem_ld_32x32b_x32(taddr + HN + EPI_COLS * c, u);
+                        tmem_ld_32x32b_x32(taddr + 64 + EPI_COLS * c, u);
                         tmem_ld_wait(g);
                         tie_registers(u);
-                        if (c == Cfg::WCHUNKS - 1) release(b);
+                        if (c == wchunks - 1) release(b);
                         finish(c, g, u);
                     }
                 }
@@ -456,13 +614,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 if (!__all_sync(0xffffffffu, W.wait(&tfull[b], aph))) break;
                 tc_fence_after_sync();
 #pragma unroll 1
-                for (int c = 0; c < Cfg::WCHUNKS; ++c) {
+                for (int c = 0; c < wchunks; ++c) {
                     const Kept k = next;
-                    if (c + 1 < Cfg::WCHUNKS) next = fetch(c + 1);
+                    if (c + 1 < wchunks) next = fetch(c + 1);
                     uint32_t d[32];
                     tmem_ld_32x32b_x32(taddr + EPI_COLS * c, d);
                     tmem_ld_wait(d);
-                    if (c == Cfg::WCHUNKS - 1) release(b);
+                    if (c == wchunks - 1) release(b);
                     if (c >= chunks) continue;
                     begin_boxes();
                     const float sg = rows::scale_value(k.sg), su = rows::scale_value(k.su);
@@ -523,7 +681,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 // What the host does with an instance
 template <class Cfg>
 struct GatedInstance {
-    static GatedShape shape() { return {Cfg::HN, Cfg::STAGES, Cfg::SMEM_BYTES, Cfg::BK, Cfg::SFA_BYTES, Cfg::SFB_BYTES}; }
+    static GatedShape shape() { return {Cfg::HN, Cfg::STAGES, Cfg::SMEM_BYTES, Cfg::BK}; }
     static cudaError_t prepare(int *clusters) {
         const void *f = reinterpret_cast<const void *>(&gated_kernel<Cfg>);
         cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
@@ -536,10 +694,12 @@ struct GatedInstance {
     }
     static cudaError_t launch(int grid, const CUtensorMap *maps, const GatedParams &p, cudaStream_t stream) {
         cudaLaunchConfig_t lc = config(grid, stream);
-        cudaLaunchAttribute attr = cluster();
-        lc.attrs = &attr;
-        lc.numAttrs = 1;
-        return cudaLaunchKernelEx(&lc, gated_kernel<Cfg>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], p);
+        cudaLaunchAttribute attr[2] = {cluster(), {}};
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 2;
+        return cudaLaunchKernelEx(&lc, gated_kernel<Cfg>, maps[0], maps[1], maps[4], maps[5], maps[2], maps[3], p);
     }
 
 private:

@@ -71,6 +71,9 @@ __device__ __forceinline__ uint32_t times(uint32_t v, uint32_t f) {
 __device__ __forceinline__ uint32_t widen_even(uint32_t w) { return (w << 4 & 0x07F007F0u) | (w << 8 & 0x80008000u); }
 __device__ __forceinline__ uint32_t widen_odd(uint32_t w) { return (w >> 4 & 0x07F007F0u) | (w & 0x80008000u); }
 
+// bit 7 of each byte: the code is NaN (bits besides those may be set too)
+__device__ __forceinline__ uint32_t not_a_number(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
+
 __device__ __forceinline__ uint32_t lane_of(const uint4 &q, int i) { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
 
 // two fp16 values as two pairs of bf16 values that sum to them
@@ -144,10 +147,17 @@ __global__ void __launch_bounds__(WARPS * 32) few_kernel(const __grid_constant__
                         mma<X_BF16>(acc[i][j], g.z, u.z, g.w, u.w, v.z, v.w);
                     }
             } else {
+                uint32_t most = 0;
 #pragma unroll
                 for (int i = 0; i < G; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) nan[i][h] |= ((sf[s][i][h] + 1u) & 0x100u) >> 1;
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 &q = w[s][i][h];
+                        const uint32_t n0 = not_a_number(q.x) | not_a_number(q.y), n1 = not_a_number(q.z) | not_a_number(q.w);
+                        nan[i][h] |= n0 | n1 | ((sf[s][i][h] + 1u) & 0x100u) >> 1;
+                        most = max(most, sf[s][i][h]);
+                    }
+                const bool far = __any_sync(0xFFFFFFFFu, most > 134u);
 #pragma unroll
                 for (int o = 0; o < 4; ++o) {             // four k of each lane at a time
                     uint32_t b[NG][X_BF16 ? 1 : 2][2];
@@ -169,10 +179,14 @@ __global__ void __launch_bounds__(WARPS * 32) few_kernel(const __grid_constant__
                         uint32_t a[4];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t q = lane_of(w[s][i][h], o), lf = low_factor(sf[s][i][h]), hf = high_factor(sf[s][i][h]);
-                            nan[i][h] |= (q & 0x7F7F7F7Fu) + 0x01010101u;
-                            a[h] = times(times(widen_even(q), lf), hf);
-                            a[2 + h] = times(times(widen_odd(q), lf), hf);
+                            const uint32_t q = lane_of(w[s][i][h], o), f = low_factor(sf[s][i][h]);
+                            a[h] = times(widen_even(q), f);
+                            a[2 + h] = times(widen_odd(q), f);
+                            if (far) {
+                                const uint32_t rest = high_factor(sf[s][i][h]);
+                                a[h] = times(a[h], rest);
+                                a[2 + h] = times(a[2 + h], rest);
+                            }
                         }
 #pragma unroll
                         for (int j = 0; j < NG; ++j)

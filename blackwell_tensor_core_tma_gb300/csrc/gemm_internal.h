@@ -186,21 +186,25 @@ cudaError_t chain_launch(int out_bf16, int cta_group, int grid, const CUtensorMa
 // The product with the gated unit (gemm_gated.cu): parameters of one launch
 struct GatedParams {
     int M, F;
-    int tiles_m, tiles_n, num_tiles;
+    int tiles_m, tiles_n;
+    int units, whole;        // units of work: `whole` tiles, then the halves of the others
     int num_kb;
     int group_m;
     int has_a;               // A is written (always, forward)
     int has_z;               // forward: the checkpoint is kept; backward: always
     int a_8bit;              // forward: A in e4m3 with scales
     int out16;               // gemm_dtype of 16-bit outputs
-    uint32_t idesc;
+    uint32_t idesc, idesc_narrow;
     int *status;
     uint64_t timeout_ns;
     int fault;
+    int K;
+    const uint8_t *sfx, *sfw;            // forward, block-scaled: the operands' scale codes
     uint8_t *sfa, *sfck;                 // forward: scale codes out
     const uint8_t *ck, *sfck_in;         // backward: the checkpoint
 };
-enum GatedForm { GATED_F16 = 0, GATED_MXF8 = 1, GATED_BACK = 2 };
+// GATED_MXF8: scales read as they are (single CTAs); GATED_MXF8_PACKED: packed by sf_pack
+enum GatedForm { GATED_F16 = 0, GATED_MXF8 = 1, GATED_MXF8_PACKED = 2, GATED_BACK = 3 };
 // plan families: forward plans and backward ones
 constexpr int FAMILY_GATED = 5;
 constexpr int FAMILY_GATED_BACK = 6;
@@ -208,12 +212,11 @@ struct GatedShape {
     int tile_n;              // columns of A per tile
     int stages, smem;
     int bk;                  // K elements per stage
-    int sfa_bytes, sfb_bytes;
 };
 GatedShape gated_shape(GatedForm form, int cta_group);
 // set the kernel's shared-memory limit; CTAs (or CTA pairs) that run at once
 cudaError_t gated_prepare(GatedForm form, int cta_group, int *clusters);
-// maps: X, W, packed SFX, packed SFW, A, checkpoint (backward: DY, W2, -, -, A, DZ)
+// maps: X, W, A, checkpoint, packed SFX, packed SFW (backward: DY, W2, A, DZ)
 cudaError_t gated_launch(GatedForm form, int cta_group, int grid, const CUtensorMap *maps, const GatedParams &p,
                          cudaStream_t stream);
 
