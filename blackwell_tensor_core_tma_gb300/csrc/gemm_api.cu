@@ -6,6 +6,7 @@
 // shared-memory tile, passed to the kernel as a __grid_constant__ parameter)
 // are encoded with the driver's cuTensorMapEncodeTiled, fetched through the
 // runtime's entry-point query so that the library does not link libcuda.
+#include <algorithm>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -1075,6 +1076,37 @@ gemm_status gemm_chain_run_host(gemm_plan_t p, const void *A, const void *B, con
 
 namespace {
 
+// The form of a gated product: single CTAs with 128 x 64 (backward 128 x 128) tiles, whose K may be cut into slices, or CTA
+// pairs with 256 x 128 (256 x 256) ones.  Estimated time in microseconds = a launch + rounds of tiles x the longer of a
+// tile's epilogue and its k-blocks (+ the exchange of slices), constants fitted to 140 shapes of each kind of operand (M 32
+// to 4096, F 512 to 8192, K 256 to 8192), both forms of each measured; the rule's choice is within 0.2 % of the
+// better form on average, 8 % at most.  For example, bf16, single CTAs and pairs: 1024 x 2048 x 4096 33.8 and 23.6, 256 x
+// 4096 x 4096 18.9 and 19.9, 256 x 2048 x 4096 17.9 whole, 13.6 in two slices, and 19.3.
+struct GatedForms {
+    double launch1, epilogue1, tile1, kb1;    // single CTAs
+    double launch2, epilogue2, tile2, kb2;    // pairs
+    double half;                              // a round of halved tiles, of a whole one's time
+};
+GatedForms gated_forms(GatedForm form) {
+    if (form == GATED_BACK) return {3.6, 4.2, 1.2, 0.255, 3.6, 9.0, 5.0, 0.31, 0.75};
+    if (form == GATED_F16) return {2.9, 1.4, 0.1, 0.245, 3.0, 2.75, 0.6, 0.30, 0.85};
+    return {3.4, 1.2, 0.35, 0.375, 5.5, 2.9, 1.5, 0.33, 0.85};
+}
+constexpr double GATED_EXCHANGE = 2.4;
+constexpr int GATED_SLICE_KB = 8;             // k-blocks of the shortest slice: 4096 x 512 x 1024 7.5 us in none, 7.7 in two
+double gated_single_time(GatedForm form, int64_t tiles, int num_kb, int units, int slices) {
+    const GatedForms f = gated_forms(form);
+    const double rounds = slices > 1 ? 1.0 : (double)((tiles + units - 1) / units);
+    const int kb = (num_kb + slices - 1) / slices;
+    return f.launch1 + rounds * std::max(f.epilogue1, f.tile1 + f.kb1 * kb) + (slices > 1 ? GATED_EXCHANGE : 0.0);
+}
+double gated_pair_time(GatedForm form, int64_t tiles, int num_kb, int units) {
+    const GatedForms f = gated_forms(form);
+    const int64_t rest = tiles % units;
+    const double rounds = (double)(tiles / units) + (rest == 0 ? 0.0 : 2 * rest <= units ? f.half : 1.0);
+    return f.launch2 + rounds * std::max(f.epilogue2, f.tile2 + f.kb2 * num_kb);
+}
+
 // Tiles that are worked on whole.  A pair's last round that would keep half of the pairs or fewer busy has its tiles
 // halved, and then takes about half as long.
 int gated_whole_tiles(int tiles, int units, int cg) {
@@ -1106,24 +1138,40 @@ gemm_status gated_plan_create(gemm_plan_t *out, int family, int64_t M, int64_t F
     p->sm_count = prop.multiProcessorCount;
     p->timeout_ns = 1000000000ull;
     p->family = family;
-    p->splits = 1;
     const GatedForm form = gated_form(p);
-    int cg = M >= 1024 && F >= 512 ? 2 : 1;
-    if (flags & GEMM_FLAG_FORCE_1CTA) cg = 1;
-    if (flags & GEMM_FLAG_FORCE_2CTA) cg = 2;
-    int units = 0;
-    if (gated_prepare(form, cg, &units) != cudaSuccess || units <= 0) {
+    // single CTAs with block scales have two forms: whichever a run takes, its tiles and slices are the same
+    auto prepare = [&](int group, int slices) {      // clusters that run at once, 0 where a call failed
+        int n = 0, m = 0;
+        if (gated_prepare(form, group, slices, &n) != cudaSuccess) return 0;
+        if (group == 2 || !block_scaled) return n;
+        return gated_prepare(GATED_MXF8, group, slices, &m) == cudaSuccess ? std::min(n, m) : 0;
+    };
+    auto tiles_of = [&](const GatedShape &shape, int group) {
+        return (M + TILE_M * group - 1) / (TILE_M * group) * ((F + shape.tile_n - 1) / shape.tile_n);
+    };
+    int units = prepare(1, 1), slices = 1;
+    const int pairs = prepare(2, 1);
+    if (units <= 0 || pairs <= 0) {
         delete p;
         return GEMM_ERR_CUDA;
     }
-    if (block_scaled && cg == 1) {        // the other form's shared-memory limit
-        int same = 0;
-        if (gated_prepare(GATED_MXF8, cg, &same) != cudaSuccess || same != units) {
-            delete p;
-            return GEMM_ERR_CUDA;
-        }
+    GatedShape sh = gated_shape(form, 1, 1);
+    const int num_kb = (int)((K + sh.bk - 1) / sh.bk);
+    const int64_t singles = tiles_of(sh, 1);
+    // the most slices that leave every tile's cluster running at once
+    for (int s = 2; s <= 8 && num_kb >= GATED_SLICE_KB * s; s *= 2)
+        if (singles * s <= units && singles <= prepare(1, s)) slices = s;
+    const GatedShape wide = gated_shape(form, 2, 1);
+    const bool pair = gated_pair_time(form, tiles_of(wide, 2), num_kb, pairs) <
+                      gated_single_time(form, singles, num_kb, units, slices);
+    const int cg = flags & GEMM_FLAG_FORCE_1CTA ? 1 : flags & GEMM_FLAG_FORCE_2CTA ? 2 : pair ? 2 : 1;
+    if (cg == 2) {
+        sh = wide;
+        units = pairs;
+        slices = 1;
+    } else if (slices > 1) {
+        sh = gated_shape(form, 1, slices);
     }
-    const GatedShape sh = gated_shape(form, cg);
     p->cta_group = cg;
     p->stages = sh.stages;
     p->smem = sh.smem;
@@ -1136,7 +1184,8 @@ gemm_status gated_plan_create(gemm_plan_t *out, int family, int64_t M, int64_t F
     p->capacity = units;
     p->whole = gated_whole_tiles(p->tiles, units, cg);
     const int work = 2 * p->tiles - p->whole;
-    p->grid = cg * (work < units ? work : units);
+    p->splits = slices;
+    p->grid = slices > 1 ? p->tiles * slices : cg * (work < units ? work : units);
     p->group_m = cg == 2 ? GB300_GROUP_M_PAIRS : GB300_GROUP_M_SINGLE;
     bool ok = cudaMalloc(&p->status, sizeof(int)) == cudaSuccess &&
               cudaMemset(p->status, 0, sizeof(int)) == cudaSuccess;
@@ -1194,6 +1243,7 @@ gemm_status gated_launch_plan(gemm_plan *p, GatedForm form, GatedParams &gp, cud
     gp.whole = p->whole;
     gp.units = 2 * p->tiles - p->whole;
     gp.num_kb = p->num_kb;
+    gp.slices = p->splits;
     gp.group_m = p->group_m;
     gp.out16 = p->d;
     const uint32_t m = (uint32_t)(TILE_M * p->cta_group), n = (uint32_t)(form == GATED_BACK ? p->tile_n : 2 * p->tile_n);

@@ -28,7 +28,9 @@
 //   * Backward: B is N-contiguous (W2 as the forward product has it), g and u come as 8-bit codes
 //     straight from memory, one chunk ahead of their use, and dz and a leave through TMA boxes.
 //
-// No split-K: sums would meet before the unit.  Every wait is bounded as in gemm_tc_kernel.
+//   * Where tiles are few, a tile's K is cut into slices over the single CTAs of a cluster, which exchange their sums
+//     before the unit: each finishes the share of the tile's 32 x 32 pieces that it owns, adding all slices in their order.
+// Every wait is bounded as in gemm_tc_kernel.
 #pragma once
 
 #include "gemm_kernel.cuh"
@@ -38,7 +40,7 @@ namespace gb300 {
 
 // Compile-time shape of one kernel instance: HN columns of A per tile; the rest as in TileCfg.
 template <int CG_, int KIND_, bool BACK_, int HN_, int STAGES_, int ACC_BUFS_, int EPI_WARPS_, int COPIERS_ = 0,
-          bool GROUPED_ = false>
+          bool GROUPED_ = false, bool SLICED_ = false>
 struct GatedCfg {
     static constexpr int CG = CG_;
     static constexpr int KIND = KIND_;
@@ -86,7 +88,6 @@ struct GatedCfg {
     static constexpr int SF_GROUP = PACKED ? 1 : 4;             // k-blocks of a group of scales
     static constexpr int SF_RING = PACKED ? STAGES : GROUPED ? 4 : 0;   // groups in shared and in tensor memory
     static constexpr int SF_BLOCKS = SF_WORDS * (1 + HALVES);   // 512-byte blocks of scales of a stage: X's, W's
-    static constexpr int WARP_SF_BLOCKS = COPIERS ? (SF_BLOCKS + COPIERS - 1) / COPIERS : 0;
     // an epilogue warp's staging: 32 rows of a chunk of each output (16-bit: 2 KiB, 8-bit: 1 KiB)
     static constexpr int EPI_BUF = BACK ? 3 * 2048 : 2048 + 2 * 1024;
     static constexpr int align1k(int x) { return (x + 1023) / 1024 * 1024; }
@@ -94,10 +95,19 @@ struct GatedCfg {
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
     static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
     static constexpr int OFF_EPI = align1k(OFF_SF + SF_RING * SF_GROUP * SF_BLOCKS * 512);
-    static constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_BUF;
+    // Tiles sliced along K over a cluster's CTAs (2, 4 or 8): of the tile's eight pieces of 32 rows and 64 columns a CTA owns
+    // 8 / slices.  Each has a staging buffer, and behind those the other slices' fp32 sums of it, 8 KiB each.
+    static constexpr bool SLICED = SLICED_;
+    static_assert(!SLICED || CG == 1, "slices over single CTAs");
+    static constexpr int MAX_SLICES = SLICED ? 8 : 1;
+    static constexpr int PIECE = 8192;
+    static constexpr int EPI_BYTES = SLICED ? EPI_BUF + 7 * PIECE : EPI_WARPS * EPI_BUF;
+    static_assert(!SLICED || (2 * (EPI_BUF + 3 * PIECE) <= EPI_BYTES && 4 * (EPI_BUF + PIECE) <= EPI_BYTES), "two, four slices");
+    static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
     // full[STAGES], empty[STAGES], tfull[2], tempty[2], drain, then with COPIER: cdrain and, per group of scales,
     // sffull (packed ones have landed), sfready (grouped ones are in tensor memory), sfempty (their MMAs are done)
-    static constexpr int NBAR = 2 * STAGES + 5 + (COPIER ? 3 * SF_RING + 1 : 0);
+    // and last, with slices, recv[4] (the other slices' sums of an owned piece have landed)
+    static constexpr int NBAR = 2 * STAGES + 5 + (COPIER ? 3 * SF_RING + 1 : 0) + (SLICED ? 4 : 0);
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;         // tmem base slot, abort flag
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;     // + alignment slack
     static constexpr int SF_SLOT = 4 * SF_WORDS * (1 + HALVES);
@@ -198,6 +208,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Cfg::OFF_MISC + 4);
     const Waiter W{abort_flag, p.status, p.timeout_ns};
+    uint64_t *recv = full + Cfg::NBAR - 4;                // SLICED only
+    // a tile's slice of K: k-blocks [kb0, kb1)
+    const int slices = Cfg::SLICED ? p.slices : 1, slice = Cfg::SLICED ? (int)cluster_ctarank() : 0;
+    const int kb0 = (int)((int64_t)slice * p.num_kb / slices), kb1 = (int)((int64_t)(slice + 1) * p.num_kb / slices);
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tmX);
@@ -221,11 +235,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if constexpr (Cfg::COPIER) {
             for (int i = 0; i < Cfg::SF_RING; ++i) {
                 mbar_init(&sffull[i], 1);
-                mbar_init(&sfready[i], Cfg::COPIERS);
+                mbar_init(&sfready[i], 1);
                 mbar_init(&sfempty[i], 1);
             }
             mbar_init(cdrain, Cfg::COPIERS);
         }
+        if constexpr (Cfg::SLICED)
+            for (int i = 0; i < 4; ++i) mbar_init(&recv[i], 1);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -234,14 +250,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         tmem_relinquish<CG>();
     }
     tc_fence_before_sync();
-    if constexpr (CG == 2) cluster_sync(); else __syncthreads();
+    if constexpr (CG == 2 || Cfg::SLICED) cluster_sync(); else __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
     rows::wait_for_previous();
     rows::let_next_launch();
 
-    const int unit0 = blockIdx.x / CG;
-    const int unit_step = gridDim.x / CG;
+    // (sliced tiles all run at once: a cluster has one)
+    const int unit0 = (int)blockIdx.x / (CG * slices);
+    const int unit_step = (int)gridDim.x / (CG * slices);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -252,8 +269,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             for (int n = unit0; ok && n < p.units; n += unit_step, ++round) {
                 const GatedUnit w = gated_unit<Cfg>(p, n);
                 const int m0 = (w.tm * CG + (int)rank) * TILE_M;
-                for (int j = 0; j < p.num_kb; ++j) {
-                    const int kb = kb_at(j, 0, p.num_kb, round);
+                for (int j = 0; j < kb1 - kb0; ++j) {
+                    const int kb = kb_at(j, kb0, kb1, round);
                     if (!W.wait(&empty[s], ph ^ 1u)) { ok = false; break; }
                     const bool withhold = p.fault == 1 && round == 0 && j == 0;
                     const uint32_t fb = smem_addr(&full[s]);
@@ -325,8 +342,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 if (!W.wait<CG == 2>(&tempty[b], aph ^ 1u)) { ok = false; break; }
                 tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + b * BN;
-                for (int j = 0; j < p.num_kb; ++j) {
-                    [[maybe_unused]] const int kb = kb_at(j, 0, p.num_kb, acc_it);
+                for (int j = 0; j < kb1 - kb0; ++j) {
+                    [[maybe_unused]] const int kb = kb_at(j, kb0, kb1, acc_it);
                     if constexpr (Cfg::GROUPED) {         // a new group of scales
                         if (j == 0 || group_begins<Cfg>(kb, acc_it))
                             if (!W.wait(&sfready[sg], sgph)) { ok = false; break; }
@@ -352,7 +369,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     if constexpr (CG == 1) tc_commit<1>(smem_addr(&empty[s]));
                     else tc_commit_pair(smem_addr(&empty[s]), 0x3);
                     if constexpr (Cfg::GROUPED) {
-                        if (j == p.num_kb - 1 || group_begins<Cfg>(kb_at(j + 1, 0, p.num_kb, acc_it), acc_it)) {
+                        if (j == kb1 - kb0 - 1 || group_begins<Cfg>(kb_at(j + 1, kb0, kb1, acc_it), acc_it)) {
                             tc_commit<1>(smem_addr(&sfempty[sg]));
                             if (++sg == Cfg::SF_RING) { sg = 0; sgph ^= 1u; }
                         }
@@ -376,7 +393,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 uint32_t ph = 0;
                 bool ok = true;
                 for (int n = unit0; ok && n < p.units; n += unit_step) {
-                    for (int j = 0; j < p.num_kb; ++j) {
+                    for (int j = 0; j < kb1 - kb0; ++j) {
                         if (!W.wait(&sffull[s], ph)) { ok = false; break; }
                         tc_fence_after_sync();
                         const uint32_t sfa_t = tmem_base + Cfg::SF_COL0 + s * Cfg::SF_SLOT;
@@ -393,78 +410,69 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             }
         }
         if constexpr (Cfg::GROUPED) {
-            const int part = warp - Cfg::COPY_WARP;       // this warp's blocks: part, part + COPIERS, ...
+            // Groups of four k-blocks, numbered over the CTA's units in the order in which the MMAs take them: copying warp c
+            // has every COPIERS-th, so that its loads for the next have that long to arrive (the fence between the words
+            // and the copies waits for them: with one warp for all groups a k-block took 0.4 us)
             const int sfk = (p.K + rows::BLOCK - 1) / rows::BLOCK;
-            const int groups = (p.num_kb + 3) / 4;
-            // codes of the rows of this warp's blocks, 16 of each row: word i of a block is row 32 i + lane.  1.0
-            // stands for rows past the matrix
+            const int first = kb0 / Cfg::SF_GROUP, groups = (kb1 - 1) / Cfg::SF_GROUP - first + 1;
+            // codes of the rows of a k-block group, 16 of each row: word i of block b is row 32 i + lane.  1.0 stands for
+            // rows past the matrix
             struct Group {
-                uint4 w[Cfg::WARP_SF_BLOCKS][4];
+                uint4 w[Cfg::SF_BLOCKS][4];
+                bool on;
             };
-            auto fetch = [&](int n, int g) {
+            auto fetch = [&](int64_t t) {                 // the t-th group
                 Group r;
+                const int turn = (int)(t / groups), i = (int)(t - (int64_t)turn * groups), n = unit0 + turn * unit_step;
+                r.on = n < p.units;
+                if (!r.on) return r;
+                const int g = first + (GB300_SERPENTINE_K && (turn & 1) ? groups - 1 - i : i);
                 const GatedUnit w = gated_unit<Cfg>(p, n);
 #pragma unroll
-                for (int b = 0; b < Cfg::WARP_SF_BLOCKS; ++b) {
-                    const int block = part + b * Cfg::COPIERS;
+                for (int b = 0; b < Cfg::SF_BLOCKS; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        int64_t row = w.tm * TILE_M + 32 * i + lane;                      // 128 rows of X
+                    for (int k = 0; k < 4; ++k) {
+                        int64_t row = w.tm * TILE_M + 32 * k + lane;                      // 128 rows of X
                         bool on = row < p.M;
-                        if (block > 0) {                                                  // 64 of g's rows, 64 of u's
-                            const int f = w.f0 + (block - 1) * 64 + 32 * (i % 2) + lane;
-                            row = (int64_t)(i / 2) * p.F + f;
-                            on = block < Cfg::SF_BLOCKS && f < p.F;
+                        if (b > 0) {                                                      // 64 of g's rows, 64 of u's
+                            const int f = w.f0 + (b - 1) * 64 + 32 * (k % 2) + lane;
+                            row = (int64_t)(k / 2) * p.F + f;
+                            on = f < p.F;
                         }
-                        r.w[b][i] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                        if (on) r.w[b][i] = __ldg(reinterpret_cast<const uint4 *>((block == 0 ? p.sfx : p.sfw) + row * sfk) + g);
+                        r.w[b][k] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                        if (on) r.w[b][k] = __ldg(reinterpret_cast<const uint4 *>((b == 0 ? p.sfx : p.sfw) + row * sfk) + g);
                     }
-                }
                 return r;
             };
-            int sg = 0;
-            uint32_t ph = 0, round = 0;
-            bool ok = true;
-            Group next = fetch(unit0 < p.units ? unit0 : 0, 0);
-            for (int n = unit0; ok && n < p.units; n += unit_step, ++round) {
-                const bool down = GB300_SERPENTINE_K && (round & 1u);
-                for (int i = 0; i < groups; ++i) {
-                    // the next group, or the next unit's first, is on its way while this one is written
-                    const Group now = next;
-                    const int after = down ? groups - 2 - i : i + 1;
-                    if (i + 1 < groups) next = fetch(n, after);
-                    else if (n + unit_step < p.units) next = fetch(n + unit_step, GB300_SERPENTINE_K && !down ? groups - 1 : 0);
-                    ok = __all_sync(0xffffffffu, W.wait(&sfempty[sg], ph ^ 1u));
-                    if (!ok) break;
-                    const uint32_t from = smem_addr(smem + Cfg::OFF_SF) + sg * Cfg::SF_GROUP * Cfg::SF_BLOCKS * 512;
+            Group next = fetch(warp - Cfg::COPY_WARP);
+            for (int64_t t = warp - Cfg::COPY_WARP; next.on; t += Cfg::COPIERS) {
+                const int slot = (int)(t % Cfg::SF_RING);
+                const uint32_t ph = (uint32_t)(t / Cfg::SF_RING) & 1u;
+                const uint32_t from = smem_addr(smem + Cfg::OFF_SF) + slot * Cfg::SF_GROUP * Cfg::SF_BLOCKS * 512;
+                const Group now = next;
+                next = fetch(t + Cfg::COPIERS);
+                if (!__all_sync(0xffffffffu, W.wait(&sfempty[slot], ph ^ 1u))) break;
 #pragma unroll
-                    for (int b = 0; b < Cfg::WARP_SF_BLOCKS; ++b) {
-                        const int block = part + b * Cfg::COPIERS;
-                        if (block >= Cfg::SF_BLOCKS) break;
-                        const uint4 *q = now.w[b];
-                        const uint32_t to = from + 512 * block + 16 * lane;
-                        st_shared_v4(to, q[0].x, q[1].x, q[2].x, q[3].x);
-                        st_shared_v4(to + Cfg::SF_BLOCKS * 512, q[0].y, q[1].y, q[2].y, q[3].y);
-                        st_shared_v4(to + 2 * Cfg::SF_BLOCKS * 512, q[0].z, q[1].z, q[2].z, q[3].z);
-                        st_shared_v4(to + 3 * Cfg::SF_BLOCKS * 512, q[0].w, q[1].w, q[2].w, q[3].w);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc_fence_after_sync();
+                for (int b = 0; b < Cfg::SF_BLOCKS; ++b) {
+                    const uint4 *q = now.w[b];
+                    const uint32_t to = from + 512 * b + 16 * lane;
+                    st_shared_v4(to, q[0].x, q[1].x, q[2].x, q[3].x);
+                    st_shared_v4(to + Cfg::SF_BLOCKS * 512, q[0].y, q[1].y, q[2].y, q[3].y);
+                    st_shared_v4(to + 2 * Cfg::SF_BLOCKS * 512, q[0].z, q[1].z, q[2].z, q[3].z);
+                    st_shared_v4(to + 3 * Cfg::SF_BLOCKS * 512, q[0].w, q[1].w, q[2].w, q[3].w);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tc_fence_after_sync();
 #pragma unroll
-                        for (int k = 0; k < Cfg::SF_GROUP; ++k)
+                    for (int k = 0; k < Cfg::SF_GROUP; ++k)
 #pragma unroll
-                            for (int b = 0; b < Cfg::WARP_SF_BLOCKS; ++b) {
-                                const int block = part + b * Cfg::COPIERS;           // X's, then W's
-                                if (block >= Cfg::SF_BLOCKS) break;
-                                tmem_cp_32x128b_warpx4<CG>(
-                                    tmem_base + Cfg::SF_COL0 + (sg * Cfg::SF_GROUP + k) * Cfg::SF_SLOT + 4 * block,
-                                    smem_desc(from + (k * Cfg::SF_BLOCKS + block) * 512, 512, 128, SWZ_NONE));
-                            }
-                        tc_commit<1>(smem_addr(&sfready[sg]));
-                    }
-                    if (++sg == Cfg::SF_RING) { sg = 0; ph ^= 1u; }
+                        for (int b = 0; b < Cfg::SF_BLOCKS; ++b)                          // X's, then W's
+                            tmem_cp_32x128b_warpx4<CG>(
+                                tmem_base + Cfg::SF_COL0 + (slot * Cfg::SF_GROUP + k) * Cfg::SF_SLOT + 4 * b,
+                                smem_desc(from + (k * Cfg::SF_BLOCKS + b) * 512, 512, 128, SWZ_NONE));
+                    tc_commit<1>(smem_addr(&sfready[slot]));
                 }
             }
             if (lane == 0) {                              // every copy this thread issued has finished before teardown
@@ -477,7 +485,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int e = warp - 2;
         const int q = warp & 3;                           // TMEM lane window of this warp
         const int h = e / 4;                              // which WCOLS-wide slice of the tile's columns
-        const uint32_t box = smem_addr(smem + Cfg::OFF_EPI + e * Cfg::EPI_BUF);
+        // slices: the CTA that owns the warp's piece (by lane window, with eight slices by column slice too), and its number there
+        const int owner = slices == 8 ? 4 * h + q : q * slices / 4;
+        const int own = slices == 8 ? 0 : slices == 4 ? h : 2 * (q % 2) + h;
+        const uint32_t box = smem_addr(smem + Cfg::OFF_EPI + (Cfg::SLICED ? own : e) * Cfg::EPI_BUF);
         const uint64_t stream_pol = l2_policy_evict_first();
         const int blocks = (p.F + rows::BLOCK - 1) / rows::BLOCK;
         const bool bf16 = p.out16 == GEMM_BF16;
@@ -513,6 +524,53 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             auto end_boxes = [&]() {
                 fence_proxy_async_smem();
                 __syncwarp();
+            };
+
+            // Slices: this warp's sums of 32 rows (v: a chunk's 32 columns of one or two accumulators) go to the piece's
+            // owner, or are added to the others' there.  False where the piece is another CTA's, or the kernel gives up.
+            auto exchange = [&](int c, uint32_t (&v)[Cfg::BACK ? 1 : 2][32]) -> bool {
+                if constexpr (!Cfg::SLICED) return true;
+                if (c >= chunks) return false;
+                const int sets = Cfg::BACK ? 1 : 2, set_bytes = 4096;
+                const uint32_t piece = smem_addr(smem + Cfg::OFF_EPI) + (uint32_t)(8 / slices * Cfg::EPI_BUF) +
+                                       (uint32_t)(own * (slices - 1) * Cfg::PIECE + c * sets * set_bytes + 16 * lane);
+                if (owner != slice) {
+                    const uint32_t to = mapa_shared(piece + (uint32_t)(slice - (slice > owner)) * Cfg::PIECE, (uint32_t)owner);
+                    const uint32_t bar = mapa_shared(smem_addr(&recv[own]), (uint32_t)owner);
+#pragma unroll
+                    for (int s = 0; s < sets; ++s)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            st_async_v4(to + s * set_bytes + 512 * i, v[s][4 * i], v[s][4 * i + 1], v[s][4 * i + 2],
+                                        v[s][4 * i + 3], bar);
+                    return false;
+                }
+                if (c == 0) {                             // all chunks of the piece
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&recv[own], (uint32_t)((slices - 1) * chunks * sets * set_bytes));
+                    if (!__all_sync(0xffffffffu, W.template wait<true>(&recv[own], 0))) return false;
+                }
+                float sum[Cfg::BACK ? 1 : 2][32] = {};
+                for (int k = 0; k < slices; ++k) {
+                    const uint32_t at = piece + (uint32_t)(k - (k > slice)) * Cfg::PIECE;
+#pragma unroll
+                    for (int s = 0; s < sets; ++s)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float4 f = make_float4(__uint_as_float(v[s][4 * i]), __uint_as_float(v[s][4 * i + 1]),
+                                                   __uint_as_float(v[s][4 * i + 2]), __uint_as_float(v[s][4 * i + 3]));
+                            if (k != slice) f = ld_shared_v4f(at + s * set_bytes + 512 * i);
+                            sum[s][4 * i] += f.x;
+                            sum[s][4 * i + 1] += f.y;
+                            sum[s][4 * i + 2] += f.z;
+                            sum[s][4 * i + 3] += f.w;
+                        }
+                }
+#pragma unroll
+                for (int s = 0; s < sets; ++s)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[s][i] = __float_as_uint(sum[s][i]);
+                return true;
             };
 
             if constexpr (!Cfg::BACK) {
@@ -578,13 +636,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 } else {
 #pragma unroll 1
                     for (int c = 0; c < wchunks; ++c) {
-                        uint32_t g[32], u[32];
-                        tmem_ld_32x32b_x32(taddr + EPI_COLS * c, g);
-                        tmem_ld_32x32b_x32(taddr + 64 + EPI_COLS * c, u);
-                        tmem_ld_wait(g);
-                        tie_registers(u);
+                        uint32_t v[2][32];
+                        tmem_ld_32x32b_x32(taddr + EPI_COLS * c, v[0]);
+                        tmem_ld_32x32b_x32(taddr + 64 + EPI_COLS * c, v[1]);
+                        tmem_ld_wait(v[0]);
+                        tie_registers(v[1]);
                         if (c == wchunks - 1) release(b);
-                        finish(c, g, u);
+                        if (exchange(c, v)) finish(c, v[0], v[1]);
                     }
                 }
             } else {
@@ -617,11 +675,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 for (int c = 0; c < wchunks; ++c) {
                     const Kept k = next;
                     if (c + 1 < wchunks) next = fetch(c + 1);
-                    uint32_t d[32];
-                    tmem_ld_32x32b_x32(taddr + EPI_COLS * c, d);
-                    tmem_ld_wait(d);
+                    uint32_t v[1][32];
+                    tmem_ld_32x32b_x32(taddr + EPI_COLS * c, v[0]);
+                    tmem_ld_wait(v[0]);
                     if (c == wchunks - 1) release(b);
-                    if (c >= chunks) continue;
+                    if (c >= chunks || !exchange(c, v)) continue;
                     begin_boxes();
                     const float sg = rows::scale_value(k.sg), su = rows::scale_value(k.su);
 #pragma unroll
@@ -632,7 +690,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         rows::decode(o % 2 ? make_uint2(uq.z, uq.w) : make_uint2(uq.x, uq.y), su, u);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float da = __uint_as_float(d[8 * o + i]);
+                            const float da = __uint_as_float(v[0][8 * o + i]);
                             float s1, s0;
                             rows::sigmoid(g[i], s1, s0);
                             const float gs = g[i] * s1;
@@ -671,7 +729,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         for (int i = 0; i < 64; ++i) __nanosleep(1000);
     }
     tc_fence_before_sync();
-    if constexpr (CG == 2) cluster_sync(); else __syncthreads();
+    // (slices: no CTA leaves while another may still send it sums)
+    if constexpr (CG == 2 || Cfg::SLICED) cluster_sync(); else __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc<CG>(tmem_base, 512);
@@ -682,19 +741,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 template <class Cfg>
 struct GatedInstance {
     static GatedShape shape() { return {Cfg::HN, Cfg::STAGES, Cfg::SMEM_BYTES, Cfg::BK}; }
-    static cudaError_t prepare(int *clusters) {
+    // the most clusters of `slices` CTAs (pairs: of two) that run at once
+    static cudaError_t prepare(int slices, int *clusters) {
         const void *f = reinterpret_cast<const void *>(&gated_kernel<Cfg>);
         cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t lc = config(2 * 1024, nullptr);
-        cudaLaunchAttribute attr = cluster();
+        cudaLaunchAttribute attr = cluster(slices);
         lc.attrs = &attr;
         lc.numAttrs = 1;
         return cudaOccupancyMaxActiveClusters(clusters, f, &lc);
     }
     static cudaError_t launch(int grid, const CUtensorMap *maps, const GatedParams &p, cudaStream_t stream) {
         cudaLaunchConfig_t lc = config(grid, stream);
-        cudaLaunchAttribute attr[2] = {cluster(), {}};
+        cudaLaunchAttribute attr[2] = {cluster(p.slices), {}};
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         lc.attrs = attr;
@@ -711,10 +771,10 @@ private:
         lc.stream = stream;
         return lc;
     }
-    static cudaLaunchAttribute cluster() {
+    static cudaLaunchAttribute cluster(int slices) {
         cudaLaunchAttribute a = {};
         a.id = cudaLaunchAttributeClusterDimension;
-        a.val.clusterDim.x = Cfg::CG;
+        a.val.clusterDim.x = Cfg::SLICED ? (unsigned)slices : (unsigned)Cfg::CG;
         a.val.clusterDim.y = a.val.clusterDim.z = 1;
         return a;
     }

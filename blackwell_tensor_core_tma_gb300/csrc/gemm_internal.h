@@ -189,6 +189,7 @@ struct GatedParams {
     int tiles_m, tiles_n;
     int units, whole;        // units of work: `whole` tiles, then the halves of the others
     int num_kb;
+    int slices;              // of K: CTAs of a cluster that share a tile (single CTAs; else 1)
     int group_m;
     int has_a;               // A is written (always, forward)
     int has_z;               // forward: the checkpoint is kept; backward: always
@@ -213,9 +214,9 @@ struct GatedShape {
     int stages, smem;
     int bk;                  // K elements per stage
 };
-GatedShape gated_shape(GatedForm form, int cta_group);
-// set the kernel's shared-memory limit; CTAs (or CTA pairs) that run at once
-cudaError_t gated_prepare(GatedForm form, int cta_group, int *clusters);
+GatedShape gated_shape(GatedForm form, int cta_group, int slices);
+// set the kernel's shared-memory limit; clusters of `slices` CTAs (or CTA pairs) that run at once
+cudaError_t gated_prepare(GatedForm form, int cta_group, int slices, int *clusters);
 // maps: X, W, A, checkpoint, packed SFX, packed SFW (backward: DY, W2, A, DZ)
 cudaError_t gated_launch(GatedForm form, int cta_group, int grid, const CUtensorMap *maps, const GatedParams &p,
                          cudaStream_t stream);

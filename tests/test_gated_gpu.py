@@ -322,3 +322,85 @@ def test_backward_wait_that_runs_out_is_reported():
             plan.set_timeout(1_000_000_000)
             DZ, _ = backward(plan, *args, M, F, "bf16", False)
             check_backward(DZ, None, DY, W2, g, u, "bf16")
+
+
+# ------------------------------------------------------------------------------------------- slices of K
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("M,F,K,slices", [(40, 80, 8256, 8), (300, 144, 4112, 8), (300, 528, 2064, 4),
+                                              (129, 1040, 8224, 4), (520, 784, 4176, 2)])
+def test_sliced_tiles(M, F, K, kind, slices):
+    """Few tiles: K in slices over a cluster's CTAs, whose sums meet before the unit."""
+    K = K if kind == "bf16" else 2 * K
+    (X, SX, x), (W, SW, w) = operands(M, F, K, kind)
+    out, again = Out(M, F, "e4m3", True), Out(M, F, "e4m3", True)
+    with gemm.GatedPlan(M, F, K, kind, "e4m3", scaled(kind)) as plan:
+        assert plan.info["splits"] == slices and plan.info["cta_group"] == 1
+        forward(plan, (dev(X), dev(SX)), (dev(W), dev(SW)), out)
+        forward(plan, (dev(X), dev(SX)), (dev(W), dev(SW)), again)
+    check(out, x, w, "e4m3", True)
+    for name in ("A", "SFA", "CK", "SFCK"):           # added in a fixed order
+        assert torch.equal(getattr(out, name).view(torch.uint8), getattr(again, name).view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("M,F,N,slices", [(40, 80, 8200, 8), (300, 272, 4104, 8), (300, 1040, 4104, 4),
+                                              (129, 2064, 8232, 4), (520, 1552, 4176, 2)])
+def test_sliced_backward(M, F, N, kind, slices):
+    DY, W2, (CK, SF, g, u) = backward_case(M, F, N, kind)
+    with gemm.GatedBackPlan(M, F, N, kind) as plan:
+        assert plan.info["splits"] == slices
+        DZ, A = backward(plan, dev(DY), dev(W2), dev(CK), dev(SF), M, F, kind, True)
+        check_backward(DZ, A, DY, W2, g, u, kind)
+        assert torch.equal(DZ, backward(plan, dev(DY), dev(W2), dev(CK), dev(SF), M, F, kind, False)[0])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "back"])
+def test_sliced_wait_that_runs_out_is_reported(kind):
+    M, F, K = 200, 80, 8192
+    if kind == "back":
+        DY, W2, (CK, SF, g, u) = backward_case(M, F, K, "bf16")
+        args = [dev(t) for t in (DY, W2, CK, SF)]
+        plan = gemm.GatedBackPlan(M, F, K)
+        run = lambda: plan.run(*args, torch.empty(M, 2 * F, dtype=torch.bfloat16, device="cuda"), None,
+                               torch.cuda.current_stream())
+    else:
+        (X, SX, x), (W, SW, w) = operands(M, F, K, kind)
+        X, SX, W, SW = (dev(t) for t in (X, SX, W, SW))
+        out = Out(M, F, "bf16", False)
+        plan = gemm.GatedPlan(M, F, K, kind, "bf16", scaled(kind))
+        run = lambda: plan.run(X, W, out.A, SX, SW, stream=torch.cuda.current_stream())
+    with plan:
+        assert plan.info["splits"] > 1
+        plan.set_timeout(2_000_000)
+        gemm.gemm_testing_set_fault(plan.handle, 1)
+        run()
+        assert plan.last_status() == gemm.GEMM_ERR_TIMEOUT
+        gemm.gemm_testing_set_fault(plan.handle, 0)
+        plan.set_timeout(1_000_000_000)
+        run()
+        assert plan.last_status() == gemm.GEMM_OK
+    if kind != "back":
+        check(out, x, w, "bf16", False)
+
+
+def test_scales_that_begin_anywhere():
+    """The same bits whether the scales' rows are read as they are or packed first."""
+    M, F, K = 100, 208, 1536
+    (X, SX, x), (W, SW, w) = operands(M, F, K, "e4m3")
+    X, SX, W, SW = (dev(t) for t in (X, SX, W, SW))
+    outs = [Out(M, F, "e4m3", True) for _ in range(3)]
+
+    def shifted(t, n):
+        b = torch.empty(t.numel() + n, dtype=torch.uint8, device="cuda")
+        b[n:] = t.view(-1)
+        return b[n:]
+
+    with gemm.GatedPlan(M, F, K, "e4m3", "e4m3", 1, ONE) as plan:
+        forward(plan, (X, SX), (W, SW), outs[0])
+        forward(plan, (X, shifted(SX, 1)), (W, SW), outs[1])
+        forward(plan, (X, SX), (W, shifted(SW, 8)), outs[2])
+    check(outs[0], x, w, "e4m3", True)
+    for o in outs[1:]:
+        for name in ("A", "SFA", "CK", "SFCK"):
+            assert torch.equal(getattr(outs[0], name).view(torch.uint8), getattr(o, name).view(torch.uint8))
