@@ -3,14 +3,17 @@
 //
 //   norm = sqrt(sum g^2),  c = g * min(1, limit / norm)
 //
-// Two kernels over the same chunks of CHUNK bytes.  The first leaves each CTA's sum of squares; in the second every CTA adds
-// those up, in the same order, so that no counter or second launch stands between them, and scales its chunks, the last
-// ones first: what the first kernel read last is still in L2.
+// Two kernels over the same rows of ROW bytes, each CTA with a range of consecutive ones.  The first leaves each CTA's sum of
+// squares; in the second every CTA adds those up, in the same order, so that no counter stands between them, and scales its
+// range from its end: what the first kernel read last is still in L2.  Few rows are left to one cluster, which does both at
+// once.
 //
-// A thread's sixteen-byte pieces of a chunk are squared and summed in fp32, scaled by a power of two where their
-// largest magnitude is far from one (a square stays within fp32's range), and everything above that is summed in 64 bits:
-// one 64-bit operation for 32 or 64 values, which the unit's rate has room for.
+// Sums: a thread squares and adds the values of a step (16 or 32 of them) in fp32 and adds that sum to a pair of fp32 numbers
+// whose sum carries twice fp32's digits.  Where a step's largest magnitude takes squares or sums past fp32's ends it is
+// scaled by a power of two first and its sum kept in 64 bits.  (In 64 bits throughout, the sums of a CTA's threads, the root
+// and the quotient alone took 5 us: the unit has two lanes per SM and clock.)
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_rows.cuh"
 
@@ -20,25 +23,43 @@ namespace {
 using namespace rows;
 
 constexpr int THREADS = 256;
-constexpr int PER_THREAD = 8;                              // 16-byte pieces of a chunk
-constexpr int CHUNK = THREADS * PER_THREAD * 16;           // bytes
-constexpr int MAX_PARTS = GEMM_CLIP_WORKSPACE / (int)sizeof(double);
+constexpr int ROW = THREADS * 16;                          // bytes: a 16-byte piece for each thread
+constexpr int STEP = 4;                                    // rows that a CTA takes at a time, of one tensor
+
+// ------------------------------------------------------------------------------------------- the list
 
 struct Entry {
     const uint8_t *g;
     uint8_t *c;
     int64_t n;
-    uint32_t first;          // its first chunk
+    uint32_t first;          // its first row
     int16_t type;
     int16_t apart;           // c is not a multiple of 16 bytes from g: written element by element
 };
-// The tensors of one launch, by value: a captured graph keeps them
+// What a CTA leaves: its sum of squares is high + low + rest
+struct Part {
+    float high, low;
+    double rest;             // of what fp32 does not hold
+};
+constexpr int MAX_PARTS = GEMM_CLIP_WORKSPACE / (int)sizeof(Part);
+// The tensors of one launch, by value: a captured graph keeps them.  start[b]: the tensor of CTA b's first row.  (Looked up
+// by halving in the launch's parameters, it costs a cache miss per step: 500 tensors of 1000 elements took 20 us, not 12.)
 template <int N>
 struct Table {
     int count;
-    uint32_t chunks;
+    uint32_t rows;
+    bool copies;             // some c is not its g
+    uint16_t start[MAX_PARTS];
     Entry e[N];
 };
+
+// A CTA's rows [begin, end)
+struct Range {
+    uint32_t begin, end;
+};
+__host__ __device__ __forceinline__ Range range_of(uint32_t rows, uint32_t cta, uint32_t ctas) {
+    return {(uint32_t)((uint64_t)rows * cta / ctas), (uint32_t)((uint64_t)rows * (cta + 1) / ctas)};
+}
 
 __device__ __forceinline__ float load_one(const uint8_t *g, int type, int64_t i) {
     if (type == GEMM_F32) return reinterpret_cast<const float *>(g)[i];
@@ -53,203 +74,384 @@ __device__ __forceinline__ void store_one(uint8_t *c, int type, int64_t i, float
 
 // A tensor's elements before its first 16-byte boundary, its whole pieces and the elements behind them
 struct Span {
-    int64_t head, pieces, tail;
+    int head, tail;
+    int64_t pieces;
     __device__ __forceinline__ Span(const Entry &e) {
         const int size = e.type == GEMM_F32 ? 4 : 2, per = 16 / size;
-        head = (int64_t)((16 - (reinterpret_cast<uintptr_t>(e.g) & 15)) & 15) / size;
-        if (head > e.n) head = e.n;
+        head = (int)((16 - (reinterpret_cast<uintptr_t>(e.g) & 15)) & 15) / size;
+        if (head > e.n) head = (int)e.n;
         pieces = (e.n - head) / per;
-        tail = e.n - head - pieces * per;
+        tail = (int)(e.n - head - pieces * per);
     }
 };
 
+// The pieces of a step: a thread's are thread, thread + THREADS, ..., zeros past the step's own.  While a step's are worked
+// on, those of the next one are on their way into the same registers.
+struct Pieces {
+    uint4 q[STEP];
+    __device__ __forceinline__ void load(int i, const uint4 *g, int left, int thread) {
+        q[i] = i * THREADS + thread < left ? g[i * THREADS + thread] : make_uint4(0, 0, 0, 0);
+    }
+};
+
+// A walk over a range's rows, up to STEP of one tensor at a time
 template <int N>
-__device__ __forceinline__ int entry_of(const Table<N> &t, uint32_t chunk) {      // the last one that begins at or before it
-    int low = 0, high = t.count - 1;
-    while (low < high) {
-        const int mid = (low + high + 1) / 2;
-        if (t.e[mid].first <= chunk) low = mid; else high = mid - 1;
+struct Walk {
+    const Table<N> &t;
+    int i;                   // the step's tensor
+    uint32_t row, rows;      // the step: rows of the list [row, row + rows)
+    const uint4 *g;          // its pieces
+    int left;                // how many
+    __device__ __forceinline__ Walk(const Table<N> &table, int start) : t(table), i(start), row(0), rows(0), g(nullptr), left(0) {}
+    __device__ __forceinline__ void up(uint32_t from, const Range &r) {            // the step that begins at `from`
+        while (i + 1 < t.count && t.e[i + 1].first <= from) ++i;
+        row = from;
+        const uint32_t end = i + 1 < t.count ? min(t.e[i + 1].first, r.end) : r.end;
+        rows = min((uint32_t)STEP, end - from);
+        place();
     }
-    return low;
-}
-
-// f(pair of values) for a piece
-template <typename F>
-__device__ __forceinline__ void each(const uint4 &q, int type, F f) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (type == GEMM_F32) {
-            f(__uint_as_float(w[i]));
-        } else if (type == GEMM_BF16) {
-            f(__uint_as_float(w[i] << 16));
-            f(__uint_as_float(w[i] & 0xFFFF0000u));
-        } else {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            f(v.x);
-            f(v.y);
-        }
+    __device__ __forceinline__ void down(uint32_t to, const Range &r) {            // the step that ends at `to`
+        while (i + 1 < t.count && t.e[i + 1].first < to) ++i;
+        while (t.e[i].first >= to) --i;
+        const uint32_t begin = max(t.e[i].first, r.begin);
+        rows = min((uint32_t)STEP, to - begin);
+        row = to - rows;
+        place();
     }
-}
+    __device__ __forceinline__ void none() { left = 0; }
 
-// The power of two that brings values of this largest magnitude to where their squares, and 64 of them together, are within
-// fp32's range with room below: fp32 loses nothing that counts beside the largest square
-__device__ __forceinline__ float shift_of(float amax) { return amax > 0x1p60f ? 0x1p-70f : amax < 0x1p-40f ? 0x1p100f : 1.f; }
-__device__ __forceinline__ double unshifted(float sum, float shift) {
-    const double back = shift == 1.f ? 1.0 : shift < 1.f ? 0x1p140 : 0x1p-200;
-    return (double)sum * back;
-}
-__device__ __forceinline__ double square_of(float v) { return (double)v * (double)v; }
-
-__device__ __forceinline__ double block_sum(double v) {            // the same order every time; valid in all threads
-    __shared__ double s[THREADS / 32];
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x / 32] = v;
-    __syncthreads();
-    double t = 0.0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) t += s[i];
-    return t;
-}
-
-template <int TYPE>
-__device__ __forceinline__ double squares(const uint4 *g, int64_t pieces) {
-    uint4 q[PER_THREAD];
-#pragma unroll
-    for (int i = 0; i < PER_THREAD; ++i) {
-        const int64_t at = i * THREADS + threadIdx.x;
-        q[i] = at < pieces ? g[at] : make_uint4(0, 0, 0, 0);
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER_THREAD; ++i) each(q[i], TYPE, [&](float v) { amax = fmaxf(amax, fabsf(v)); });
-    const float shift = shift_of(amax);
-    float sum[4] = {};
-#pragma unroll
-    for (int i = 0; i < PER_THREAD; ++i) {
-        float &s = sum[i % 4];
-        each(q[i], TYPE, [&](float v) { v *= shift; s = fmaf(v, v, s); });
-    }
-    return unshifted((sum[0] + sum[1]) + (sum[2] + sum[3]), shift);
-}
-
-template <int N>
-__global__ void __launch_bounds__(THREADS) clip_norm_kernel(const __grid_constant__ Table<N> t, double *parts) {
-    wait_for_previous();
-    let_next_launch();
-    double sum = 0.0;
-    for (uint32_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
-        const Entry &e = t.e[entry_of(t, chunk)];
+private:
+    __device__ __forceinline__ void place() {
+        const Entry &e = t.e[i];
         const Span s(e);
-        const int size = e.type == GEMM_F32 ? 4 : 2;
-        const uint32_t c = chunk - e.first;
-        const int64_t at = (int64_t)c * (THREADS * PER_THREAD);
-        const uint4 *g = reinterpret_cast<const uint4 *>(e.g + s.head * size) + at;
-        if (e.type == GEMM_F32) sum += squares<GEMM_F32>(g, s.pieces - at);
-        else if (e.type == GEMM_BF16) sum += squares<GEMM_BF16>(g, s.pieces - at);
-        else sum += squares<GEMM_F16>(g, s.pieces - at);
-        if (c == 0) {                                      // at most seven elements before and behind the pieces
-            if (threadIdx.x < s.head) sum += square_of(load_one(e.g, e.type, threadIdx.x));
-            if (threadIdx.x < s.tail) sum += square_of(load_one(e.g, e.type, e.n - s.tail + threadIdx.x));
+        const int64_t at = (int64_t)(row - e.first) * THREADS;
+        g = reinterpret_cast<const uint4 *>(e.g + s.head * (e.type == GEMM_F32 ? 4 : 2)) + at;
+        left = (int)max((int64_t)0, min(s.pieces - at, (int64_t)(rows * THREADS)));
+    }
+};
+
+// ------------------------------------------------------------------------------------------- sums
+
+// not zero, by its bits: a comparison in 64 bits takes the slow unit too
+__device__ __forceinline__ bool any_bits(double v) { return (__double2hiint(v) | __double2loint(v)) != 0; }
+
+// high + low, low what high's rounding left; and what fp32 does not hold
+struct Sum {
+    float high = 0.f, low = 0.f;
+    double rest = 0.0;
+    __device__ __forceinline__ void add(float v) {
+        const float s = high + v, z = s - high;
+        low += (high - (s - z)) + (v - z);
+        high = s;
+    }
+    __device__ __forceinline__ void add(const Part &p) {
+        add(p.high);
+        low += p.low;
+        if (any_bits(p.rest)) rest += p.rest;
+    }
+};
+__device__ __forceinline__ Sum warp_sum(Sum s) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        const float h = __shfl_xor_sync(0xFFFFFFFFu, s.high, o), l = __shfl_xor_sync(0xFFFFFFFFu, s.low, o);
+        // the same in both lanes of a pair
+        const float a = fmaxf(s.high, h), b = fminf(s.high, h), t = a + b;
+        s.low = (s.low + l) + (b - (t - a));
+        s.high = s.high != s.high || h != h ? s.high + h : t;
+    }
+    if (__any_sync(0xFFFFFFFFu, any_bits(s.rest))) {
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) s.rest += __shfl_xor_sync(0xFFFFFFFFu, s.rest, o);
+    }
+    return s;
+}
+// Over a CTA, in the same order every time; valid in all threads
+__device__ __forceinline__ Sum block_sum(const Sum &v) {
+    __shared__ Part warps[THREADS / 32];
+    const Sum w = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x / 32] = Part{w.high, w.low, w.rest};
+    __syncthreads();
+    Sum s;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) s.add(warps[i]);
+    return s;
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+// f(pair of values) for a piece
+template <int TYPE, typename F>
+__device__ __forceinline__ void pairs(const uint4 &q, F f) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (TYPE == GEMM_F32) {
+        f(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])));
+        f(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (TYPE == GEMM_BF16) f(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
+            else f(__half22float2(*reinterpret_cast<const __half2 *>(&w[i])));
         }
     }
-    sum = block_sum(sum);
-    if (threadIdx.x == 0) parts[blockIdx.x] = sum;
+}
+// The largest magnitude of a thread's values, NaN left out
+template <int TYPE>
+__device__ __forceinline__ float largest(const Pieces &p) {
+    if constexpr (TYPE == GEMM_F32) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < STEP; ++i) pairs<TYPE>(p.q[i], [&](float2 v) { m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))); });
+        return m;
+    } else {
+        using T2 = typename std::conditional<TYPE == GEMM_BF16, __nv_bfloat162, __half2>::type;
+        const uint32_t zero = 0;
+        T2 m = *reinterpret_cast<const T2 *>(&zero);
+#pragma unroll
+        for (int i = 0; i < STEP; ++i) {
+            const uint32_t w[4] = {p.q[i].x, p.q[i].y, p.q[i].z, p.q[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m = __hmax2(m, __habs2(*reinterpret_cast<const T2 *>(&w[k])));
+        }
+        return fmaxf(fabsf((float)m.x), fabsf((float)m.y));
+    }
+}
+
+// A step's squares.  With every magnitude at most 2^40, and the largest at least 2^-56, neither squares nor the sums of 2^43
+// of them leave fp32's range, and what squares below its normal numbers lose does not count beside the largest.
+template <int TYPE, typename W>
+__device__ __forceinline__ void add_squares(Pieces &p, const W &next, int thread, Sum &sum) {
+    float2 s[2] = {};
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) {
+        int k = 0;
+        pairs<TYPE>(p.q[i], [&](float2 v) { s[k] = fma2(v, v, s[k]); k ^= 1; });
+    }
+    const float amax = largest<TYPE>(p);
+    if (amax > 0x1p40f || (amax < 0x1p-56f && amax != 0.f)) {
+        const float shift = amax > 1.f ? 0x1p-70f : 0x1p90f;
+        float all = 0.f;
+#pragma unroll
+        for (int i = 0; i < STEP; ++i)
+            pairs<TYPE>(p.q[i], [&](float2 v) {
+                v.x *= shift;
+                v.y *= shift;
+                all = fmaf(v.x, v.x, fmaf(v.y, v.y, all));
+            });
+        sum.rest += (double)all * (amax > 1.f ? 0x1p140 : 0x1p-180);
+    } else {
+        sum.add((s[0].x + s[0].y) + (s[1].x + s[1].y));
+    }
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) p.load(i, next.g, next.left, thread);
+}
+__device__ __forceinline__ void add_square(float v, Sum &sum) {
+    const float a = fabsf(v);
+    if (a <= 0x1p40f && a >= 0x1p-56f) sum.add(v * v);
+    else if (v != 0.f) sum.rest += (double)v * (double)v;
+}
+
+// The squares of a range
+template <int N>
+__device__ __forceinline__ void norm_rows(const Table<N> &t, const Range &r, int start, int thread, Sum &sum) {
+    if (r.begin >= r.end) return;
+    Walk<N> next(t, start);
+    Pieces p;
+    next.up(r.begin, r);
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) p.load(i, next.g, next.left, thread);
+    for (uint32_t row = r.begin; row < r.end;) {
+        const Entry &e = t.e[next.i];
+        const bool first = row == e.first;
+        row += next.rows;
+        if (row < r.end) next.up(row, r); else next.none();
+        if (e.type == GEMM_F32) add_squares<GEMM_F32>(p, next, thread, sum);
+        else if (e.type == GEMM_BF16) add_squares<GEMM_BF16>(p, next, thread, sum);
+        else add_squares<GEMM_F16>(p, next, thread, sum);
+        if (first) {                                       // at most seven elements before and behind the pieces
+            const Span s(e);
+            if (thread < s.head) add_square(load_one(e.g, e.type, thread), sum);
+            if (thread < s.tail) add_square(load_one(e.g, e.type, e.n - s.tail + thread), sum);
+        }
+    }
 }
 
 // limit / norm as a product of two: where it is below fp32's normal numbers' upper part, a power of two and the rest
 struct Factor {
     float rest, power;
+    bool one;
     __device__ __forceinline__ float operator()(float v) const { return v * power * rest; }
 };
-
-template <int TYPE>
-__device__ __forceinline__ void scale(const uint4 *g, uint4 *c, int64_t pieces, const Factor &factor) {
-    uint4 q[PER_THREAD];
-#pragma unroll
-    for (int i = 0; i < PER_THREAD; ++i) {
-        const int64_t at = i * THREADS + threadIdx.x;
-        q[i] = at < pieces ? g[at] : make_uint4(0, 0, 0, 0);
+// min(1, limit / norm); a norm that is not a number makes a factor that is none
+__device__ __forceinline__ Factor factor_of(const Sum &s, float limit, float &norm) {
+    if (!any_bits(s.rest) && s.high >= 0x1p-100f) {            // at least the largest square, and at most 2^125
+        norm = sqrtf(s.high + s.low);
+        const bool one = norm <= limit;
+        const float power = limit < 0x1p-60f ? 0x1p-60f : 1.f;
+        return {one ? 1.f : limit / power / norm, one ? 1.f : power, one};
     }
+    const double exact = sqrt((double)s.high + (double)s.low + s.rest), ratio = (double)limit / exact;
+    norm = (float)exact;
+    const bool one = exact <= (double)limit;
+    const float power = ratio < 0x1p-100 ? 0x1p-100f : 1.f;
+    return {one ? 1.f : (float)(ratio / (double)power), one ? 1.f : power, one};
+}
+
+// ------------------------------------------------------------------------------------------- results
+
+template <int TYPE, typename W>
+__device__ __forceinline__ void scale_pieces(Pieces &p, uint4 *to, int left, const W &next, int thread, const Factor &factor) {
+    const float2 rest = make_float2(factor.rest, factor.rest), none = make_float2(-0.f, -0.f);      // x * rest + -0 is x * rest
 #pragma unroll
-    for (int i = 0; i < PER_THREAD; ++i) {
-        const int64_t at = i * THREADS + threadIdx.x;
+    for (int i = 0; i < STEP; ++i) {
         float v[8];
         int n = 0;
-        each(q[i], TYPE, [&](float f) { v[n++] = factor(f); });
-        if (at < pieces) {
-            if constexpr (TYPE == GEMM_F32)
-                c[at] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-            else if constexpr (TYPE == GEMM_BF16) c[at] = pack8(static_cast<const __nv_bfloat16 *>(nullptr), v);
-            else c[at] = pack8(static_cast<const __half *>(nullptr), v);
-        }
+        pairs<TYPE>(p.q[i], [&](float2 f) {
+            if (factor.power != 1.f) {
+                f.x *= factor.power;
+                f.y *= factor.power;
+            }
+            f = fma2(f, rest, none);
+            v[n++] = f.x;
+            v[n++] = f.y;
+        });
+        uint4 q;
+        if constexpr (TYPE == GEMM_F32)
+            q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else if constexpr (TYPE == GEMM_BF16) q = pack8(static_cast<const __nv_bfloat16 *>(nullptr), v);
+        else q = pack8(static_cast<const __half *>(nullptr), v);
+        if (i * THREADS + thread < left) to[i * THREADS + thread] = q;
+        p.load(i, next.g, next.left, thread);
     }
 }
 
+// A step's rows of a c that lies otherwise on its lines than g: element by element
+__device__ __forceinline__ void scale_apart(const Entry &e, uint32_t row, uint32_t rows, int thread, const Factor &factor) {
+    const Span s(e);
+    const int per = e.type == GEMM_F32 ? 4 : 8;
+    const int64_t at = (int64_t)row * THREADS, pieces = max((int64_t)0, min(s.pieces - at, (int64_t)(rows * THREADS)));
+    const int64_t begin = s.head + at * per;
+    for (int k = thread; k < pieces * per; k += THREADS)
+        store_one(e.c, e.type, begin + k, factor(load_one(e.g, e.type, begin + k)));
+}
+
+// A range scaled, its last rows first
 template <int N>
-__global__ void __launch_bounds__(THREADS)
-    clip_scale_kernel(const __grid_constant__ Table<N> t, const double *parts, int n, float limit, float *norm_out) {
-    wait_for_previous();
-    let_next_launch();
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < n; i += THREADS) sum += parts[i];
-    const double norm = sqrt(block_sum(sum));
-    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-    // a norm that is not a number makes a factor that is none
-    const double ratio = norm <= (double)limit ? 1.0 : (double)limit / norm;
-    const float power = ratio < 0x1p-100 ? 0x1p-100f : 1.f;
-    const Factor factor{(float)(ratio / (double)power), power};
-    for (uint32_t i = blockIdx.x; i < t.chunks; i += gridDim.x) {
-        const uint32_t chunk = t.chunks - 1 - i;
-        const Entry &e = t.e[entry_of(t, chunk)];
-        if (!e.c || (ratio == 1.0 && e.c == e.g)) continue;
-        const Span s(e);
-        const int size = e.type == GEMM_F32 ? 4 : 2;
-        const uint32_t c = chunk - e.first;
-        const int64_t at = (int64_t)c * (THREADS * PER_THREAD);
-        if (e.apart) {
-            const int64_t per = 16 / size, first = s.head + at * per;
-            const int64_t last = min(s.head + s.pieces * per, first + THREADS * PER_THREAD * per);
-            for (int64_t k = first + threadIdx.x; k < last; k += THREADS)
-                store_one(e.c, e.type, k, factor(load_one(e.g, e.type, k)));
-        } else {
-            const uint4 *g = reinterpret_cast<const uint4 *>(e.g + s.head * size) + at;
-            uint4 *to = reinterpret_cast<uint4 *>(e.c + s.head * size) + at;
-            if (e.type == GEMM_F32) scale<GEMM_F32>(g, to, s.pieces - at, factor);
-            else if (e.type == GEMM_BF16) scale<GEMM_BF16>(g, to, s.pieces - at, factor);
-            else scale<GEMM_F16>(g, to, s.pieces - at, factor);
-        }
-        if (c == 0) {
-            if (threadIdx.x < s.head) store_one(e.c, e.type, threadIdx.x, factor(load_one(e.g, e.type, threadIdx.x)));
-            if (threadIdx.x < s.tail) {
-                const int64_t k = e.n - s.tail + threadIdx.x;
+__device__ __forceinline__ void scale_rows(const Table<N> &t, const Range &r, int start, int thread, const Factor &factor) {
+    if (r.begin >= r.end || (factor.one && !t.copies)) return;
+    Walk<N> next(t, start);
+    Pieces p;
+    auto down = [&](uint32_t to) {                         // nothing to load where nothing is written, or apart
+        next.down(to, r);
+        const Entry &e = t.e[next.i];
+        if (!e.c || e.apart || (factor.one && e.c == e.g)) next.none();
+    };
+    down(r.end);
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) p.load(i, next.g, next.left, thread);
+    for (uint32_t row = r.end; row > r.begin;) {
+        const Entry &e = t.e[next.i];
+        const uint32_t rows = next.rows;
+        const int left = next.left;
+        uint4 *to = reinterpret_cast<uint4 *>(e.c + (reinterpret_cast<const uint8_t *>(next.g) - e.g));
+        row = next.row;
+        if (row > r.begin) down(row); else next.none();
+        if (e.type == GEMM_F32) scale_pieces<GEMM_F32>(p, to, left, next, thread, factor);
+        else if (e.type == GEMM_BF16) scale_pieces<GEMM_BF16>(p, to, left, next, thread, factor);
+        else scale_pieces<GEMM_F16>(p, to, left, next, thread, factor);
+        if (!e.c || (factor.one && e.c == e.g)) continue;
+        if (e.apart) scale_apart(e, row - e.first, rows, thread, factor);
+        if (row == e.first) {
+            const Span s(e);
+            if (thread < s.head) store_one(e.c, e.type, thread, factor(load_one(e.g, e.type, thread)));
+            if (thread < s.tail) {
+                const int64_t k = e.n - s.tail + thread;
                 store_one(e.c, e.type, k, factor(load_one(e.g, e.type, k)));
             }
         }
     }
 }
 
-// Tables by size: a launch copies all of its own
-constexpr int SMALL = 32, MIDDLE = 256, LARGE = 1000;
+// ------------------------------------------------------------------------------------------- kernels
 
-int64_t chunks_of(const gemm_clip_tensor &t) {             // at least one for a tensor that is not empty
-    const int64_t bytes = t.n * (t.type == GEMM_F32 ? 4 : 2);
-    return t.n == 0 ? 0 : std::max<int64_t>(1, (bytes + CHUNK - 1) / CHUNK);
+// Bound by memory, which the tensors pass three times.  CTAS_PER_SM of them run at once on an SM, and the grid is at most that
+// many: no second wave.  1 billion fp32 values: 1.77 ms, 6750 GB/s over the three passes (a copy's rate); 100.7 million 195 us,
+// 6190 GB/s; 40 million in 291 tensors of both types, copied, 66 us.  Steps of eight rows, four or six CTAs: within 3 %;
+// stores that leave L2 first, loads past L1: the same or slower.
+constexpr int CTAS_PER_SM = 5;
+template <int N>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) clip_norm_kernel(const __grid_constant__ Table<N> t, Part *parts) {
+    const Range r = range_of(t.rows, blockIdx.x, gridDim.x);
+    const int start = t.start[blockIdx.x];
+    Sum sum;
+    wait_for_previous();
+    let_next_launch();
+    norm_rows(t, r, start, threadIdx.x, sum);
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) parts[blockIdx.x] = Part{sum.high, sum.low, sum.rest};
 }
 
 template <int N>
-void fill(Table<N> &t, const gemm_clip_tensor *tensors, int64_t count) {
-    t.count = 0;
-    t.chunks = 0;
-    for (int64_t i = 0; i < count; ++i) {
-        const gemm_clip_tensor &from = tensors[i];
-        if (from.n == 0) continue;
-        const uintptr_t apart = reinterpret_cast<uintptr_t>(from.g) ^ reinterpret_cast<uintptr_t>(from.c);
-        t.e[t.count++] = Entry{static_cast<const uint8_t *>(from.g), static_cast<uint8_t *>(from.c), from.n, t.chunks,
-                               (int16_t)from.type, (int16_t)((apart & 15) != 0)};
-        t.chunks += (uint32_t)chunks_of(from);
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
+    clip_scale_kernel(const __grid_constant__ Table<N> t, const Part *parts, int n, float limit, float *norm_out) {
+    const Range r = range_of(t.rows, blockIdx.x, gridDim.x);
+    const int start = t.start[blockIdx.x];
+    wait_for_previous();
+    let_next_launch();
+    Sum sum;
+    for (int k = threadIdx.x; k < n; k += THREADS) sum.add(parts[k]);
+    float norm;
+    const Factor factor = factor_of(block_sum(sum), limit, norm);
+    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+    scale_rows(t, r, start, threadIdx.x, factor);
+}
+
+// Few rows: one cluster does both, its CTAs' sums exchanged through shared memory.
+constexpr int FEW_CTAS = 8;
+template <int N>
+__global__ void __launch_bounds__(THREADS)
+    clip_few_kernel(const __grid_constant__ Table<N> t, float limit, float *norm_out) {
+    __shared__ Part sums[FEW_CTAS];
+    const Range r = range_of(t.rows, blockIdx.x, FEW_CTAS);
+    const int start = t.start[blockIdx.x];
+    Sum sum;
+    wait_for_previous();
+    let_next_launch();
+    norm_rows(t, r, start, threadIdx.x, sum);
+    sum = block_sum(sum);
+    if (threadIdx.x < FEW_CTAS) {
+        uint32_t to;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(to)
+            : "r"((uint32_t)__cvta_generic_to_shared(&sums[blockIdx.x])), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(sum.high), "f"(sum.low) : "memory");
+        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + 8), "d"(sum.rest) : "memory");
     }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    Sum all;
+#pragma unroll
+    for (int k = 0; k < FEW_CTAS; ++k) all.add(sums[k]);
+    float norm;
+    const Factor factor = factor_of(all, limit, norm);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+    scale_rows(t, r, start, threadIdx.x, factor);
+}
+
+// ------------------------------------------------------------------------------------------- launches
+
+// Tables by size: a launch copies all of its own
+constexpr int SMALL = 32, MIDDLE = 256, LARGE = 900;
+
+int64_t rows_of(const gemm_clip_tensor &t) {               // at least one for a tensor that is not empty
+    const int64_t bytes = t.n * (t.type == GEMM_F32 ? 4 : 2);
+    return t.n == 0 ? 0 : std::max<int64_t>(1, (bytes + ROW - 1) / ROW);
 }
 
 struct Call {
@@ -257,39 +459,66 @@ struct Call {
     int64_t count;
     float limit;
     float *norm;
-    double *parts;
+    Part *parts;
     int sms;
     cudaStream_t stream;
 };
+
+// Up to this many rows go to the single cluster: one launch where the host's two would be what a call costs (9 tensors of 20 011
+// values together 7.6 us in a queue of calls, two kernels 10.2; captured, 7.2 and 5.5)
+constexpr uint32_t FEW_ROWS = 64;
 
 // The tensors in launches of up to N: all norms' kernels, then all scalings'
 template <int N>
 cudaError_t clip(const Call &k) {
     const int launches = (int)std::max<int64_t>(1, (k.count + N - 1) / N);
-    const int most = std::max(1, std::min(4 * k.sms, MAX_PARTS / launches));
+    const int most = std::max(1, std::min(CTAS_PER_SM * k.sms, MAX_PARTS / launches));
     Table<N> t;
-    int parts = 0;
-    bool any = false;
+    int parts = 0, grid = 0;
+    bool any = false, few = false;
     auto table = [&](int l) {
-        const int64_t first = (int64_t)l * N;
-        fill(t, k.tensors + first, std::min<int64_t>(N, k.count - first));
+        t.count = 0;
+        t.rows = 0;
+        t.copies = false;
+        const int64_t first = (int64_t)l * N, last = std::min<int64_t>(first + N, k.count);
+        for (int64_t i = first; i < last; ++i) {
+            const gemm_clip_tensor &from = k.tensors[i];
+            if (from.n == 0) continue;
+            const uintptr_t apart = reinterpret_cast<uintptr_t>(from.g) ^ reinterpret_cast<uintptr_t>(from.c);
+            t.e[t.count++] = Entry{static_cast<const uint8_t *>(from.g), static_cast<uint8_t *>(from.c), from.n, t.rows,
+                                   (int16_t)from.type, (int16_t)((apart & 15) != 0)};
+            t.rows += (uint32_t)rows_of(from);
+            t.copies = t.copies || (from.c && from.c != from.g);
+            any = any || from.c;
+        }
+        few = launches == 1 && t.rows <= FEW_ROWS;
+        grid = few ? FEW_CTAS : (int)std::min<uint32_t>(std::max(1u, t.rows), (uint32_t)most);
+        for (int b = 0, i = 0; b < grid; ++b) {
+            const uint32_t begin = range_of(t.rows, (uint32_t)b, (uint32_t)grid).begin;
+            while (i + 1 < t.count && t.e[i + 1].first <= begin) ++i;
+            t.start[b] = (uint16_t)i;
+        }
     };
     for (int l = 0; l < launches; ++l) {
         table(l);
-        for (int i = 0; i < t.count; ++i) any = any || t.e[i].c;
-        const int grid = (int)std::min<uint32_t>(std::max(1u, t.chunks), (uint32_t)most);
+        if (few) {
+            const Launch c(FEW_CTAS, THREADS, 0, FEW_CTAS, k.stream);
+            return cudaLaunchKernelEx(&c.config, clip_few_kernel<N>, t, k.limit, k.norm);
+        }
         const cudaError_t e = launch(clip_norm_kernel<N>, grid, THREADS, 0, k.stream, t, k.parts + parts);
         if (e != cudaSuccess) return e;
         parts += grid;
     }
     for (int l = 0; l < launches; ++l) {
         if (launches > 1) table(l);
-        if (!any) t.chunks = 0;                            // the norm alone
-        const int grid = (int)std::min<uint32_t>(std::max(1u, t.chunks), (uint32_t)(4 * k.sms));
-        const cudaError_t e = launch(clip_scale_kernel<N>, grid, THREADS, 0, k.stream, t, (const double *)k.parts, parts, k.limit,
+        if (!any) {                                        // the norm alone
+            t.count = 0;
+            t.rows = 0;
+            grid = 1;
+        }
+        const cudaError_t e = launch(clip_scale_kernel<N>, grid, THREADS, 0, k.stream, t, (const Part *)k.parts, parts, k.limit,
                                      l == 0 ? k.norm : (float *)nullptr);
-        if (e != cudaSuccess) return e;
-        if (!any) break;
+        if (e != cudaSuccess || !any) return e;
     }
     return cudaSuccess;
 }
@@ -304,21 +533,21 @@ extern "C" gemm_status gemm_clip_run(int64_t count, const gemm_clip_tensor *tens
     if (count < 0 || !(limit >= 0.f) || (count > 0 && !tensors) || !NORM || !workspace || workspace_bytes < GEMM_CLIP_WORKSPACE)
         return GEMM_ERR_INVALID_ARG;
     if (count > (int64_t)LARGE * MAX_PARTS) return GEMM_ERR_UNSUPPORTED;
-    int64_t chunks = 0;
+    int64_t rows = 0;
     for (int64_t i = 0; i < count; ++i) {
         const gemm_clip_tensor &t = tensors[i];
         if (t.n < 0 || t.n > (int64_t)1 << 40 || (t.n > 0 && !t.g)) return GEMM_ERR_INVALID_ARG;
         if (t.type != GEMM_F32 && t.type != GEMM_BF16 && t.type != GEMM_F16) return GEMM_ERR_UNSUPPORTED;
         const uintptr_t size = t.type == GEMM_F32 ? 4 : 2;
         if (reinterpret_cast<uintptr_t>(t.g) % size || reinterpret_cast<uintptr_t>(t.c) % size) return GEMM_ERR_ALIGNMENT;
-        chunks += chunks_of(t);
+        rows += rows_of(t);
     }
-    if (chunks > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (rows > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(NORM) % 4 || !rows::aligned16(workspace)) return GEMM_ERR_ALIGNMENT;
     int sms = 0;
     const gemm_status st = rows::device_sms(&sms);
     if (st != GEMM_OK) return st;
-    const Call k{tensors, count, limit, NORM, static_cast<double *>(workspace), sms, reinterpret_cast<cudaStream_t>(cuda_stream)};
+    const Call k{tensors, count, limit, NORM, static_cast<Part *>(workspace), sms, reinterpret_cast<cudaStream_t>(cuda_stream)};
     const cudaError_t e = count <= SMALL ? clip<SMALL>(k) : count <= MIDDLE ? clip<MIDDLE>(k) : clip<LARGE>(k);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }

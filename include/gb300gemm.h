@@ -482,7 +482,7 @@ gemm_status gemm_gated_matvec_run(int64_t M, int64_t F, int64_t K, gemm_dtype x,
  * limit is infinite).  A c that equals its g is not written where nothing is scaled.  The workspace has GEMM_CLIP_WORKSPACE bytes
  * (less: GEMM_ERR_INVALID_ARG), 16-byte aligned, whose contents do not matter before or after; calls that may overlap on
  * the GPU need one each.  Results do not depend on timing, but on the list's order, the alignment of its tensors and
- * the GPU's SM count.  More than 2 million tensors or 2^46 bytes: GEMM_ERR_UNSUPPORTED.
+ * the GPU's SM count.  More than 900 000 tensors or 2^43 bytes: GEMM_ERR_UNSUPPORTED.
  */
 #define GEMM_CLIP_WORKSPACE 16384
 typedef struct {
