@@ -72,11 +72,7 @@ def test_every_code_and_the_scales_ends(x, M):
     for low, high in ((100, 120), (0, 40), (127, 145), (130, 136)):
         SF = torch.randint(low, high + 1, (2 * F, K // 32), generator=gen, dtype=torch.uint8)
         wide = ref.decode_e4m3(W) * ref.spread(SF, K)
-        z, size = gr.product(X.double(), wide)
         g, u, want, tg, tu, tol = gr.gated(X.double(), wide)
-        # weights below 2^-126 are bf16's subnormal numbers, off by half of 2^-133 each
-        lost = X.double().abs().sum(1, keepdim=True) * 2.0 ** -134
-        tol = tol + 1.2 * lost * (g.abs() + u.abs() + 2 * lost)
         A = run(M, F, K, x, "e4m3", X, W, SF)
         # past the type's largest value it is infinite
         limit = float(torch.finfo(gr.TORCH[x]).max)
@@ -85,6 +81,31 @@ def test_every_code_and_the_scales_ends(x, M):
         assert A[edge].isinf().all()
         gr.assert_output("a", torch.where(inside, A.double(), 0.0), None, torch.where(inside, want, 0.0),
                          torch.where(inside, tol, 0.0), x)
+
+
+@pytest.mark.parametrize("x_scale,low,high", [(2.0 ** -100, 190, 215), (2.0 ** 100, 20, 40), (2.0 ** -120, 127, 140), (2.0 ** 60, 60, 75)])
+def test_activations_far_from_one(x_scale, low, high):
+    """bf16 activations of any magnitude, tokens of a batch far apart, products that only together are ordinary numbers."""
+    M, F, K = 11, 24, 640
+    gen = torch.Generator().manual_seed(low)
+    W = torch.randint(0, 256, (2 * F, K), generator=gen, dtype=torch.uint8)
+    W[(W & 127) == 127] = 126
+    SF = torch.randint(low, high + 1, (2 * F, K // 32), generator=gen, dtype=torch.uint8)
+    X = torch.randn(M, K, generator=gen).double() * x_scale * torch.exp2(-2.0 * torch.arange(M).double())[:, None]
+    X = X.to(torch.bfloat16)
+    wide = ref.decode_e4m3(W) * ref.spread(SF, K)
+    g, u, want, _, _, tol = gr.gated(X.double(), wide)
+    A = run(M, F, K, "bf16", "e4m3", X, W, SF)
+    # off by 2^-39 of the largest of a token's 128 k, times the weights there
+    most = torch.stack([c.abs().amax(1) for c in X.double().split(128, 1)], 1)
+    heavy = torch.stack([c.abs().sum(1) for c in wide.split(128, 1)], 1)
+    lost = most @ heavy.t() * 2.0 ** -39
+    tol = tol + 1.2 * (lost[:, :F] * (u.abs() + lost[:, F:]) + lost[:, F:] * g.abs()) + 1e-42
+    limit = float(torch.finfo(torch.bfloat16).max)
+    inside = want.abs() + tol < limit
+    assert A[want.abs() - tol >= limit * (1 + 2.0 ** -8)].isinf().all()
+    gr.assert_output("a", torch.where(inside, A.double(), 0.0), None, torch.where(inside, want, 0.0), torch.where(inside, tol, 0.0),
+                     "bf16")
 
 
 def test_nonfinite_values_stay_their_own():
