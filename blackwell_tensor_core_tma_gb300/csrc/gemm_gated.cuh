@@ -155,14 +155,15 @@ __device__ __forceinline__ uint32_t quantise_chunk(const float (&v)[32], uint32_
 #pragma unroll
     for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));      // fmaxf drops NaN
     const uint32_t code = rows::scale_code(amax);
-    const float inv = rows::scale_inverse(code);
+    const float2 inv = rows::both(rows::scale_inverse(code));
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float *x = v + 16 * c + 4 * i;
-            w[i] = rows::e4m3x2(x[0] * inv, x[1] * inv) | rows::e4m3x2(x[2] * inv, x[3] * inv) << 16;
+            const float2 a = rows::mul2(make_float2(x[0], x[1]), inv), b = rows::mul2(make_float2(x[2], x[3]), inv);
+            w[i] = rows::e4m3x2(a.x, a.y) | rows::e4m3x2(b.x, b.y) << 16;
         }
         st_shared_v4(box + swz_off<32>(lane, c), w[0], w[1], w[2], w[3]);
     }
@@ -579,12 +580,18 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     const int f = f_warp + EPI_COLS * c;
                     float g[32], u[32], a[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        g[i] = __uint_as_float(gr[i]);
-                        u[i] = __uint_as_float(ur[i]);
-                        float s1, s0;
-                        rows::sigmoid(g[i], s1, s0);
-                        a[i] = g[i] * s1 * u[i];
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 g2 = make_float2(__uint_as_float(gr[i]), __uint_as_float(gr[i + 1]));
+                        const float2 u2 = make_float2(__uint_as_float(ur[i]), __uint_as_float(ur[i + 1]));
+                        float2 s1, s0;
+                        rows::sigmoid2(g2, s1, s0);
+                        const float2 a2 = rows::mul2(rows::mul2(g2, s1), u2);
+                        g[i] = g2.x;
+                        g[i + 1] = g2.y;
+                        u[i] = u2.x;
+                        u[i + 1] = u2.y;
+                        a[i] = a2.x;
+                        a[i + 1] = a2.y;
                     }
                     begin_boxes();
                     const int64_t block = (int64_t)row * blocks + f / rows::BLOCK;
@@ -689,14 +696,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         rows::decode(o % 2 ? make_uint2(gq.z, gq.w) : make_uint2(gq.x, gq.y), sg, g);
                         rows::decode(o % 2 ? make_uint2(uq.z, uq.w) : make_uint2(uq.x, uq.y), su, u);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float da = __uint_as_float(v[0][8 * o + i]);
-                            float s1, s0;
-                            rows::sigmoid(g[i], s1, s0);
-                            const float gs = g[i] * s1;
-                            a[i] = gs * u[i];
-                            dg[i] = da * u[i] * (s1 * (1.f + g[i] * s0));
-                            du[i] = da * gs;
+                        for (int i = 0; i < 8; i += 2) {
+                            using namespace rows;
+                            const float2 da = make_float2(__uint_as_float(v[0][8 * o + i]), __uint_as_float(v[0][8 * o + i + 1]));
+                            const float2 g2 = make_float2(g[i], g[i + 1]), u2 = make_float2(u[i], u[i + 1]);
+                            float2 s1, s0;
+                            sigmoid2(g2, s1, s0);
+                            const float2 gs = mul2(g2, s1), a2 = mul2(gs, u2), du2 = mul2(da, gs);
+                            const float2 dg2 = mul2(mul2(da, u2), mul2(s1, fma2(g2, s0, both(1.f))));
+                            a[i] = a2.x;
+                            a[i + 1] = a2.y;
+                            dg[i] = dg2.x;
+                            dg[i + 1] = dg2.y;
+                            du[i] = du2.x;
+                            du[i + 1] = du2.y;
                         }
                         auto put = [&](uint32_t to, const float (&v)[8]) {
                             const uint4 w = bf16 ? rows::pack8(static_cast<const __nv_bfloat16 *>(nullptr), v)

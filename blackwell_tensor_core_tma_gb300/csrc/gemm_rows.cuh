@@ -144,6 +144,25 @@ __device__ __forceinline__ void round_store(__nv_bfloat16 *p, bool on, float (&v
     unpack(p, q, v);
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // ------------------------------------------------------------- the gated unit
 
 // s = 1 / (1 + exp(-g)) and t = 1 - s = exp(-g) s, which a subtraction would leave few digits of.  With p = 2^-16 exp(-g / 2)
@@ -158,6 +177,19 @@ __device__ __forceinline__ void sigmoid(float g, float &s, float &t) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(p, p, 0x1p-32f)));
     s = r * 0x1p-32f;
     t = fminf(p * p, 0x1p126f) * r;
+}
+
+// The same for two values, operation by operation
+__device__ __forceinline__ void sigmoid2(float2 g, float2 &s, float2 &t) {
+    float2 p = mul2(g, both(-0.72134752f)), r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(p.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(p.y));
+    p = mul2(p, both(0x1p-16f));
+    const float2 d = fma2(p, p, both(0x1p-32f)), q = mul2(p, p);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+    s = mul2(r, both(0x1p-32f));
+    t = mul2(make_float2(fminf(q.x, 0x1p126f), fminf(q.y, 0x1p126f)), r);
 }
 
 // ------------------------------------------------------------- e4m3 with UE8M0
@@ -215,8 +247,9 @@ __device__ __forceinline__ void decode(uint2 q, float s, float (&v)[8]) {
         uint32_t h;                                   // two halves: every e4m3 value is exact in f16
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i / 2] >> (16 * (i & 1)))));
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        v[2 * i] = f.x * s;
-        v[2 * i + 1] = f.y * s;
+        const float2 m = mul2(f, both(s));
+        v[2 * i] = m.x;
+        v[2 * i + 1] = m.y;
     }
 }
 
