@@ -403,6 +403,9 @@ def gemm_gated_matvec_run(M: int, F: int, K: int, x, w, a, X, W, SFW, A, stream=
     return st
 
 
+TORCH_NAMES = {GEMM_F32: "torch.float32", GEMM_BF16: "torch.bfloat16", GEMM_F16: "torch.float16"}
+
+
 class ClipTensors:
     """The list of tensors of gemm_clip_run, laid out once: (g, c, type) with g and c torch tensors (c may be g or None), or
     (g, c, type, n) with addresses.  Keeps the tensors alive."""
@@ -415,7 +418,7 @@ class ClipTensors:
                 for x in (g, c):
                     if x is not None and not (x.is_contiguous() and x.numel() == g.numel() and x.dtype == g.dtype):
                         raise ValueError("tensors are contiguous, and c has g's size and type")
-                if g.element_size() != (4 if DTYPE.get(kind, kind) == GEMM_F32 else 2):
+                if TORCH_NAMES[DTYPE.get(kind, kind)] != str(g.dtype):
                     raise ValueError(f"{g.dtype} is not {kind}")
             entry.g, entry.c, entry.n, entry.type = _ptr(g), _ptr(c), n[0] if n else g.numel(), DTYPE.get(kind, kind)
 
