@@ -6,7 +6,8 @@
 // Two kernels over the same rows of ROW bytes, each CTA with a range of consecutive ones.  The first leaves each CTA's sum of
 // squares; in the second every CTA adds those up, in the same order, so that no counter stands between them, and scales its
 // range from its end: what the first kernel read last is still in L2.  Few rows are left to one cluster, which does both at
-// once.
+// once.  A list that is longer than a launch's parameters goes through several of the first kernel, whose CTAs add to the sums
+// that those before them left, and as many of the second.
 //
 // Sums: a thread squares and adds the values of a step (16 or 32 of them) in fp32 and adds that sum to a pair of fp32 numbers
 // whose sum carries twice fp32's digits.  Where a step's largest magnitude takes squares or sums past fp32's ends it is
@@ -226,16 +227,18 @@ __device__ __forceinline__ void add_squares(Pieces &p, const W &next, int thread
     }
     const float amax = largest<TYPE>(p);
     if (amax > 0x1p40f || (amax < 0x1p-56f && amax != 0.f)) {
-        const float shift = amax > 1.f ? 0x1p-70f : 0x1p90f;
-        float all = 0.f;
+        const float2 shift = both(amax > 1.f ? 0x1p-70f : 0x1p90f);
+        s[0] = s[1] = both(0.f);
 #pragma unroll
-        for (int i = 0; i < STEP; ++i)
+        for (int i = 0; i < STEP; ++i) {
+            int k = 0;
             pairs<TYPE>(p.q[i], [&](float2 v) {
-                v.x *= shift;
-                v.y *= shift;
-                all = fmaf(v.x, v.x, fmaf(v.y, v.y, all));
+                v = mul2(v, shift);
+                s[k] = fma2(v, v, s[k]);
+                k ^= 1;
             });
-        sum.rest += (double)all * (amax > 1.f ? 0x1p140 : 0x1p-180);
+        }
+        sum.rest += (double)((s[0].x + s[0].y) + (s[1].x + s[1].y)) * (amax > 1.f ? 0x1p140 : 0x1p-180);
     } else {
         sum.add((s[0].x + s[0].y) + (s[1].x + s[1].y));
     }
@@ -377,7 +380,7 @@ __device__ __forceinline__ void scale_rows(const Table<N> &t, const Range &r, in
 // stores that leave L2 first, loads past L1: the same or slower.
 constexpr int CTAS_PER_SM = 5;
 template <int N>
-__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) clip_norm_kernel(const __grid_constant__ Table<N> t, Part *parts) {
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) clip_norm_kernel(const __grid_constant__ Table<N> t, Part *parts, int before) {
     const Range r = range_of(t.rows, blockIdx.x, gridDim.x);
     const int start = t.start[blockIdx.x];
     Sum sum;
@@ -385,7 +388,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) clip_norm_kernel(const _
     let_next_launch();
     norm_rows(t, r, start, threadIdx.x, sum);
     sum = block_sum(sum);
-    if (threadIdx.x == 0) parts[blockIdx.x] = Part{sum.high, sum.low, sum.rest};
+    if (threadIdx.x == 0) {
+        if ((int)blockIdx.x < before) sum.add(parts[blockIdx.x]);          // of the launches before this one
+        parts[blockIdx.x] = Part{sum.high, sum.low, sum.rest};
+    }
 }
 
 template <int N>
@@ -462,16 +468,16 @@ constexpr uint32_t FEW_ROWS = 64;
 // The tensors in launches of up to N: all norms' kernels, then all scalings'
 template <int N>
 cudaError_t clip(const Call &k) {
-    const int launches = (int)std::max<int64_t>(1, (k.count + N - 1) / N);
-    const int most = std::max(1, std::min(CTAS_PER_SM * k.sms, MAX_PARTS / launches));
+    const int64_t launches = std::max<int64_t>(1, (k.count + N - 1) / N);
+    const int most = std::min(CTAS_PER_SM * k.sms, MAX_PARTS);
     Table<N> t;
     int parts = 0, grid = 0;
     bool any = false, few = false;
-    auto table = [&](int l) {
+    auto table = [&](int64_t l) {
         t.count = 0;
         t.rows = 0;
         t.copies = false;
-        const int64_t first = (int64_t)l * N, last = std::min<int64_t>(first + N, k.count);
+        const int64_t first = l * N, last = std::min<int64_t>(first + N, k.count);
         for (int64_t i = first; i < last; ++i) {
             const gemm_clip_tensor &from = k.tensors[i];
             if (from.n == 0) continue;
@@ -490,17 +496,17 @@ cudaError_t clip(const Call &k) {
             t.start[b] = (uint16_t)i;
         }
     };
-    for (int l = 0; l < launches; ++l) {
+    for (int64_t l = 0; l < launches; ++l) {
         table(l);
         if (few) {
             const Launch c(FEW_CTAS, THREADS, 0, FEW_CTAS, k.stream);
             return cudaLaunchKernelEx(&c.config, clip_few_kernel<N>, t, k.limit, k.norm);
         }
-        const cudaError_t e = launch(clip_norm_kernel<N>, grid, THREADS, 0, k.stream, t, k.parts + parts);
+        const cudaError_t e = launch(clip_norm_kernel<N>, grid, THREADS, 0, k.stream, t, k.parts, parts);
         if (e != cudaSuccess) return e;
-        parts += grid;
+        parts = std::max(parts, grid);
     }
-    for (int l = 0; l < launches; ++l) {
+    for (int64_t l = 0; l < launches; ++l) {
         if (launches > 1) table(l);
         if (!any) {                                        // the norm alone
             t.count = 0;
@@ -523,7 +529,6 @@ extern "C" gemm_status gemm_clip_run(int64_t count, const gemm_clip_tensor *tens
                                      size_t workspace_bytes, void *cuda_stream) {
     if (count < 0 || !(limit >= 0.f) || (count > 0 && !tensors) || !NORM || !workspace || workspace_bytes < GEMM_CLIP_WORKSPACE)
         return GEMM_ERR_INVALID_ARG;
-    if (count > (int64_t)LARGE * MAX_PARTS) return GEMM_ERR_UNSUPPORTED;
     int64_t rows = 0;
     for (int64_t i = 0; i < count; ++i) {
         const gemm_clip_tensor &t = tensors[i];
@@ -532,8 +537,8 @@ extern "C" gemm_status gemm_clip_run(int64_t count, const gemm_clip_tensor *tens
         const uintptr_t size = t.type == GEMM_F32 ? 4 : 2;
         if (reinterpret_cast<uintptr_t>(t.g) % size || reinterpret_cast<uintptr_t>(t.c) % size) return GEMM_ERR_ALIGNMENT;
         rows += rows_of(t);
+        if (rows > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
     }
-    if (rows > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(NORM) % 4 || !rows::aligned16(workspace)) return GEMM_ERR_ALIGNMENT;
     int sms = 0;
     const gemm_status st = rows::device_sms(&sms);

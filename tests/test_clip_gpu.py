@@ -10,8 +10,8 @@ from tests.test_norm_gpu import guarded
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-# A thread sums at most 16 squares in each of four fp32 sums and adds those (one rounding of each square, 16 of its sum, two of
-# the join); the rest is in 64 bits.  The root halves that; the result rounds once.
+# A thread adds at most 32 squares of a step in four fp32 sums of 8 (16-bit types; fused, one rounding apiece) and joins those (two);
+# what follows carries twice fp32's digits.  The root halves those 10 and rounds once: 6, and this is no less.
 NORM_REL = (19 / 2 + 1) * ref.U
 
 
