@@ -843,7 +843,7 @@ gemm_status gemm_plan_get_info(gemm_plan_t p, gemm_plan_info *info) {
     // block-scaled plans also launch the scale-packing kernel, split-K plans the D = C kernel
     // (a gated plan: where its scales need packing whatever the pointers)
     const bool scaled = is_gated(p) ? gated_scales_packed(p, nullptr, nullptr) : p->family != KIND_F16 && is_product(p);
-    info->launches_per_run = (scaled ? 2 : 1) + (p->splits > 1 ? 1 : 0);
+    info->launches_per_run = (scaled ? 2 : 1) + (p->splits > 1 && is_product(p) ? 1 : 0);
     info->splits = p->splits;
     info->stream_k = p->sk;
     info->sm_count = p->sm_count;
@@ -1266,9 +1266,9 @@ gemm_status gated_launch_plan(gemm_plan *p, GatedForm form, GatedParams &gp, cud
 
 gemm_status gated_sizes(gemm_plan_t *out, int64_t M, int64_t F, int64_t K, unsigned flags) {
     if (!out || M <= 0 || F <= 0 || K <= 0) return GEMM_ERR_INVALID_ARG;
-    if (M > INT32_MAX || F > (1 << 20) || K > INT32_MAX) return GEMM_ERR_INVALID_ARG;
-    // units of work and rows of packed scales are counted in 32 bits
-    if ((M + TILE_M) / TILE_M * ((F + 63) / 64) > INT32_MAX || ((M + F) / 32 + 16) * (K / 64 + 1) > INT32_MAX)
+    // coordinates, which run to the end of a tile, units of work and rows of packed scales are counted in 32 bits
+    if (M > INT32_MAX - 256 || F > (1 << 20) || K > INT32_MAX - 256) return GEMM_ERR_INVALID_ARG;
+    if ((M + TILE_M) / TILE_M * ((F + 63) / 64) > INT32_MAX / 2 || ((M + F) / 32 + 16) * (K / 64 + 1) > INT32_MAX)
         return GEMM_ERR_INVALID_ARG;
     if ((flags & GEMM_FLAG_FORCE_1CTA) && (flags & GEMM_FLAG_FORCE_2CTA)) return GEMM_ERR_INVALID_ARG;
     return GEMM_OK;

@@ -206,7 +206,7 @@ gemm_status gemm_plan_set_split_k(gemm_plan_t p, int splits);
  * with split-K.  enable = 1 (the default) uses it where it was measured to pay — fp32 D,
  * at least 64 K blocks per tile and fewer than 4 waves — and 0 never; other values
  * return GEMM_ERR_INVALID_ARG.  Runs of one stream-K plan must not overlap on the GPU
- * (they share the flags).  Chain plans (gemm_chain_plan_create) take it only on
+ * (they share the flags).  Gated plans do not take it (GEMM_ERR_UNSUPPORTED).  Chain plans (gemm_chain_plan_create) take it only on
  * request (enable = 1; it measured slower than whole tiles on the shapes tried): they
  * then share out the first product's K blocks the same way when their tiles make more
  * than one wave but fewer than 4 and not a whole number, with at least 16 K blocks per
@@ -223,7 +223,7 @@ gemm_status gemm_plan_set_stream_k(gemm_plan_t p, int enable);
  * first use and clears it; every later gemm_run and gemm_run_host of the plan then has
  * thread 0 of each CTA add its SM clock cycles (clock64) and globaltimer nanoseconds,
  * from kernel entry to exit, into that counter (two atomic adds per CTA).  enable = 0
- * stops counting; other values return GEMM_ERR_INVALID_ARG; chain plans return
+ * stops counting; other values return GEMM_ERR_INVALID_ARG; chain and gated plans return
  * GEMM_ERR_UNSUPPORTED.  gemm_plan_read_clock_meter synchronises the device, reads and
  * clears the counter, and returns *sm_mhz = cycles / nanoseconds * 1000 (the mean SM
  * clock over every counted CTA lifetime) and *cta_seconds (those lifetimes summed); both
@@ -428,14 +428,17 @@ gemm_status gemm_matvec_run(int64_t M, int64_t N, int64_t K, gemm_dtype x, gemm_
  * a plan's: GEMM_F16 or GEMM_BF16 with GEMM_SCALE_NONE, or GEMM_E4M3 with GEMM_SCALE_UE8M0_32 (SFX: M x ceil(K/32), SFW:
  * 2F x ceil(K/32)).  A and, with CK != NULL, the checkpoint of g and u are gemm_gate_run's (a: GEMM_E4M3 with SFA, GEMM_BF16
  * or GEMM_F16), made from the fp32 sums: no 16-bit z stands between.  F % 16 == 0 and 16-byte rows of X and W
- * (GEMM_ERR_ALIGNMENT), F <= 2^20.  The sums of an element run in an order that depends on K, and on the tile that it is in.
+ * (GEMM_ERR_ALIGNMENT); F <= 2^20, M and K < 2^31 - 256 (GEMM_ERR_INVALID_ARG).  A's and the checkpoint's values are those of the
+ * fp32 sums: a block whose largest magnitude lies within their error of 448 times a power of two may have either scale.
  *
- * A gated plan is a plan: gemm_plan_last_status, gemm_plan_get_info (tile_n: columns of A), gemm_plan_set_timeout,
- * gemm_plan_destroy and the flags work on it (it takes CTA pairs by the rule that gemm_gated_plan_create documents
- * in its info); gemm_run and gemm_run_host refuse it (GEMM_ERR_INVALID_ARG), and splits, stream-K and the clock meter
- * do not apply (GEMM_ERR_UNSUPPORTED).  A block-scaled plan packs SFX and SFW into memory of its own in each run: runs of one
- * plan must not overlap on the GPU.  Pointers are 16-byte aligned but for the scale codes.  X, W and their codes must not
- * overlap the outputs.
+ * A gated plan is a plan: gemm_plan_last_status, gemm_plan_get_info, gemm_plan_set_timeout, gemm_plan_destroy and the flags
+ * work on it.  It takes CTA pairs, single CTAs or, where tiles are few, single CTAs that share a tile's K, whichever its
+ * estimate has faster (info: tile_n, columns of A; splits, slices of K), and gives the same bits from run to run: an element's sums
+ * run in an order that depends on M, F, K, the type, the flags, the GPU's SM count and how many clusters it runs at once.  gemm_run and gemm_run_host refuse it
+ * (GEMM_ERR_INVALID_ARG), and gemm_plan_set_split_k (but 0 and 1), stream-K and the clock meter do not apply
+ * (GEMM_ERR_UNSUPPORTED).  A block-scaled plan may pack SFX and SFW into memory of its own in each run: runs of one
+ * plan must not overlap on the GPU.  Pointers are 16-byte aligned but for the scale codes (rows of scale codes that begin at
+ * multiples of 16 bytes save a small product the packing).  X, W and their codes must not overlap the outputs.
  */
 gemm_status gemm_gated_plan_create(gemm_plan_t *out, int64_t M, int64_t F, int64_t K, gemm_dtype ab, gemm_dtype a,
                                    int block_scaled, unsigned flags);
@@ -482,7 +485,7 @@ gemm_status gemm_gated_matvec_run(int64_t M, int64_t F, int64_t K, gemm_dtype x,
  * limit is infinite).  A c that equals its g is not written where nothing is scaled.  The workspace has GEMM_CLIP_WORKSPACE bytes
  * (less: GEMM_ERR_INVALID_ARG), 16-byte aligned, whose contents do not matter before or after; calls that may overlap on
  * the GPU need one each.  Results do not depend on timing, but on the list's order, the alignment of its tensors and
- * the GPU's SM count.  More than 900 000 tensors or 2^43 bytes: GEMM_ERR_UNSUPPORTED.
+ * the GPU's SM count.  More than 2^43 bytes: GEMM_ERR_UNSUPPORTED.
  */
 #define GEMM_CLIP_WORKSPACE 16384
 typedef struct {

@@ -12,7 +12,7 @@
  * (D comes out wrong, nothing faults) and the checks build of the library
  * reports GEMM_ERR_CHECK.  fault = 0 restores normal runs.  Returns
  * GEMM_ERR_INVALID_ARG for a NULL plan, another fault value, or fault = 2 on a
- * chain plan.
+ * chain plan or a gated one.
  */
 #ifndef GB300GEMM_TESTING_H
 #define GB300GEMM_TESTING_H
@@ -56,7 +56,7 @@ gemm_status gemm_testing_e4m3_pair_tile_n(int64_t M, int64_t N, int64_t K, gemm_
  * scales, its issue time, k-blocks, pieces, first and last MMA, the scale copier's wait
  * and issue, the epilogue warps' accumulator wait, TMEM loads, C wait, store work,
  * pieces and end).  NULL stops tracing.  GEMM_ERR_UNSUPPORTED in a build without the
- * trace or for a chain plan, GEMM_ERR_INVALID_ARG for a NULL plan or a buffer too small.
+ * trace or for a chain or gated plan, GEMM_ERR_INVALID_ARG for a NULL plan or a buffer too small.
  */
 int gemm_testing_trace_slots(void);
 gemm_status gemm_testing_set_trace(gemm_plan_t p, void *dev_buffer, int64_t bytes);

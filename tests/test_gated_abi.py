@@ -84,3 +84,9 @@ def test_clip_list_takes_contiguous_tensors_of_its_type():
         with pytest.raises(ValueError):
             gemm.clip_tensors([bad])
     assert len(gemm.clip_tensors([(g, None, "f32"), (g, g, "f32")])) == 2
+
+
+@pytest.mark.parametrize("sizes", [((1 << 31) - 256, 16, 16), (1, 16, (1 << 31) - 256), (1, (1 << 20) + 16, 16), (1 << 30, 1 << 20, 16)])
+def test_sizes_past_what_is_counted(sizes):
+    refused(INVALID, gemm.gemm_gated_plan_create, *sizes, "bf16", "bf16", 0, 0)
+    refused(INVALID, gemm.gemm_gated_back_plan_create, *sizes, "bf16", 0)

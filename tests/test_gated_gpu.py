@@ -404,3 +404,12 @@ def test_scales_that_begin_anywhere():
     for o in outs[1:]:
         for name in ("A", "SFA", "CK", "SFCK"):
             assert torch.equal(getattr(outs[0], name).view(torch.uint8), getattr(o, name).view(torch.uint8))
+
+
+@pytest.mark.parametrize("M,F,K,kind,flags,launches,slices", [
+    (4096, 1024, 512, "bf16", TWO, 1, 1), (4096, 1024, 512, "e4m3", TWO, 2, 1),      # pairs take packed scales
+    (128, 256, 512, "e4m3", ONE, 1, 1), (128, 256, 528, "e4m3", ONE, 2, 1),          # 17 codes a row: packed
+    (64, 128, 8192, "bf16", ONE, 1, 8), (64, 128, 8192, "e4m3", ONE, 1, 8), (64, 128, 8208, "e4m3", ONE, 2, 8)])
+def test_what_a_run_launches(M, F, K, kind, flags, launches, slices):
+    with gemm.GatedPlan(M, F, K, kind, "bf16", scaled(kind), flags) as plan:
+        assert plan.info["launches_per_run"] == launches and plan.info["splits"] == slices
