@@ -144,7 +144,8 @@ bool is_gated(const gemm_plan *p) { return p->family == FAMILY_GATED || p->famil
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 GatedForm gated_form(const gemm_plan *p) {
-    return p->family == FAMILY_GATED_BACK ? GATED_BACK : (p->block_scaled ? GATED_MXF8_PACKED : GATED_F16);
+    if (p->family == FAMILY_GATED_BACK) return p->tile_n == 64 ? GATED_BACK_NARROW : GATED_BACK;
+    return p->block_scaled ? GATED_MXF8_PACKED : GATED_F16;
 }
 // Single CTAs read the scales as they are where each row of them begins at a multiple of 16 bytes
 bool gated_scales_packed(const gemm_plan *p, const uint8_t *SFX, const uint8_t *SFW) {
@@ -1100,6 +1101,9 @@ double gated_single_time(GatedForm form, int64_t tiles, int num_kb, int units, i
     const int kb = (num_kb + slices - 1) / slices;
     return f.launch1 + rounds * std::max(f.epilogue1, f.tile1 + f.kb1 * kb) + (slices > 1 ? GATED_EXCHANGE : 0.0);
 }
+// Backward: tiles of half the width, where all run at once.  A tile's epilogue, which bounds a short sum (1300 instructions of a
+// warp for 32 columns), is on twice as many SMs: 200 x 1040 x 528 6.4 us, 8.4 in tiles of 128 columns.
+double gated_narrow_time(int num_kb) { return 4.2 + 0.237 * num_kb; }
 double gated_pair_time(GatedForm form, int64_t tiles, int num_kb, int units) {
     const GatedForms f = gated_forms(form);
     const int64_t rest = tiles % units;
@@ -1162,15 +1166,25 @@ gemm_status gated_plan_create(gemm_plan_t *out, int family, int64_t M, int64_t F
     for (int s = 2; s <= 8 && num_kb >= GATED_SLICE_KB * s; s *= 2)
         if (singles * s <= units && singles <= prepare(1, s)) slices = s;
     const GatedShape wide = gated_shape(form, 2, 1);
-    const bool pair = gated_pair_time(form, tiles_of(wide, 2), num_kb, pairs) <
-                      gated_single_time(form, singles, num_kb, units, slices);
+    double single = gated_single_time(form, singles, num_kb, units, slices);
+    const bool narrow = form == GATED_BACK && tiles_of(gated_shape(GATED_BACK_NARROW, 1, 1), 1) <= units &&
+                        gated_narrow_time(num_kb) < single;
+    if (narrow) single = gated_narrow_time(num_kb);
+    const bool pair = gated_pair_time(form, tiles_of(wide, 2), num_kb, pairs) < single;
     const int cg = flags & GEMM_FLAG_FORCE_1CTA ? 1 : flags & GEMM_FLAG_FORCE_2CTA ? 2 : pair ? 2 : 1;
     if (cg == 2) {
         sh = wide;
         units = pairs;
         slices = 1;
-    } else if (slices > 1) {
+    } else if (!narrow) {
         sh = gated_shape(form, 1, slices);
+    } else {
+        slices = 1;
+        sh = gated_shape(GATED_BACK_NARROW, 1, 1);
+        if (gated_prepare(GATED_BACK_NARROW, 1, 1, &units) != cudaSuccess || units <= 0) {
+            delete p;
+            return GEMM_ERR_CUDA;
+        }
     }
     p->cta_group = cg;
     p->stages = sh.stages;
@@ -1246,7 +1260,8 @@ gemm_status gated_launch_plan(gemm_plan *p, GatedForm form, GatedParams &gp, cud
     gp.slices = p->splits;
     gp.group_m = p->group_m;
     gp.out16 = p->d;
-    const uint32_t m = (uint32_t)(TILE_M * p->cta_group), n = (uint32_t)(form == GATED_BACK ? p->tile_n : 2 * p->tile_n);
+    const uint32_t m = (uint32_t)(TILE_M * p->cta_group);
+    const uint32_t n = (uint32_t)(p->family == FAMILY_GATED_BACK ? p->tile_n : 2 * p->tile_n);
     auto idesc = [&](uint32_t cols) {
         return p->block_scaled ? idesc_mxf8(m, cols, 0, 0)
                                   : idesc_f16(p->ab == GEMM_BF16 ? 1u : 0u, m, cols) | ((uint32_t)p->b_mn << 16);
@@ -1333,7 +1348,7 @@ gemm_status gemm_gated_back_run(gemm_plan_t p, const void *DY, const void *W2, c
     gp.has_z = 1;
     gp.ck = CK;
     gp.sfck_in = SFCK;
-    return gated_launch_plan(p, GATED_BACK, gp, reinterpret_cast<cudaStream_t>(cuda_stream));
+    return gated_launch_plan(p, gated_form(p), gp, reinterpret_cast<cudaStream_t>(cuda_stream));
 }
 
 // Test hook (declared in include/gb300gemm_testing.h): the pair tile-width rule alone.

@@ -49,8 +49,8 @@ struct GatedCfg {
     static constexpr int HN = HN_;
     static constexpr int BN = BACK ? HN : 2 * HN;               // columns of the MMA
     // the narrow form of a tile: all that a single CTA has, a pair's halved tile
-    static constexpr int NARROW = BACK ? 128 : 64;              // columns of A
-    static_assert(HN == NARROW * CG_, "a pair's tile is two narrow ones wide");
+    static constexpr int NARROW = HN / CG_;                     // columns of A
+    static_assert(BACK || NARROW == 64, "64 columns of g and of u");
     static constexpr int STAGES = STAGES_;
     static constexpr int ACC_BUFS = ACC_BUFS_;
     static constexpr int EPI_WARPS = EPI_WARPS_;
@@ -77,7 +77,7 @@ struct GatedCfg {
     static constexpr int SFB_BYTES = 512 * SF_WORDS * HALVES;
     static constexpr int BOX_BYTES = 64 * 128;                  // a box of B: 64 rows (backward: columns) of 128 bytes
     static constexpr int BOXES = B_BYTES / BOX_BYTES;
-    static constexpr int NARROW_BOXES = 128 / CG / 64;          // of a narrow tile: 128 columns of the MMA
+    static constexpr int NARROW_BOXES = (BACK ? NARROW : 2 * NARROW) / CG / 64;
     static constexpr int TX_AB = CG * (A_BYTES + B_BYTES);
     static constexpr int NARROW_TX_AB = CG * (A_BYTES + NARROW_BOXES * BOX_BYTES);
     static constexpr bool GROUPED = GROUPED_;                   // the copying warp packs the scales

@@ -204,8 +204,9 @@ struct GatedParams {
     uint8_t *sfa, *sfck;                 // forward: scale codes out
     const uint8_t *ck, *sfck_in;         // backward: the checkpoint
 };
-// GATED_MXF8: scales read as they are (single CTAs); GATED_MXF8_PACKED: packed by sf_pack
-enum GatedForm { GATED_F16 = 0, GATED_MXF8 = 1, GATED_MXF8_PACKED = 2, GATED_BACK = 3 };
+// GATED_MXF8: scales read as they are (single CTAs); GATED_MXF8_PACKED: packed by sf_pack; GATED_BACK_NARROW: single CTAs with
+// tiles of half the width
+enum GatedForm { GATED_F16 = 0, GATED_MXF8 = 1, GATED_MXF8_PACKED = 2, GATED_BACK = 3, GATED_BACK_NARROW = 4 };
 // plan families: forward plans and backward ones
 constexpr int FAMILY_GATED = 5;
 constexpr int FAMILY_GATED_BACK = 6;

@@ -413,3 +413,14 @@ def test_scales_that_begin_anywhere():
 def test_what_a_run_launches(M, F, K, kind, flags, launches, slices):
     with gemm.GatedPlan(M, F, K, kind, "bf16", scaled(kind), flags) as plan:
         assert plan.info["launches_per_run"] == launches and plan.info["splits"] == slices
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("M,F,N,tile", [(1000, 1296, 72, 128), (520, 1040, 648, 64), (129, 4112, 8, 64), (64, 16, 1000, 64)])
+def test_backward_widths_of_single_tiles(M, F, N, kind, tile):
+    """Tiles of 64 columns where all of them run at once, else of 128."""
+    DY, W2, (CK, SF, g, u) = backward_case(M, F, N, kind)
+    with gemm.GatedBackPlan(M, F, N, kind, ONE) as plan:
+        assert (plan.info["tile_n"], plan.info["splits"], plan.info["cta_group"]) == (tile, 1, 1)
+        DZ, A = backward(plan, dev(DY), dev(W2), dev(CK), dev(SF), M, F, kind, True)
+        check_backward(DZ, A, DY, W2, g, u, kind)
