@@ -20,7 +20,7 @@ using Mx8Sliced = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 4, 2, 8, 2, tr
 using Mx8SlicedPacked = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 4, 2, 8, 1, false, true>>;
 using BackPair = GatedInstance<GatedCfg<2, KIND_F16, true, 256, 5, 2, 8>>;
 using BackSingle = GatedInstance<GatedCfg<1, KIND_F16, true, 128, 5, 2, 8>>;
-using BackNarrow = GatedInstance<GatedCfg<1, KIND_F16, true, 64, 7, 2, 8>>;
+using BackNarrow = GatedInstance<GatedCfg<1, KIND_F16, true, 64, 7, 2, 8, 0, false, false, 2>>;
 using BackSliced = GatedInstance<GatedCfg<1, KIND_F16, true, 128, 5, 2, 8, 0, false, true>>;
 
 // f(instance) for a form, a CTA group and a number of slices

@@ -26,8 +26,12 @@
 //   * A thread owns a row; its chunk of 32 columns is one scale block of e4m3, so that a block's
 //     maximum is a thread's own.
 //   * Backward: B is N-contiguous (W2 as the forward product has it), g and u come as 8-bit codes
-//     straight from memory, one chunk ahead of their use, and dz and a leave through TMA boxes.
-//
+//     straight from memory, one chunk ahead of their use, and dz and a leave through TMA boxes.  (A tile ahead, or brought to L2
+//     a tile ahead: no faster.  4096 x 8192 x 2048 takes 114 us, the product alone 87; the traffic of the codes and that of dz
+//     are 11 to 12 us of the rest each, the arithmetic 1.5.)
+//   * Two warps may issue a CTA's MMAs, every other k-block each, into accumulators that the epilogue adds: one thread takes 450
+//     clocks for a k-block's four MMAs, their wait and their commit, whatever their N.  Backward tiles of 64 columns: 0.158 us per
+//     k-block, 0.237 with one.  (128 columns gain nothing: there the operands' way from L2 takes as long.)
 //   * Where tiles are few, a tile's K is cut into slices over the single CTAs of a cluster, which exchange their sums
 //     before the unit: each finishes the share of the tile's 32 x 32 pieces that it owns, adding all slices in their order.
 // Every wait is bounded as in gemm_tc_kernel.
@@ -40,7 +44,7 @@ namespace gb300 {
 
 // Compile-time shape of one kernel instance: HN columns of A per tile; the rest as in TileCfg.
 template <int CG_, int KIND_, bool BACK_, int HN_, int STAGES_, int ACC_BUFS_, int EPI_WARPS_, int COPIERS_ = 0,
-          bool GROUPED_ = false, bool SLICED_ = false>
+          bool GROUPED_ = false, bool SLICED_ = false, int ISSUERS_ = 1>
 struct GatedCfg {
     static constexpr int CG = CG_;
     static constexpr int KIND = KIND_;
@@ -57,7 +61,14 @@ struct GatedCfg {
     static constexpr int COPIERS = COPIERS_;
     static constexpr bool COPIER = COPIERS > 0;
     static constexpr int COPY_WARP = 2 + EPI_WARPS;
-    static constexpr int THREADS = 64 + 32 * EPI_WARPS + 32 * COPIERS;
+    // warps that issue MMAs, each every ISSUERS-th k-block into an accumulator of its own
+    static constexpr int ISSUERS = ISSUERS_;
+    static constexpr int SECOND_ISSUER = COPY_WARP + COPIERS;   // the first one is warp 1
+    static constexpr int THREADS = 32 * (SECOND_ISSUER + ISSUERS - 1);
+    static_assert(ISSUERS == 1 || (ISSUERS == 2 && CG == 1), "one or, in single CTAs, two");
+    // The barriers of loaded stages: an even number with two issuers, so that each has its own, whose phases it sees one after
+    // the other (a wait for one phase says nothing where the phase before it may be open)
+    static constexpr int FULLS = STAGES_ % ISSUERS == 0 ? STAGES_ : 2 * STAGES_;
     static_assert(EPI_WARPS == 8, "two epilogue warps per TMEM lane window");
     // chunks of A's columns one epilogue warp handles
     static constexpr int WCHUNKS = HN / 2 / EPI_COLS, NARROW_WCHUNKS = NARROW / 2 / EPI_COLS;
@@ -104,19 +115,20 @@ struct GatedCfg {
     static constexpr int EPI_BYTES = SLICED ? EPI_BUF + 7 * PIECE : EPI_WARPS * EPI_BUF;
     static_assert(!SLICED || (2 * (EPI_BUF + 3 * PIECE) <= EPI_BYTES && 4 * (EPI_BUF + PIECE) <= EPI_BYTES), "two, four slices");
     static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
-    // full[STAGES], empty[STAGES], tfull[2], tempty[2], drain, then with COPIER: cdrain and, per group of scales,
+    // full[FULLS], empty[STAGES], tfull[2], tempty[2], drain, then with COPIER: cdrain and, per group of scales,
     // sffull (packed ones have landed), sfready (grouped ones are in tensor memory), sfempty (their MMAs are done)
     // and last, with slices, recv[4] (the other slices' sums of an owned piece have landed)
-    static constexpr int NBAR = 2 * STAGES + 5 + (COPIER ? 3 * SF_RING + 1 : 0) + (SLICED ? 4 : 0);
+    static constexpr int NBAR = FULLS + STAGES + 5 + (COPIER ? 3 * SF_RING + 1 : 0) + (SLICED ? 4 : 0);
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;         // tmem base slot, abort flag
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;     // + alignment slack
     static constexpr int SF_SLOT = 4 * SF_WORDS * (1 + HALVES);
-    static constexpr int SF_COL0 = ACC_BUFS * BN;
+    static constexpr int ACC_COLS = ISSUERS * BN;               // of an accumulator buffer
+    static constexpr int SF_COL0 = ACC_BUFS * ACC_COLS;
     static_assert(CG == 1 || CG == 2, "CTA group");
     static_assert(KIND == KIND_F16 || KIND == KIND_MXF8, "operand kind");
     static_assert(!BACK || KIND == KIND_F16, "the backward product has 16-bit operands");
     static_assert(COPIER == SCALED, "block-scaled instances have copier warps");
-    static_assert(ACC_BUFS * BN + SF_RING * SF_GROUP * SF_SLOT <= 512, "TMEM budget");
+    static_assert(SF_COL0 + SF_RING * SF_GROUP * SF_SLOT <= 512, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared-memory budget");
     static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && EPI_BUF % 1024 == 0, "1024-byte regions");
     static_assert(BN <= 256 && SF_WORDS <= 1, "tile columns, one word of scales per stage and row");
@@ -198,7 +210,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
 
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR);
-    uint64_t *empty = full + STAGES;
+    uint64_t *empty = full + Cfg::FULLS;
     uint64_t *tfull = empty + STAGES;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
@@ -223,21 +235,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
         if (p.has_a) prefetch_tensormap(&tmA);
         if (p.has_z) prefetch_tensormap(&tmZ);
-        for (int s = 0; s < STAGES; ++s) {
-            // the producer's arrival and, with packed scales, each copier warp's commit
-            mbar_init(&full[s], 1 + (Cfg::PACKED ? Cfg::COPIERS : 0));
-            mbar_init(&empty[s], 1);
-        }
+        // the producer's arrival and, with packed scales, each copier warp's commit
+        for (int s = 0; s < Cfg::FULLS; ++s) mbar_init(&full[s], 1 + (Cfg::PACKED ? Cfg::COPIERS : 0));
+        for (int s = 0; s < STAGES; ++s) mbar_init(&empty[s], 1);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&tfull[b], 1);
+            mbar_init(&tfull[b], Cfg::ISSUERS);
             mbar_init(&tempty[b], Cfg::EPI_WARPS * CG);
         }
-        mbar_init(drain, 1);
+        mbar_init(drain, Cfg::ISSUERS);
         if constexpr (Cfg::COPIER) {
             for (int i = 0; i < Cfg::SF_RING; ++i) {
                 mbar_init(&sffull[i], 1);
                 mbar_init(&sfready[i], 1);
-                mbar_init(&sfempty[i], 1);
+                mbar_init(&sfempty[i], Cfg::ISSUERS);
             }
             mbar_init(cdrain, Cfg::COPIERS);
         }
@@ -264,7 +274,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
-            int s = 0;
+            int s = 0, fs = 0;
             uint32_t ph = 0, round = 0;
             bool ok = true;
             for (int n = unit0; ok && n < p.units; n += unit_step, ++round) {
@@ -274,7 +284,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     const int kb = kb_at(j, kb0, kb1, round);
                     if (!W.wait(&empty[s], ph ^ 1u)) { ok = false; break; }
                     const bool withhold = p.fault == 1 && round == 0 && j == 0;
-                    const uint32_t fb = smem_addr(&full[s]);
+                    const uint32_t fb = smem_addr(&full[fs]);
                     const uint32_t bar = CG == 1 ? fb : mapa_shared(fb, 0);      // the leader's
                     if constexpr (Cfg::PACKED) {          // the scales first: the copier warps start on them
                         if (rank == 0) mbar_arrive_expect_tx(&sffull[s], w.narrow ? Cfg::NARROW_TX_SF : Cfg::TX_SF);
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                                         checked_y(p.status, ((w.f0 / 64 + i) * p.num_kb + kb) * 4,
                                                   p.tiles_n * CG * p.num_kb * 4));
                     }
-                    if (rank == 0 && !withhold) mbar_arrive_expect_tx(&full[s], w.narrow ? Cfg::NARROW_TX_AB : Cfg::TX_AB);
+                    if (rank == 0 && !withhold) mbar_arrive_expect_tx(&full[fs], w.narrow ? Cfg::NARROW_TX_AB : Cfg::TX_AB);
                     const uint32_t a_dst = smem_addr(smem + Cfg::OFF_A + s * Cfg::A_BYTES);
                     const uint32_t b_dst = smem_addr(smem + Cfg::OFF_B + s * Cfg::B_BYTES);
                     const int kx = checked_x<Cfg::ELEM_BYTES>(p.status, kb * Cfg::BK, p.num_kb * Cfg::BK);
@@ -322,17 +332,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         }
                     }
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
+                    if (++fs == Cfg::FULLS) fs = 0;
                 }
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || (Cfg::ISSUERS == 2 && warp == Cfg::SECOND_ISSUER)) {
         // ----------------------------------------------------------- MMA issue
+        const int me = warp == 1 ? 0 : 1;
         if (rank == 0 && lane == 0) {
             // descriptors as in gemm_tc_kernel: K-major operands step 32 bytes per MMA, an
             // N-contiguous B MMA_K rows of 128 bytes
             constexpr uint32_t B_LBO = Cfg::BACK ? Cfg::ATOM_BYTES : 16;
             constexpr uint32_t B_STEP = Cfg::BACK ? (Cfg::MMA_K * 128) >> 4 : 2;
-            int s = 0, sg = 0;
+            int s = 0, fs = 0, sg = 0;
             uint32_t ph = 0, sgph = 0, acc_it = 0;
             bool ok = true;
             for (int n = unit0; ok && n < p.units; n += unit_step, ++acc_it) {
@@ -342,40 +354,45 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const uint32_t aph = Cfg::ACC_BUFS == 2 ? ((acc_it >> 1) & 1u) : (acc_it & 1u);
                 if (!W.wait<CG == 2>(&tempty[b], aph ^ 1u)) { ok = false; break; }
                 tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + b * BN;
+                const uint32_t d_tmem = tmem_base + b * Cfg::ACC_COLS + me * BN;
+                uint32_t more = 0;                        // the accumulator holds a sum of this tile's
                 for (int j = 0; j < kb1 - kb0; ++j) {
                     [[maybe_unused]] const int kb = kb_at(j, kb0, kb1, acc_it);
                     if constexpr (Cfg::GROUPED) {         // a new group of scales
                         if (j == 0 || group_begins<Cfg>(kb, acc_it))
                             if (!W.wait(&sfready[sg], sgph)) { ok = false; break; }
                     }
-                    if (!W.wait(&full[s], ph)) { ok = false; break; }
-                    tc_fence_after_sync();
-                    const uint64_t ad = smem_desc(smem_addr(smem + Cfg::OFF_A + s * Cfg::A_BYTES), 16, 1024, SWZ_128B);
-                    const uint64_t bd = smem_desc(smem_addr(smem + Cfg::OFF_B + s * Cfg::B_BYTES), B_LBO, 1024, SWZ_128B);
-                    if constexpr (Cfg::SCALED) {
-                        const uint32_t sfa_t = tmem_base + Cfg::SF_COL0 + (Cfg::PACKED ? s : sg * Cfg::SF_GROUP + kb % Cfg::SF_GROUP) * Cfg::SF_SLOT;
-                        const uint32_t sfb_t = sfa_t + 4 * Cfg::SF_WORDS;
+                    if (Cfg::ISSUERS == 1 || fs % Cfg::ISSUERS == me) {
+                        if (!W.wait(&full[fs], ph)) { ok = false; break; }
+                        tc_fence_after_sync();
+                        const uint64_t ad = smem_desc(smem_addr(smem + Cfg::OFF_A + s * Cfg::A_BYTES), 16, 1024, SWZ_128B);
+                        const uint64_t bd = smem_desc(smem_addr(smem + Cfg::OFF_B + s * Cfg::B_BYTES), B_LBO, 1024, SWZ_128B);
+                        if constexpr (Cfg::SCALED) {
+                            const uint32_t sfa_t = tmem_base + Cfg::SF_COL0 + (Cfg::PACKED ? s : sg * Cfg::SF_GROUP + kb % Cfg::SF_GROUP) * Cfg::SF_SLOT;
+                            const uint32_t sfb_t = sfa_t + 4 * Cfg::SF_WORDS;
 #pragma unroll
-                        for (int k = 0; k < Cfg::BK / Cfg::MMA_K; ++k) {
-                            const uint32_t w = (uint32_t)k / 4u, id = (uint32_t)k % 4u;
-                            mma_scaled<Cfg::KIND, CG>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29),
-                                                      sfa_t + 4 * w, sfb_t + 4 * Cfg::HALVES * w, (j != 0) | (k != 0));
+                            for (int k = 0; k < Cfg::BK / Cfg::MMA_K; ++k) {
+                                const uint32_t w = (uint32_t)k / 4u, id = (uint32_t)k % 4u;
+                                mma_scaled<Cfg::KIND, CG>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29),
+                                                          sfa_t + 4 * w, sfb_t + 4 * Cfg::HALVES * w, more | (k != 0));
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < Cfg::BK / Cfg::MMA_K; ++k)
+                                mma_f16<CG>(d_tmem, ad + 2 * k, bd + B_STEP * k, idesc, more | (k != 0));
                         }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < Cfg::BK / Cfg::MMA_K; ++k)
-                            mma_f16<CG>(d_tmem, ad + 2 * k, bd + B_STEP * k, idesc, (j != 0) | (k != 0));
+                        more = 1;
+                        if constexpr (CG == 1) tc_commit<1>(smem_addr(&empty[s]));
+                        else tc_commit_pair(smem_addr(&empty[s]), 0x3);
                     }
-                    if constexpr (CG == 1) tc_commit<1>(smem_addr(&empty[s]));
-                    else tc_commit_pair(smem_addr(&empty[s]), 0x3);
                     if constexpr (Cfg::GROUPED) {
                         if (j == kb1 - kb0 - 1 || group_begins<Cfg>(kb_at(j + 1, kb0, kb1, acc_it), acc_it)) {
                             tc_commit<1>(smem_addr(&sfempty[sg]));
                             if (++sg == Cfg::SF_RING) { sg = 0; sgph ^= 1u; }
                         }
                     }
-                    if (++s == STAGES) { s = 0; ph ^= 1u; }
+                    if (++s == STAGES) s = 0;
+                    if (++fs == Cfg::FULLS) { fs = 0; ph ^= 1u; }
                 }
                 if (!ok) break;
                 if constexpr (CG == 1) tc_commit<1>(smem_addr(&tfull[b]));
@@ -390,7 +407,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if constexpr (Cfg::PACKED) {
             if (rank == 0 && lane == 0) {
                 // (a narrow tile copies what a whole one's second block left in the stage, which no MMA reads)
-                int s = 0;
+                int s = 0, fs = 0;
                 uint32_t ph = 0;
                 bool ok = true;
                 for (int n = unit0; ok && n < p.units; n += unit_step) {
@@ -399,9 +416,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         tc_fence_after_sync();
                         const uint32_t sfa_t = tmem_base + Cfg::SF_COL0 + s * Cfg::SF_SLOT;
                         copy_scales<Cfg, Cfg::COPIERS>(smem, s, sfa_t, sfa_t + 4 * Cfg::SF_WORDS, warp - Cfg::COPY_WARP);
-                        if constexpr (CG == 1) tc_commit<1>(smem_addr(&full[s]));
-                        else tc_commit_pair(smem_addr(&full[s]), 0x1);
+                        if constexpr (CG == 1) tc_commit<1>(smem_addr(&full[fs]));
+                        else tc_commit_pair(smem_addr(&full[fs]), 0x1);
                         if (++s == STAGES) { s = 0; ph ^= 1u; }
+                        if (++fs == Cfg::FULLS) fs = 0;
                     }
                 }
                 // every copy this thread issued has finished before teardown
@@ -513,7 +531,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int row = m_warp + lane;
             // forward: g's columns of the warp's slice, u's are 64 further on; backward: da's
             const int col = Cfg::BACK ? h * wchunks * EPI_COLS : (w.narrow ? 32 * h : 128 * h);
-            const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + b * BN + col;
+            const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + b * Cfg::ACC_COLS + col;
+            // 32 columns' sums, the issuers' added up (of a tile of one k-block only the one whose turn it was has some)
+            auto load_sums = [&](uint32_t from, uint32_t (&v)[32]) {
+                tmem_ld_32x32b_x32(Cfg::ISSUERS == 2 && kb1 - kb0 == 1 && (acc_it & 1u) ? from + BN : from, v);
+                if constexpr (Cfg::ISSUERS == 2) {
+                    if (kb1 - kb0 > 1) {
+                        uint32_t other[32];
+                        tmem_ld_32x32b_x32(from + BN, other);
+                        tmem_ld_wait(v);
+                        tie_registers(other);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(other[i]));
+                    }
+                }
+            };
             // chunks with a column of the matrix; none where the warp's rows are all past M
             const int chunks = m_warp < p.M ? max(0, min(wchunks, (p.F - f_warp + EPI_COLS - 1) / EPI_COLS)) : 0;
 
@@ -622,7 +654,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 };
                 if (!__all_sync(0xffffffffu, W.wait(&tfull[b], aph))) break;
                 tc_fence_after_sync();
-                if constexpr (Cfg::ACC_BUFS == 1) {
+                if constexpr (Cfg::ACC_BUFS == 1 && Cfg::WCHUNKS > 1) {
                     // the whole slice to registers first, so that the MMA can start the next tile
                     uint32_t g[Cfg::WCHUNKS][32], u[Cfg::WCHUNKS][32];
 #pragma unroll
@@ -644,8 +676,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll 1
                     for (int c = 0; c < wchunks; ++c) {
                         uint32_t v[2][32];
-                        tmem_ld_32x32b_x32(taddr + EPI_COLS * c, v[0]);
-                        tmem_ld_32x32b_x32(taddr + 64 + EPI_COLS * c, v[1]);
+                        load_sums(taddr + EPI_COLS * c, v[0]);
+                        load_sums(taddr + 64 + EPI_COLS * c, v[1]);
                         tmem_ld_wait(v[0]);
                         tie_registers(v[1]);
                         if (c == wchunks - 1) release(b);
@@ -683,7 +715,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     const Kept k = next;
                     if (c + 1 < wchunks) next = fetch(c + 1);
                     uint32_t v[1][32];
-                    tmem_ld_32x32b_x32(taddr + EPI_COLS * c, v[0]);
+                    load_sums(taddr + EPI_COLS * c, v[0]);
                     tmem_ld_wait(v[0]);
                     if (c == wchunks - 1) release(b);
                     if (c >= chunks || !exchange(c, v)) continue;

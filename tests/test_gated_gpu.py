@@ -345,7 +345,7 @@ def test_sliced_tiles(M, F, K, kind, slices):
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("M,F,N,slices", [(40, 80, 8200, 8), (300, 272, 4104, 8), (300, 1040, 4104, 4),
-                                              (129, 2064, 8232, 4), (520, 1552, 4176, 2)])
+                                              (129, 2064, 8232, 4), (520, 1552, 4176, 2), (520, 1552, 4160, 1)])
 def test_sliced_backward(M, F, N, kind, slices):
     DY, W2, (CK, SF, g, u) = backward_case(M, F, N, kind)
     with gemm.GatedBackPlan(M, F, N, kind) as plan:
@@ -424,3 +424,21 @@ def test_backward_widths_of_single_tiles(M, F, N, kind, tile):
         assert (plan.info["tile_n"], plan.info["splits"], plan.info["cta_group"]) == (tile, 1, 1)
         DZ, A = backward(plan, dev(DY), dev(W2), dev(CK), dev(SF), M, F, kind, True)
         check_backward(DZ, A, DY, W2, g, u, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("K", [48, 64, 80, 128, 144, 192, 208, 400])
+def test_few_k_blocks_and_many_tiles_of_single_ctas(K, kind):
+    """One k-block to several, an odd and an even number, over several tiles of each CTA."""
+    M, F = 1100, 2080
+    (X, SX, x), (W, SW, w) = operands(M, F, K, kind)
+    out = Out(M, F, "bf16", False)
+    with gemm.GatedPlan(M, F, K, kind, "bf16", scaled(kind), ONE) as plan:
+        assert plan.info["tiles"] > 152
+        forward(plan, (dev(X), dev(SX)), (dev(W), dev(SW)), out)
+    check(out, x, w, "bf16", False)
+    if kind == "bf16":
+        DY, W2, (CK, SF, g, u) = backward_case(M, F, K, kind)
+        with gemm.GatedBackPlan(M, F, K, kind, ONE) as plan:
+            DZ, A = backward(plan, dev(DY), dev(W2), dev(CK), dev(SF), M, F, kind, True)
+            check_backward(DZ, A, DY, W2, g, u, kind)
