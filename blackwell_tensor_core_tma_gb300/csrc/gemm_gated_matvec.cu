@@ -15,6 +15,7 @@
 // activations' and the scales; it runs on from one tile of columns to the next, so that memory does not wait for the sums.
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "gemm_rows.cuh"
@@ -366,7 +367,7 @@ constexpr int STAGE = 16 * 128 + 16 * 4;                   // 8 rows of g, 8 of 
 constexpr int WIDE_WARPS = 16;
 template <int NG>
 struct Wide {
-    static constexpr int DEPTH = NG == 1 ? 4 : 3;                                   // stages of a warp's ring
+    static constexpr int DEPTH = NG == 1 ? 4 : 3;// stages of a warp's ring
     static constexpr int RINGS = WIDE_WARPS * DEPTH * STAGE;
     // activations held at once, twice: (chunk, token)s of 128 k, and their powers of two
     static constexpr int PIECES = 4;                                                // of sixteen lanes
@@ -384,7 +385,8 @@ struct WideParams {
     int M, F, K;
     int chunks;              // of K
     int tiles;               // of 8 * groups columns
-    int groups;              // of 8 columns side by side in a CTA; WIDE_WARPS / groups warps share a group's K
+    int groups;              // of 8 columns side by side in a CTA
+    int shares;              // warps that share a group's K; those behind the last group's have none
 };
 
 template <typename XT, int NG>
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) few_scaled_kernel(const __gri
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(shared), ring = base + at.warp * DEPTH * STAGE;
     const int blocks = (p.K + BLOCK - 1) / BLOCK;
     const bool whole_scales = blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(p.sfw) & 3) == 0;
-    const int group = at.warp % p.groups, share = at.warp / p.groups, shares = WIDE_WARPS / p.groups;
+    const int shares = p.shares, group = at.warp % p.groups, share = at.warp / p.groups < shares ? at.warp / p.groups : p.chunks;
     // the CTA's slice: chunks [c0, c1), every shares-th of them this warp's
     const int c0 = (int)((int64_t)p.chunks * at.rank / at.ranks), c1 = (int)((int64_t)p.chunks * (at.rank + 1) / at.ranks);
     const int rows = min(p.M, 8 * NG), phase_chunks = W::HELD / rows, phases = (c1 - c0 + phase_chunks - 1) / phase_chunks;
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) few_scaled_kernel(const __gri
             sums[n][0] = sums[n][1] = 0.f;
             if (o >= outputs) break;
             const int w = o / (64 * NG), j = o / 64 % NG, e = o / 32 % 2, l = o % 32;
-            for (int k = w; k < WIDE_WARPS; k += p.groups) {
+            for (int k = w; k < p.groups * shares; k += p.groups) {
                 sums[n][0] += part[k][j][e][l];
                 sums[n][1] += part[k][j][e + 2][l];
             }
@@ -619,21 +621,72 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) few_scaled_kernel(const __gri
     wait_copies<0>();
 }
 
+// How columns and K are shared out: `groups` column groups per CTA, the warps that are left and the CTAs of a cluster sharing K.
+// The estimate in microseconds, but for what every shape costs, is fitted to 2900 times of 85 sizes (M 1 to 16, F 333 to 65 536, K
+// 512 to 32 768) in every shape; the shape that it takes is 1.1 % slower than the fastest on average, 21 % at most.  For
+// example 16 x 8192 x 8192: 14 groups and clusters of two 35.3 us, 16 and two 36.9, 7 and one 37.1, 16 and four 46; 1 x 14336 x
+// 4096: 12 or 6 groups 22.4, 13 25.3, 16 31.
+struct WideShape {
+    int groups, cluster, slots;                            // slots: clusters that run at once
+};
+constexpr int CLUSTERS = 4;                                // of 1, 2, 4 and 8 CTAs
+WideShape wide_shape(int M, int F, int K, const int (&slots)[CLUSTERS]) {
+    const bool few = M <= 8;
+    const float cluster_us = few ? 0.16f : 0.74f, round_us = few ? 0.38f : 0.54f, cluster_round_us = few ? 1.19f : 1.49f;
+    const float step_us = few ? 0.111f : 0.365f, warp_us = few ? 0.036f : 0.0437f, x_us = few ? 0.0038f : 0.0073f;
+    const uint32_t columns = (uint32_t)(F + 7) / 8, chunks = (uint32_t)(K + CHUNK - 1) / CHUNK;
+    WideShape best{};
+    float least = 0.f;
+    for (int i = 0; i < CLUSTERS && (1u << i) <= chunks; ++i) {
+        const uint32_t slice = (chunks + (1u << i) - 1) >> i;
+        if (slots[i] < 1) continue;
+        for (uint32_t groups = 2; groups <= WIDE_WARPS; ++groups) {
+            const uint32_t tiles = (columns + groups - 1) / groups, rounds = (tiles + slots[i] - 1) / slots[i];
+            const uint32_t shares = WIDE_WARPS / groups, steps = (slice + shares - 1) / shares;
+            const uint32_t warps = groups * std::min(shares, slice);
+            const float us = (i > 0 ? cluster_us : 0.f) +
+                             (float)rounds * (round_us + (i > 0 ? cluster_round_us : 0.f) + (float)steps * (step_us + warp_us * (float)warps) +
+                                              x_us * (float)(slice * (uint32_t)M));
+            if (best.groups == 0 || us < least) {
+                least = us;
+                best = WideShape{(int)groups, 1 << i, slots[i]};
+            }
+        }
+    }
+    return best;
+}
+
 template <typename XT, int NG>
 cudaError_t few_scaled_launch(const FewParams &q, int sms, cudaStream_t stream) {
     const auto kernel = few_scaled_kernel<XT, NG>;
-    static std::atomic<bool> ready[MAX_DEVICES];
-    const cudaError_t e = allow_shared(kernel, ready, Wide<NG>::BYTES);
+    static std::mutex mu;
+    static int known[MAX_DEVICES][CLUSTERS];               // clusters that run at once; they are asked for once
+    static thread_local struct {
+        int dev, M, F, K;
+        WideShape shape;
+    } last{-1, 0, 0, 0, {}};                               // the shape is a microsecond's work
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    WideParams p{q.x, q.w, q.sfw, q.a, q.M, q.F, q.K, (q.K + CHUNK - 1) / CHUNK, 0, WIDE_WARPS};
-    // where warps are left K is shared out, first among a CTA's, then over the CTAs of a cluster
-    const int columns = (p.F + 7) / 8;
-    while (p.groups > 2 && (columns + p.groups - 1) / p.groups * 2 <= sms && p.chunks >= 2 * (WIDE_WARPS / p.groups)) p.groups /= 2;
-    p.tiles = (columns + p.groups - 1) / p.groups;
-    int cluster = 1;
-    while (cluster < MAX_CLUSTER && p.tiles * cluster * 2 <= sms && p.chunks >= 2 * cluster * (WIDE_WARPS / p.groups)) cluster *= 2;
-    const int slots = std::max(1, sms / cluster), rounds = (p.tiles + slots - 1) / slots, ctas = (p.tiles + rounds - 1) / rounds;
-    const Launch l(ctas * cluster, WIDE_WARPS * 32, Wide<NG>::BYTES, cluster, stream);
+    if (last.dev != dev || last.M != q.M || last.F != q.F || last.K != q.K) {
+        std::lock_guard<std::mutex> lock(mu);
+        int(&slots)[CLUSTERS] = known[dev];
+        if (slots[0] == 0) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<NG>::BYTES);
+            for (int i = CLUSTERS - 1; i > 0 && e == cudaSuccess; --i) {
+                const Launch l(1 << i, WIDE_WARPS * 32, Wide<NG>::BYTES, 1 << i, nullptr, false);
+                e = cudaOccupancyMaxActiveClusters(&slots[i], kernel, &l.config);
+            }
+            if (e != cudaSuccess) return e;
+            slots[0] = sms;
+        }
+        last = {dev, q.M, q.F, q.K, wide_shape(q.M, q.F, q.K, slots)};
+    }
+    const WideShape &s = last.shape;
+    const int columns = (q.F + 7) / 8, tiles = (columns + s.groups - 1) / s.groups;
+    const WideParams p{q.x, q.w, q.sfw, q.a, q.M, q.F, q.K, (q.K + CHUNK - 1) / CHUNK, tiles, s.groups, WIDE_WARPS / s.groups};
+    const int rounds = (tiles + s.slots - 1) / s.slots, ctas = (tiles + rounds - 1) / rounds;
+    const Launch l(ctas * s.cluster, WIDE_WARPS * 32, Wide<NG>::BYTES, s.cluster, stream);
     return cudaLaunchKernelEx(&l.config, kernel, p);
 }
 
