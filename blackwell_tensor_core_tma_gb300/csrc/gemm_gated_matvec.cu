@@ -357,17 +357,18 @@ __device__ __forceinline__ uint32_t largest2(uint32_t a, uint32_t b) {          
 // codes, the four lanes of a row have one scale's block side by side, so that two MMAs sum a block, whose sum takes the scale.
 // fp16 activations meet the codes as they are.  bf16 ones are brought to fp16 by a power of two for each token's 128 of k,
 // which puts the largest of them at 2^14 to 2^15: those down to 2^-31 of it are exact, smaller ones off by 2^-39 of it at
-// most.  That is done once for all columns of a CTA: its sixteen warps have 8 columns each of up to 128, and share K between
-// them only where columns are few; the activations lie in shared memory, a phase of K's chunks ahead.  1 x 8192 x 8192 25.3 us
-// (5480 GB/s), 8 rows 29.4, 16 rows 39: instructions, half of them conversions and their products with scales, and their
-// latencies, which 16 warps do not cover.  (Each warp a part of K, its activations converted by itself: 28.4, 29.1 and 46;
-// weights made bf16 by their bits and a product, from registers: 35, 36 and 43.)
+// most.  That is done once for all columns of a CTA: its sixteen warps have 8 columns each of up to 128, or share
+// K between them; the activations lie in shared memory, a phase of K's chunks ahead.  1 x 8192 x 8192 24.8 us
+// (5580 GB/s), 8 rows 28, 16 rows 35.3: shared memory (64 % of its rate; half of what a warp reads are activations) and
+// instructions (half of a scheduler's slots, half of them conversions and products with scales), in turn.  (Each warp a part of
+// K, its activations converted by itself: 28.4, 29.1 and 46; weights made bf16 by their bits and a product, from registers: 35,
+// 36 and 43; 24 warps with 80 registers: 25.8, 30.2 and 41.8; addresses that run on instead of being computed: 36 for 16 rows.)
 constexpr int CHUNK = 128;                                 // of k: a line of a weight row
 constexpr int STAGE = 16 * 128 + 16 * 4;                   // 8 rows of g, 8 of u, and their scales
 constexpr int WIDE_WARPS = 16;
 template <int NG>
 struct Wide {
-    static constexpr int DEPTH = NG == 1 ? 4 : 3;// stages of a warp's ring
+    static constexpr int DEPTH = NG == 1 ? 4 : 3;                                   // stages of a warp's ring
     static constexpr int RINGS = WIDE_WARPS * DEPTH * STAGE;
     // activations held at once, twice: (chunk, token)s of 128 k, and their powers of two
     static constexpr int PIECES = 4;                                                // of sixteen lanes
