@@ -353,16 +353,17 @@ __device__ __forceinline__ uint32_t largest2(uint32_t a, uint32_t b) {          
 }
 
 // The weights are a power of two per 32 of k times codes, which become fp16, which holds them all, by one conversion for two:
-// what bounds this kernel next to memory is instructions, and what they are spent on is chosen for that.  A lane's 8 bytes are 8
+// A lane's 8 bytes are 8
 // codes, the four lanes of a row have one scale's block side by side, so that two MMAs sum a block, whose sum takes the scale.
 // fp16 activations meet the codes as they are.  bf16 ones are brought to fp16 by a power of two for each token's 128 of k,
 // which puts the largest of them at 2^14 to 2^15: those down to 2^-31 of it are exact, smaller ones off by 2^-39 of it at
 // most.  That is done once for all columns of a CTA: its sixteen warps have 8 columns each of up to 128, or share
-// K between them; the activations lie in shared memory, a phase of K's chunks ahead.  1 x 8192 x 8192 24.8 us
-// (5580 GB/s), 8 rows 28, 16 rows 35.3: shared memory (64 % of its rate; half of what a warp reads are activations) and
-// instructions (half of a scheduler's slots, half of them conversions and products with scales), in turn.  (Each warp a part of
-// K, its activations converted by itself: 28.4, 29.1 and 46; weights made bf16 by their bits and a product, from registers: 35,
-// 36 and 43; 24 warps with 80 registers: 25.8, 30.2 and 41.8; addresses that run on instead of being computed: 36 for 16 rows.)
+// K between them; the activations lie in shared memory, a phase of K's chunks ahead.  1 x 8192 x 8192 25.1 us (5500 GB/s), 8 rows
+// 28, 16 rows 35.3: the weights' way through shared memory and the chains of MMAs behind it (16 rows with no weights loaded take
+// 27, without the products with scales 32.6, without conversions or reads of activations no less).  Tried, for 1, 8 and 16 rows:
+// each warp a part of K, its activations converted by itself 28.4, 29.1 and 46; weights made bf16 by their bits and a product, from
+// registers 35, 36 and 43; 24 warps with 80 registers 25.8, 30.2 and 41.8; weights by tensor boxes, one per chunk 25.9, 29 and
+// 37.9; for 16 rows a stage more 38, a stage less 37.7.
 constexpr int CHUNK = 128;                                 // of k: a line of a weight row
 constexpr int STAGE = 16 * 128 + 16 * 4;                   // 8 rows of g, 8 of u, and their scales
 constexpr int WIDE_WARPS = 16;
@@ -371,7 +372,8 @@ struct Wide {
     static constexpr int DEPTH = NG == 1 ? 4 : 3;                                   // stages of a warp's ring
     static constexpr int RINGS = WIDE_WARPS * DEPTH * STAGE;
     // activations held at once, twice: (chunk, token)s of 128 k, and their powers of two
-    static constexpr int PIECES = 4;                                                // of sixteen lanes
+    // (what the first sums wait for: 4 x 2048 x 2048 3.8 us with two pieces, 4.2 with four; 16 x 8192 x 8192 36.9 and 35.3)
+    static constexpr int PIECES = NG == 1 ? 2 : 4;                                  // of sixteen lanes
     static constexpr int HELD = PIECES * WIDE_WARPS * 2;
     static constexpr int OFF_FX = HELD * 256;
     static constexpr int X_BYTES = OFF_FX + (HELD + 16) * 4;
