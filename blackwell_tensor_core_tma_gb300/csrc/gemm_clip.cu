@@ -86,12 +86,42 @@ struct Span {
     }
 };
 
+// What L2 does with lines that a kernel is through with: leave in their turn, or first
+__device__ __forceinline__ uint64_t in_turn() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t first_out() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
 // The pieces of a step: a thread's are thread, thread + THREADS, ..., zeros past the step's own.  While a step's are worked
-// on, those of the next one are on their way into the same registers.
+// on, those of the next one are on their way into the same registers.  HINTS: with `policy` for L2.
+template <bool HINTS>
 struct Pieces {
     uint4 q[STEP];
+    uint64_t policy;
     __device__ __forceinline__ void load(int i, const uint4 *g, int left, int thread) {
-        q[i] = i * THREADS + thread < left ? g[i * THREADS + thread] : make_uint4(0, 0, 0, 0);
+        const uint4 *from = g + (i * THREADS + thread);
+        q[i] = make_uint4(0, 0, 0, 0);
+        if (i * THREADS + thread >= left) return;
+        if constexpr (HINTS)
+            asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                         : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
+                         : "l"(from), "l"(policy)
+                         : "memory");
+        else
+            q[i] = *from;
+    }
+    __device__ __forceinline__ void store(uint4 *to, const uint4 &v) const {
+        if constexpr (HINTS)
+            asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w),
+                         "l"(policy)
+                         : "memory");
+        else
+            *to = v;
     }
 };
 
@@ -194,8 +224,8 @@ __device__ __forceinline__ void pairs(const uint4 &q, F f) {
     }
 }
 // The largest magnitude of a thread's values, NaN left out
-template <int TYPE>
-__device__ __forceinline__ float largest(const Pieces &p) {
+template <int TYPE, bool HINTS>
+__device__ __forceinline__ float largest(const Pieces<HINTS> &p) {
     if constexpr (TYPE == GEMM_F32) {
         float m = 0.f;
 #pragma unroll
@@ -217,8 +247,8 @@ __device__ __forceinline__ float largest(const Pieces &p) {
 
 // A step's squares.  With every magnitude at most 2^40, and the largest at least 2^-56, neither squares nor the sums of 2^43
 // of them leave fp32's range, and what squares below its normal numbers lose does not count beside the largest.
-template <int TYPE, typename W>
-__device__ __forceinline__ void add_squares(Pieces &p, const W &next, int thread, Sum &sum) {
+template <int TYPE, bool HINTS, typename W>
+__device__ __forceinline__ void add_squares(Pieces<HINTS> &p, const W &next, int thread, Sum &sum) {
     float2 s[2] = {};
 #pragma unroll
     for (int i = 0; i < STEP; ++i) {
@@ -251,12 +281,14 @@ __device__ __forceinline__ void add_square(float v, Sum &sum) {
     else if (v != 0.f) sum.rest += (double)v * (double)v;
 }
 
-// The squares of a range
-template <int N>
-__device__ __forceinline__ void norm_rows(const Table<N> &t, const Range &r, int start, int thread, Sum &sum) {
+// The squares of a range, of which the last `keep` rows are to stay in L2
+template <bool HINTS, int N>
+__device__ __forceinline__ void norm_rows(const Table<N> &t, const Range &r, int start, int thread, uint32_t keep, Sum &sum) {
     if (r.begin >= r.end) return;
+    const uint64_t stay = HINTS ? in_turn() : 0, leave = HINTS ? first_out() : 0;
     Walk<N> next(t, start);
-    Pieces p;
+    Pieces<HINTS> p;
+    p.policy = r.end - r.begin > keep ? leave : stay;
     next.up(r.begin, r);
 #pragma unroll
     for (int i = 0; i < STEP; ++i) p.load(i, next.g, next.left, thread);
@@ -265,6 +297,7 @@ __device__ __forceinline__ void norm_rows(const Table<N> &t, const Range &r, int
         const bool first = row == e.first;
         row += next.rows;
         if (row < r.end) next.up(row, r); else next.none();
+        if constexpr (HINTS) p.policy = r.end - row > keep ? leave : stay;
         if (e.type == GEMM_F32) add_squares<GEMM_F32>(p, next, thread, sum);
         else if (e.type == GEMM_BF16) add_squares<GEMM_BF16>(p, next, thread, sum);
         else add_squares<GEMM_F16>(p, next, thread, sum);
@@ -299,8 +332,8 @@ __device__ __forceinline__ Factor factor_of(const Sum &s, float limit, float &no
 
 // ------------------------------------------------------------------------------------------- results
 
-template <int TYPE, typename W>
-__device__ __forceinline__ void scale_pieces(Pieces &p, uint4 *to, int left, const W &next, int thread, const Factor &factor) {
+template <int TYPE, bool HINTS, typename W>
+__device__ __forceinline__ void scale_pieces(Pieces<HINTS> &p, uint4 *to, int left, const W &next, int thread, const Factor &factor) {
     const float2 rest = make_float2(factor.rest, factor.rest), none = make_float2(-0.f, -0.f);      // x * rest + -0 is x * rest
 #pragma unroll
     for (int i = 0; i < STEP; ++i) {
@@ -320,7 +353,7 @@ __device__ __forceinline__ void scale_pieces(Pieces &p, uint4 *to, int left, con
             q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
         else if constexpr (TYPE == GEMM_BF16) q = pack8(static_cast<const __nv_bfloat16 *>(nullptr), v);
         else q = pack8(static_cast<const __half *>(nullptr), v);
-        if (i * THREADS + thread < left) to[i * THREADS + thread] = q;
+        if (i * THREADS + thread < left) p.store(to + (i * THREADS + thread), q);
         p.load(i, next.g, next.left, thread);
     }
 }
@@ -335,12 +368,13 @@ __device__ __forceinline__ void scale_apart(const Entry &e, uint32_t row, uint32
         store_one(e.c, e.type, begin + k, factor(load_one(e.g, e.type, begin + k)));
 }
 
-// A range scaled, its last rows first
-template <int N>
-__device__ __forceinline__ void scale_rows(const Table<N> &t, const Range &r, int start, int thread, const Factor &factor) {
+// A range scaled, its last rows first; `leave`: what it reads and writes leaves L2 first
+template <bool HINTS, int N>
+__device__ __forceinline__ void scale_rows(const Table<N> &t, const Range &r, int start, int thread, bool leave, const Factor &factor) {
     if (r.begin >= r.end || (factor.one && !t.copies)) return;
     Walk<N> next(t, start);
-    Pieces p;
+    Pieces<HINTS> p;
+    p.policy = !HINTS ? 0 : leave ? first_out() : in_turn();
     auto down = [&](uint32_t to) {                         // nothing to load where nothing is written, or apart
         next.down(to, r);
         const Entry &e = t.e[next.i];
@@ -375,18 +409,18 @@ __device__ __forceinline__ void scale_rows(const Table<N> &t, const Range &r, in
 // ------------------------------------------------------------------------------------------- kernels
 
 // Bound by memory, which the tensors pass three times.  CTAS_PER_SM of them run at once on an SM, and the grid is at most that
-// many: no second wave.  1 billion fp32 values: 1.77 ms, 6750 GB/s over the three passes (a copy's rate); 100.7 million 195 us,
-// 6190 GB/s; 40 million in 291 tensors of both types, copied, 66 us.  Steps of eight rows, four or six CTAs: within 3 %;
-// stores that leave L2 first, loads past L1: the same or slower.
+// many: no second wave.  1 billion fp32 values: 1.77 ms, 6750 GB/s over the three passes (a copy's rate); 100.7 million 190 us,
+// 6370 GB/s; 40 million in 291 tensors of both types, copied, 62 us.  Steps of eight rows, four or six CTAs: within 3 %; loads
+// past L1: the same.
 constexpr int CTAS_PER_SM = 5;
 template <int N>
-__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) clip_norm_kernel(const __grid_constant__ Table<N> t, Part *parts, int before) {
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) clip_norm_kernel(const __grid_constant__ Table<N> t, Part *parts, int before, uint32_t keep) {
     const Range r = range_of(t.rows, blockIdx.x, gridDim.x);
     const int start = t.start[blockIdx.x];
     Sum sum;
     wait_for_previous();
     let_next_launch();
-    norm_rows(t, r, start, threadIdx.x, sum);
+    norm_rows<true>(t, r, start, threadIdx.x, keep, sum);
     sum = block_sum(sum);
     if (threadIdx.x == 0) {
         if ((int)blockIdx.x < before) sum.add(parts[blockIdx.x]);          // of the launches before this one
@@ -396,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) clip_norm_kernel(const _
 
 template <int N>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
-    clip_scale_kernel(const __grid_constant__ Table<N> t, const Part *parts, int n, float limit, float *norm_out) {
+    clip_scale_kernel(const __grid_constant__ Table<N> t, const Part *parts, int n, float limit, float *norm_out, bool leave) {
     const Range r = range_of(t.rows, blockIdx.x, gridDim.x);
     const int start = t.start[blockIdx.x];
     wait_for_previous();
@@ -406,7 +440,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     float norm;
     const Factor factor = factor_of(block_sum(sum), limit, norm);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-    scale_rows(t, r, start, threadIdx.x, factor);
+    scale_rows<true>(t, r, start, threadIdx.x, leave, factor);
 }
 
 // Few rows: one cluster does both, its CTAs' sums exchanged through shared memory.
@@ -420,7 +454,7 @@ __global__ void __launch_bounds__(THREADS)
     Sum sum;
     wait_for_previous();
     let_next_launch();
-    norm_rows(t, r, start, threadIdx.x, sum);
+    norm_rows<false>(t, r, start, threadIdx.x, 0, sum);
     sum = block_sum(sum);
     if (threadIdx.x < FEW_CTAS) {
         uint32_t to;
@@ -438,7 +472,7 @@ __global__ void __launch_bounds__(THREADS)
     float norm;
     const Factor factor = factor_of(all, limit, norm);
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-    scale_rows(t, r, start, threadIdx.x, factor);
+    scale_rows<false>(t, r, start, threadIdx.x, false, factor);
 }
 
 // ------------------------------------------------------------------------------------------- launches
@@ -465,6 +499,11 @@ struct Call {
 // values together 7.6 us in a queue of calls, two kernels 10.2; captured, 7.2 and 5.5)
 constexpr uint32_t FEW_ROWS = 64;
 
+// A list too large for L2: of what the first kernel reads the last KEEP_BYTES stay there, and what the second one is through
+// with leaves first.  100.7 million fp32 values 190 us, 195 without (48 million bytes 192); 291 tensors 62 and 66.
+// The stores' part of it alone costs 1 %.
+constexpr int64_t L2_BYTES = 60000000, KEEP_BYTES = 96000000;
+
 // The tensors in launches of up to N: all norms' kernels, then all scalings'
 template <int N>
 cudaError_t clip(const Call &k) {
@@ -472,7 +511,7 @@ cudaError_t clip(const Call &k) {
     const int most = std::min(CTAS_PER_SM * k.sms, MAX_PARTS);
     Table<N> t;
     int parts = 0, grid = 0;
-    bool any = false, few = false;
+    bool any = false, few = false, large = false;
     auto table = [&](int64_t l) {
         t.count = 0;
         t.rows = 0;
@@ -489,6 +528,7 @@ cudaError_t clip(const Call &k) {
             any = any || from.c;
         }
         few = launches == 1 && t.rows <= FEW_ROWS;
+        large = launches == 1 && (int64_t)t.rows * ROW > L2_BYTES;
         grid = few ? FEW_CTAS : (int)std::min<uint32_t>(std::max(1u, t.rows), (uint32_t)most);
         for (int b = 0, i = 0; b < grid; ++b) {
             const uint32_t begin = range_of(t.rows, (uint32_t)b, (uint32_t)grid).begin;
@@ -502,7 +542,8 @@ cudaError_t clip(const Call &k) {
             const Launch c(FEW_CTAS, THREADS, 0, FEW_CTAS, k.stream);
             return cudaLaunchKernelEx(&c.config, clip_few_kernel<N>, t, k.limit, k.norm);
         }
-        const cudaError_t e = launch(clip_norm_kernel<N>, grid, THREADS, 0, k.stream, t, k.parts, parts);
+        const cudaError_t e = launch(clip_norm_kernel<N>, grid, THREADS, 0, k.stream, t, k.parts, parts,
+                                     large ? (uint32_t)(KEEP_BYTES / ROW / grid) : ~0u);
         if (e != cudaSuccess) return e;
         parts = std::max(parts, grid);
     }
@@ -514,7 +555,7 @@ cudaError_t clip(const Call &k) {
             grid = 1;
         }
         const cudaError_t e = launch(clip_scale_kernel<N>, grid, THREADS, 0, k.stream, t, (const Part *)k.parts, parts, k.limit,
-                                     l == 0 ? k.norm : (float *)nullptr);
+                                     l == 0 ? k.norm : (float *)nullptr, large);
         if (e != cudaSuccess || !any) return e;
     }
     return cudaSuccess;

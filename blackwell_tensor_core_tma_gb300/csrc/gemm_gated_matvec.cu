@@ -352,9 +352,9 @@ __device__ __forceinline__ uint32_t largest2(uint32_t a, uint32_t b) {          
     return *reinterpret_cast<const uint32_t *>(&m);
 }
 
-// The weights are a power of two per 32 of k times codes, which become fp16, which holds them all, by one conversion for two:
-// A lane's 8 bytes are 8
-// codes, the four lanes of a row have one scale's block side by side, so that two MMAs sum a block, whose sum takes the scale.
+// The weights are a power of two per 32 of k times codes, which become fp16, which holds them all, by one conversion for two.
+// A lane's 8 bytes are 8 codes, the four lanes of a row have one scale's block side by side, so that two MMAs sum a block, whose
+// sum takes the scale.
 // fp16 activations meet the codes as they are.  bf16 ones are brought to fp16 by a power of two for each token's 128 of k,
 // which puts the largest of them at 2^14 to 2^15: those down to 2^-31 of it are exact, smaller ones off by 2^-39 of it at
 // most.  That is done once for all columns of a CTA: its sixteen warps have 8 columns each of up to 128, or share
