@@ -45,12 +45,12 @@ struct Part {
 constexpr int MAX_PARTS = GEMM_CLIP_WORKSPACE / (int)sizeof(Part);
 // The tensors of one launch, by value: a captured graph keeps them.  start[b]: the tensor of CTA b's first row.  (Looked up
 // by halving in the launch's parameters, it costs a cache miss per step: 500 tensors of 1000 elements took 20 us, not 12.)
-template <int N>
+template <int N, int CTAS = MAX_PARTS>
 struct Table {
     int count;
     uint32_t rows;
     bool copies;             // some c is not its g
-    uint16_t start[MAX_PARTS];
+    uint16_t start[CTAS];
     Entry e[N];
 };
 
@@ -98,42 +98,35 @@ __device__ __forceinline__ uint64_t first_out() {
     return p;
 }
 // The pieces of a step: a thread's are thread, thread + THREADS, ..., zeros past the step's own.  While a step's are worked
-// on, those of the next one are on their way into the same registers.  HINTS: with `policy` for L2.
-template <bool HINTS>
+// on, those of the next one are on their way into the same registers.
 struct Pieces {
     uint4 q[STEP];
     uint64_t policy;
     __device__ __forceinline__ void load(int i, const uint4 *g, int left, int thread) {
         const uint4 *from = g + (i * THREADS + thread);
         q[i] = make_uint4(0, 0, 0, 0);
-        if (i * THREADS + thread >= left) return;
-        if constexpr (HINTS)
+        if (i * THREADS + thread < left)
             asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
                          : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
                          : "l"(from), "l"(policy)
                          : "memory");
-        else
-            q[i] = *from;
     }
     __device__ __forceinline__ void store(uint4 *to, const uint4 &v) const {
-        if constexpr (HINTS)
-            asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w),
-                         "l"(policy)
-                         : "memory");
-        else
-            *to = v;
+        asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w),
+                     "l"(policy)
+                     : "memory");
     }
 };
 
 // A walk over a range's rows, up to STEP of one tensor at a time
-template <int N>
+template <typename T>
 struct Walk {
-    const Table<N> &t;
+    const T &t;
     int i;                   // the step's tensor
     uint32_t row, rows;      // the step: rows of the list [row, row + rows)
     const uint4 *g;          // its pieces
     int left;                // how many
-    __device__ __forceinline__ Walk(const Table<N> &table, int start) : t(table), i(start), row(0), rows(0), g(nullptr), left(0) {}
+    __device__ __forceinline__ Walk(const T &table, int start) : t(table), i(start), row(0), rows(0), g(nullptr), left(0) {}
     __device__ __forceinline__ void up(uint32_t from, const Range &r) {            // the step that begins at `from`
         while (i + 1 < t.count && t.e[i + 1].first <= from) ++i;
         row = from;
@@ -224,8 +217,8 @@ __device__ __forceinline__ void pairs(const uint4 &q, F f) {
     }
 }
 // The largest magnitude of a thread's values, NaN left out
-template <int TYPE, bool HINTS>
-__device__ __forceinline__ float largest(const Pieces<HINTS> &p) {
+template <int TYPE>
+__device__ __forceinline__ float largest(const Pieces &p) {
     if constexpr (TYPE == GEMM_F32) {
         float m = 0.f;
 #pragma unroll
@@ -247,8 +240,8 @@ __device__ __forceinline__ float largest(const Pieces<HINTS> &p) {
 
 // A step's squares.  With every magnitude at most 2^40, and the largest at least 2^-56, neither squares nor the sums of 2^43
 // of them leave fp32's range, and what squares below its normal numbers lose does not count beside the largest.
-template <int TYPE, bool HINTS, typename W>
-__device__ __forceinline__ void add_squares(Pieces<HINTS> &p, const W &next, int thread, Sum &sum) {
+template <int TYPE, typename W>
+__device__ __forceinline__ void add_squares(Pieces &p, const W &next, int thread, Sum &sum) {
     float2 s[2] = {};
 #pragma unroll
     for (int i = 0; i < STEP; ++i) {
@@ -282,12 +275,12 @@ __device__ __forceinline__ void add_square(float v, Sum &sum) {
 }
 
 // The squares of a range, of which the last `keep` rows are to stay in L2
-template <bool HINTS, int N>
-__device__ __forceinline__ void norm_rows(const Table<N> &t, const Range &r, int start, int thread, uint32_t keep, Sum &sum) {
+template <typename T>
+__device__ __forceinline__ void norm_rows(const T &t, const Range &r, int start, int thread, uint32_t keep, Sum &sum) {
     if (r.begin >= r.end) return;
-    const uint64_t stay = HINTS ? in_turn() : 0, leave = HINTS ? first_out() : 0;
-    Walk<N> next(t, start);
-    Pieces<HINTS> p;
+    const uint64_t stay = in_turn(), leave = first_out();
+    Walk<T> next(t, start);
+    Pieces p;
     p.policy = r.end - r.begin > keep ? leave : stay;
     next.up(r.begin, r);
 #pragma unroll
@@ -297,7 +290,7 @@ __device__ __forceinline__ void norm_rows(const Table<N> &t, const Range &r, int
         const bool first = row == e.first;
         row += next.rows;
         if (row < r.end) next.up(row, r); else next.none();
-        if constexpr (HINTS) p.policy = r.end - row > keep ? leave : stay;
+        p.policy = r.end - row > keep ? leave : stay;
         if (e.type == GEMM_F32) add_squares<GEMM_F32>(p, next, thread, sum);
         else if (e.type == GEMM_BF16) add_squares<GEMM_BF16>(p, next, thread, sum);
         else add_squares<GEMM_F16>(p, next, thread, sum);
@@ -332,8 +325,8 @@ __device__ __forceinline__ Factor factor_of(const Sum &s, float limit, float &no
 
 // ------------------------------------------------------------------------------------------- results
 
-template <int TYPE, bool HINTS, typename W>
-__device__ __forceinline__ void scale_pieces(Pieces<HINTS> &p, uint4 *to, int left, const W &next, int thread, const Factor &factor) {
+template <int TYPE, typename W>
+__device__ __forceinline__ void scale_pieces(Pieces &p, uint4 *to, int left, const W &next, int thread, const Factor &factor) {
     const float2 rest = make_float2(factor.rest, factor.rest), none = make_float2(-0.f, -0.f);      // x * rest + -0 is x * rest
 #pragma unroll
     for (int i = 0; i < STEP; ++i) {
@@ -369,12 +362,12 @@ __device__ __forceinline__ void scale_apart(const Entry &e, uint32_t row, uint32
 }
 
 // A range scaled, its last rows first; `leave`: what it reads and writes leaves L2 first
-template <bool HINTS, int N>
-__device__ __forceinline__ void scale_rows(const Table<N> &t, const Range &r, int start, int thread, bool leave, const Factor &factor) {
+template <typename T>
+__device__ __forceinline__ void scale_rows(const T &t, const Range &r, int start, int thread, bool leave, const Factor &factor) {
     if (r.begin >= r.end || (factor.one && !t.copies)) return;
-    Walk<N> next(t, start);
-    Pieces<HINTS> p;
-    p.policy = !HINTS ? 0 : leave ? first_out() : in_turn();
+    Walk<T> next(t, start);
+    Pieces p;
+    p.policy = leave ? first_out() : in_turn();
     auto down = [&](uint32_t to) {                         // nothing to load where nothing is written, or apart
         next.down(to, r);
         const Entry &e = t.e[next.i];
@@ -420,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) clip_norm_kernel(const _
     Sum sum;
     wait_for_previous();
     let_next_launch();
-    norm_rows<true>(t, r, start, threadIdx.x, keep, sum);
+    norm_rows(t, r, start, threadIdx.x, keep, sum);
     sum = block_sum(sum);
     if (threadIdx.x == 0) {
         if ((int)blockIdx.x < before) sum.add(parts[blockIdx.x]);          // of the launches before this one
@@ -440,27 +433,111 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     float norm;
     const Factor factor = factor_of(block_sum(sum), limit, norm);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-    scale_rows<true>(t, r, start, threadIdx.x, leave, factor);
+    scale_rows(t, r, start, threadIdx.x, leave, factor);
 }
 
-// Few rows: one cluster does both, its CTAs' sums exchanged through shared memory.
-constexpr int FEW_CTAS = 8;
+// Few rows: one cluster does both, its CTAs' sums exchanged through shared memory.  A CTA has at most a row for each of its warps:
+// a thread holds its pieces of all of them, read at once, and warp i's lanes the elements before and behind the pieces of the
+// tensor that begins in row i.  Nothing is read twice: 20 011 values in 9 tensors 5.0 us, 7.2 with the rows walked twice.
+constexpr int FEW_CTAS = 8, FEW_HELD = THREADS / 32;
+constexpr uint32_t FEW_ROWS = FEW_CTAS * FEW_HELD;
+
+template <int TYPE>
+__device__ __forceinline__ void add_piece(const uint4 &q, Sum &sum) {
+    float2 s = both(0.f);
+    float amax = 0.f;
+    pairs<TYPE>(q, [&](float2 v) {
+        s = fma2(v, v, s);
+        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+    });
+    if (amax > 0x1p40f || (amax < 0x1p-56f && amax != 0.f)) {              // as in add_squares
+        const float2 shift = both(amax > 1.f ? 0x1p-70f : 0x1p90f);
+        s = both(0.f);
+        pairs<TYPE>(q, [&](float2 v) {
+            v = mul2(v, shift);
+            s = fma2(v, v, s);
+        });
+        sum.rest += (double)(s.x + s.y) * (amax > 1.f ? 0x1p140 : 0x1p-180);
+    } else {
+        sum.add(s.x + s.y);
+    }
+}
+// A piece scaled, element k of it the tensor's element `at` + k
+template <int TYPE>
+__device__ __forceinline__ void scale_piece(const Entry &e, const uint4 &q, int64_t at, const Factor &factor) {
+    float v[8];
+    int n = 0;
+    pairs<TYPE>(q, [&](float2 f) {
+        v[n++] = factor(f.x);
+        v[n++] = factor(f.y);
+    });
+    constexpr int SIZE = TYPE == GEMM_F32 ? 4 : 2;
+    if (e.apart) {
+#pragma unroll
+        for (int k = 0; k < 16 / SIZE; ++k) store_one(e.c, TYPE, at + k, v[k]);
+        return;
+    }
+    uint4 *to = reinterpret_cast<uint4 *>(e.c + at * SIZE);
+    if constexpr (TYPE == GEMM_F32)
+        *to = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    else if constexpr (TYPE == GEMM_BF16) *to = pack8(static_cast<const __nv_bfloat16 *>(nullptr), v);
+    else *to = pack8(static_cast<const __half *>(nullptr), v);
+}
+
 template <int N>
 __global__ void __launch_bounds__(THREADS)
-    clip_few_kernel(const __grid_constant__ Table<N> t, float limit, float *norm_out) {
+    clip_few_kernel(const __grid_constant__ Table<N, FEW_CTAS> t, float limit, float *norm_out) {
     __shared__ Part sums[FEW_CTAS];
     const Range r = range_of(t.rows, blockIdx.x, FEW_CTAS);
-    const int start = t.start[blockIdx.x];
-    Sum sum;
+    const int thread = threadIdx.x, warp = thread / 32, lane = thread % 32;
+    uint4 q[FEW_HELD];
+    int owner[FEW_HELD];                                   // the row's tensor, -1 past the range
+    int64_t at[FEW_HELD];                                  // the piece's first element, -1 where there is none
+    int64_t edge = -1;                                     // the thread's element outside the pieces
+    int edge_owner = 0;
+    float edge_value = 0.f;
+    int i = t.start[blockIdx.x];
     wait_for_previous();
     let_next_launch();
-    norm_rows<false>(t, r, start, threadIdx.x, 0, sum);
+#pragma unroll
+    for (int k = 0; k < FEW_HELD; ++k) {
+        const uint32_t row = r.begin + k;
+        owner[k] = -1;
+        at[k] = -1;
+        q[k] = make_uint4(0, 0, 0, 0);
+        if (row >= r.end) continue;
+        while (i + 1 < t.count && t.e[i + 1].first <= row) ++i;
+        const Entry &e = t.e[i];
+        const Span s(e);
+        const int64_t piece = (int64_t)(row - e.first) * THREADS + thread;
+        owner[k] = i;
+        if (piece < s.pieces) {
+            at[k] = s.head + piece * (e.type == GEMM_F32 ? 4 : 8);
+            q[k] = *reinterpret_cast<const uint4 *>(e.g + at[k] * (e.type == GEMM_F32 ? 4 : 2));
+        }
+        if (k == warp && row == e.first) {                 // lanes 0 to 6: before the pieces, 16 to 22: behind them
+            if (lane < s.head) edge = lane;
+            if (lane >= 16 && lane - 16 < s.tail) edge = e.n - s.tail + (lane - 16);
+            edge_owner = i;
+        }
+    }
+    if (edge >= 0) edge_value = load_one(t.e[edge_owner].g, t.e[edge_owner].type, edge);
+    Sum sum;
+#pragma unroll
+    for (int k = 0; k < FEW_HELD; ++k) {
+        if (owner[k] < 0) break;
+        const int type = t.e[owner[k]].type;
+        if (type == GEMM_F32) add_piece<GEMM_F32>(q[k], sum);
+        else if (type == GEMM_BF16) add_piece<GEMM_BF16>(q[k], sum);
+        else add_piece<GEMM_F16>(q[k], sum);
+    }
+    add_square(edge_value, sum);
     sum = block_sum(sum);
-    if (threadIdx.x < FEW_CTAS) {
+    if (thread < FEW_CTAS) {
         uint32_t to;
         asm("mapa.shared::cluster.u32 %0, %1, %2;"
             : "=r"(to)
-            : "r"((uint32_t)__cvta_generic_to_shared(&sums[blockIdx.x])), "r"(threadIdx.x));
+            : "r"((uint32_t)__cvta_generic_to_shared(&sums[blockIdx.x])), "r"(thread));
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(sum.high), "f"(sum.low) : "memory");
         asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + 8), "d"(sum.rest) : "memory");
     }
@@ -471,8 +548,21 @@ __global__ void __launch_bounds__(THREADS)
     for (int k = 0; k < FEW_CTAS; ++k) all.add(sums[k]);
     float norm;
     const Factor factor = factor_of(all, limit, norm);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-    scale_rows<false>(t, r, start, threadIdx.x, false, factor);
+    if (blockIdx.x == 0 && thread == 0) *norm_out = norm;
+    auto written = [&](const Entry &e) { return e.c && !(factor.one && e.c == e.g); };
+#pragma unroll
+    for (int k = 0; k < FEW_HELD; ++k) {
+        if (at[k] < 0) continue;
+        const Entry &e = t.e[owner[k]];
+        if (!written(e)) continue;
+        if (e.type == GEMM_F32) scale_piece<GEMM_F32>(e, q[k], at[k], factor);
+        else if (e.type == GEMM_BF16) scale_piece<GEMM_BF16>(e, q[k], at[k], factor);
+        else scale_piece<GEMM_F16>(e, q[k], at[k], factor);
+    }
+    if (edge >= 0) {
+        const Entry &e = t.e[edge_owner];
+        if (written(e)) store_one(e.c, e.type, edge, factor(edge_value));
+    }
 }
 
 // ------------------------------------------------------------------------------------------- launches
@@ -495,9 +585,18 @@ struct Call {
     cudaStream_t stream;
 };
 
-// Up to this many rows go to the single cluster: one launch where the host's two would be what a call costs (9 tensors of 20 011
-// values together 7.6 us in a queue of calls, two kernels 10.2; captured, 7.2 and 5.5)
-constexpr uint32_t FEW_ROWS = 64;
+// Up to FEW_ROWS rows go to the single cluster: one launch where the host's two would be what a call costs
+template <int N, int M>
+cudaError_t clip_few(const Call &k, const Table<M> &from) {
+    Table<N, FEW_CTAS> t;
+    t.count = from.count;
+    t.rows = from.rows;
+    t.copies = from.copies;
+    std::copy(from.start, from.start + FEW_CTAS, t.start);
+    std::copy(from.e, from.e + from.count, t.e);
+    const Launch c(FEW_CTAS, THREADS, 0, FEW_CTAS, k.stream);
+    return cudaLaunchKernelEx(&c.config, clip_few_kernel<N>, t, k.limit, k.norm);
+}
 
 // A list too large for L2: of what the first kernel reads the last KEEP_BYTES stay there, and what the second one is through
 // with leaves first.  100.7 million fp32 values 190 us, 195 without (48 million bytes 192); 291 tensors 62 and 66.
@@ -538,10 +637,7 @@ cudaError_t clip(const Call &k) {
     };
     for (int64_t l = 0; l < launches; ++l) {
         table(l);
-        if (few) {
-            const Launch c(FEW_CTAS, THREADS, 0, FEW_CTAS, k.stream);
-            return cudaLaunchKernelEx(&c.config, clip_few_kernel<N>, t, k.limit, k.norm);
-        }
+        if (few) return t.count <= 16 ? clip_few<16>(k, t) : clip_few<FEW_ROWS>(k, t);      // (a tensor has a row at least)
         const cudaError_t e = launch(clip_norm_kernel<N>, grid, THREADS, 0, k.stream, t, k.parts, parts,
                                      large ? (uint32_t)(KEEP_BYTES / ROW / grid) : ~0u);
         if (e != cudaSuccess) return e;
