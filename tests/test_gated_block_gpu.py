@@ -134,3 +134,72 @@ def test_decoding_on_the_blocks_own_weights(ff, m):  # noqa: F811
     # a step as norms (the products of random weights keep a relative error's size)
     assert rel(out, want) < 4.1 * 2.0 ** -8
     block.close()
+
+
+def test_two_blocks_on_two_streams(ff):  # noqa: F811
+    """Steps and decoded tokens of two blocks at once, nothing waited for in between: the bits of each block alone."""
+    def make(k):
+        block = ff.FeedForward(200 + 56 * k, 288, 544, seed=20 + k, fused=True)
+        return block, data(200 + 56 * k, 288, 30 + k), ff.Decoder(block)
+
+    def run(block, t, decoder, n):
+        kept = []
+        for i in range(n):
+            block.forward(t[0], t[1])
+            block.backward(t[2], t[3])
+            block.clip(2.0 + i)
+            few, _ = decoder(t[0][:3 + i], t[1][:3 + i])
+            kept += [block.out.clone(), block.dx.clone(), block.total.clone(), few, *(g.clone() for g in grads(block))]
+        return kept
+
+    made = [make(k) for k in range(2)]
+    alone = [run(*m, 6) for m in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    both = [[], []]
+    for _ in range(3):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                both[k] = run(*made[k], 6)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+    for block, _, _ in made:
+        assert block.up.last_status() == 0 and block.d_down.last_status() == 0
+        block.close()
+
+
+def test_two_graphs_of_one_block(ff):  # noqa: F811
+    """Two graphs of the same plans and buffers, replayed one behind the other in either order, and eager calls between them."""
+    block = ff.FeedForward(200, 544, 320, seed=40, fused=True)
+    inputs = [data(200, 544, 41 + k) for k in range(2)]
+
+    def run(t):
+        block.forward(t[0], t[1])
+        block.backward(t[2], t[3])
+        block.clip(1.0)
+
+    def results():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (block.out, block.dx, block.total, *grads(block))]
+
+    eager = []
+    for t in inputs:
+        run(t)
+        eager.append(results())
+    graphs = []
+    for t in inputs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(t)
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0)):
+        for k in order:
+            graphs[k].replay()
+            got = results()
+            assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(got, eager[k]))
+        run(inputs[order[0]])
+        graphs[order[1]].replay()
+        got = results()
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(got, eager[order[1]]))
+    block.close()
