@@ -62,6 +62,10 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
 }
+// the same by way of L1
+__device__ __forceinline__ void copy16_l1(uint32_t to, const void *from, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
 __device__ __forceinline__ void copy4(uint32_t to, const void *from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
@@ -215,6 +219,9 @@ __global__ void __launch_bounds__(WARPS * 32) few_kernel(const __grid_constant__
     wait_for_previous();
     let_next_launch();
 
+    // Rows of X that begin inside a sector of 32 bytes come by way of L1, where a sector that two copies share is read once:
+    // 8 x 8000 x 1000 8.9 us, 14.0 past it, 8 x 8192 x 4104 26.8 and 34.0; rows of whole sectors 8 x 8192 x 8192 44.2, 40.1 past it.
+    const bool whole_sectors = p.K % 16 == 0;
     // fills stage s with chunk c of the tile whose columns begin at f0: lane l has piece l % 8 of every fourth line from l / 8 on
     const int piece = at.lane % 8, line0 = at.lane / 8;
     auto fill = [&](int s, int c, int f0) {
@@ -232,8 +239,10 @@ __global__ void __launch_bounds__(WARPS * 32) few_kernel(const __grid_constant__
         for (int i = 0; i < 2 * NG; ++i) {
             const int m = line0 + 4 * i;
             if (m >= p.M) break;                          // zero from the start
-            copy16(to + R::OFF_X + m * 128 + 16 * half(m, piece),
-                   static_cast<const uint8_t *>(p.x) + (in ? m * row_bytes + byte : 0), in);
+            const uint32_t x_to = to + R::OFF_X + m * 128 + 16 * half(m, piece);
+            const uint8_t *from = static_cast<const uint8_t *>(p.x) + (in ? m * row_bytes + byte : 0);
+            if (whole_sectors) copy16(x_to, from, in);
+            else copy16_l1(x_to, from, in);
         }
     };
     // tokens that are not there are zero in every stage
