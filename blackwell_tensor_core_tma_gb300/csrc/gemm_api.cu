@@ -1101,12 +1101,15 @@ double gated_single_time(GatedForm form, int64_t tiles, int num_kb, int units, i
     const int kb = (num_kb + slices - 1) / slices;
     return f.launch1 + rounds * std::max(f.epilogue1, f.tile1 + f.kb1 * kb) + (slices > 1 ? GATED_EXCHANGE : 0.0);
 }
-// Backward: tiles of half the width, where all run at once.  A tile's epilogue, which bounds a short sum (1300 instructions of a
-// warp for 32 columns), is on twice as many SMs, and two warps issue its MMAs (gemm_gated.cuh): 200 x 1040 x 528 5.7 us, 7.7 in
-// tiles of 128 columns; 512 x 2048 x 2048 9.6, 12.3 in two slices; 256 x 2048 x 4096 14.6, 13.4 in four.  (Measured 4.4 us + 0.158
-// per k-block; 0.8 less here, by which the estimate of slices is low.)  Where DY's rows begin within lines of 128 bytes its boxes
-// take up to twice as many lines: 128 x 8192 x 3000 20 us, 16.5 in two slices.
-double gated_narrow_time(int64_t N) { return 3.6 + (N % 64 == 0 ? 0.158 : 0.24) * (double)((N + 63) / 64); }
+// Backward: tiles of half the width, whole or sliced, where all run at once.  A tile's epilogue, which bounds a short sum (1300
+// instructions of a warp for 32 columns), is on twice as many SMs, and two warps issue its MMAs (gemm_gated.cuh): 200 x 1040 x 528
+// 5.7 us, 7.7 in tiles of 128 columns; 200 x 1040 x 4096 8.6 in four slices, 12.7; 256 x 2048 x 16384 26 in two, 25.3 in four of 128
+// columns.  (Measured 4.4 us + 0.158 per k-block, with slices 5.8; 0.8 less here, by which the estimate of wider ones is low.)  Where
+// DY's rows begin within lines of 128 bytes its boxes take up to twice as many lines: 128 x 8192 x 3000 20 us, 16.2 in two slices of
+// 128 columns.
+double gated_narrow_time(int64_t N, int slices) {
+    return 3.6 + (N % 64 == 0 ? 0.158 : 0.24) * (double)(((N + 63) / 64 + slices - 1) / slices) + (slices > 1 ? 1.5 : 0.0);
+}
 double gated_pair_time(GatedForm form, int64_t tiles, int num_kb, int units) {
     const GatedForms f = gated_forms(form);
     const int64_t rest = tiles % units;
@@ -1170,24 +1173,26 @@ gemm_status gated_plan_create(gemm_plan_t *out, int family, int64_t M, int64_t F
         if (singles * s <= units && singles <= prepare(1, s)) slices = s;
     const GatedShape wide = gated_shape(form, 2, 1);
     double single = gated_single_time(form, singles, num_kb, units, slices);
-    const bool narrow = form == GATED_BACK && tiles_of(gated_shape(GATED_BACK_NARROW, 1, 1), 1) <= units &&
-                        gated_narrow_time(K) < single;
-    if (narrow) single = gated_narrow_time(K);
+    int narrow = 0;                                  // backward: slices of tiles of half the width where those are faster
+    if (form == GATED_BACK) {
+        const int64_t thin = tiles_of(gated_shape(GATED_BACK_NARROW, 1, 1), 1);
+        for (int s = 1, n = 0; s <= 8 && thin * s <= units && (s == 1 || num_kb >= GATED_SLICE_KB * s); s *= 2)
+            if (gated_narrow_time(K, s) < single && gated_prepare(GATED_BACK_NARROW, 1, s, &n) == cudaSuccess && thin <= n) {
+                narrow = s;
+                single = gated_narrow_time(K, s);
+            }
+    }
     const bool pair = gated_pair_time(form, tiles_of(wide, 2), num_kb, pairs) < single;
     const int cg = flags & GEMM_FLAG_FORCE_1CTA ? 1 : flags & GEMM_FLAG_FORCE_2CTA ? 2 : pair ? 2 : 1;
     if (cg == 2) {
         sh = wide;
         units = pairs;
         slices = 1;
-    } else if (!narrow) {
-        sh = gated_shape(form, 1, slices);
+    } else if (narrow > 0) {
+        slices = narrow;
+        sh = gated_shape(GATED_BACK_NARROW, 1, slices);
     } else {
-        slices = 1;
-        sh = gated_shape(GATED_BACK_NARROW, 1, 1);
-        if (gated_prepare(GATED_BACK_NARROW, 1, 1, &units) != cudaSuccess || units <= 0) {
-            delete p;
-            return GEMM_ERR_CUDA;
-        }
+        sh = gated_shape(form, 1, slices);
     }
     p->cta_group = cg;
     p->stages = sh.stages;

@@ -3,7 +3,7 @@
 //                      or sliced along K
 //   forward, e4m3      the same tiles; a pair's accumulator takes half of tensor memory and the scales of
 //                      the stages part of the rest, so that the epilogue empties it into registers at once
-//   backward, 16-bit   pairs, 256 x 256 tiles; single CTAs, 128 x 128 tiles, whole or sliced, and 128 x 64
+//   backward, 16-bit   pairs, 256 x 256 tiles; single CTAs, 128 x 128 and 128 x 64 tiles, whole or sliced
 // each with as many stages as shared memory holds.
 #include "gemm_gated.cuh"
 
@@ -21,6 +21,7 @@ using Mx8SlicedPacked = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 4, 2, 8,
 using BackPair = GatedInstance<GatedCfg<2, KIND_F16, true, 256, 5, 2, 8>>;
 using BackSingle = GatedInstance<GatedCfg<1, KIND_F16, true, 128, 5, 2, 8>>;
 using BackNarrow = GatedInstance<GatedCfg<1, KIND_F16, true, 64, 7, 2, 8, 0, false, false, 2>>;
+using BackNarrowSliced = GatedInstance<GatedCfg<1, KIND_F16, true, 64, 7, 2, 8, 0, false, true, 2>>;
 using BackSliced = GatedInstance<GatedCfg<1, KIND_F16, true, 128, 5, 2, 8, 0, false, true>>;
 
 // f(instance) for a form, a CTA group and a number of slices
@@ -30,7 +31,7 @@ auto with(GatedForm form, int cta_group, int slices, F f) {
     if (form == GATED_F16) return pair ? f(F16Pair()) : sliced ? f(F16Sliced()) : f(F16Single());
     if (form == GATED_MXF8) return sliced ? f(Mx8Sliced()) : f(Mx8Single());
     if (form == GATED_MXF8_PACKED) return pair ? f(Mx8Pair()) : sliced ? f(Mx8SlicedPacked()) : f(Mx8SinglePacked());
-    if (form == GATED_BACK_NARROW) return f(BackNarrow());
+    if (form == GATED_BACK_NARROW) return sliced ? f(BackNarrowSliced()) : f(BackNarrow());
     return pair ? f(BackPair()) : sliced ? f(BackSliced()) : f(BackSingle());
 }
 

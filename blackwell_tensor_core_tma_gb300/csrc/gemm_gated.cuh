@@ -106,14 +106,15 @@ struct GatedCfg {
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
     static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
     static constexpr int OFF_EPI = align1k(OFF_SF + SF_RING * SF_GROUP * SF_BLOCKS * 512);
-    // Tiles sliced along K over a cluster's CTAs (2, 4 or 8): of the tile's eight pieces of 32 rows and 64 columns a CTA owns
-    // 8 / slices.  Each has a staging buffer, and behind those the other slices' fp32 sums of it, 8 KiB each.
+    // Tiles sliced along K over a cluster's CTAs (2, 4 or 8): of the tile's eight pieces, a warp's 32 rows and half of the tile's
+    // columns, a CTA owns 8 / slices.  Each has a staging buffer, and behind those the other slices' fp32 sums of it.
     static constexpr bool SLICED = SLICED_;
     static_assert(!SLICED || CG == 1, "slices over single CTAs");
     static constexpr int MAX_SLICES = SLICED ? 8 : 1;
-    static constexpr int PIECE = 8192;
-    static constexpr int EPI_BYTES = SLICED ? EPI_BUF + 7 * PIECE : EPI_WARPS * EPI_BUF;
-    static_assert(!SLICED || (2 * (EPI_BUF + 3 * PIECE) <= EPI_BYTES && 4 * (EPI_BUF + PIECE) <= EPI_BYTES), "two, four slices");
+    static constexpr int PIECE = 4096 * WCHUNKS * (BACK ? 1 : 2);
+    static constexpr int larger(int x, int y) { return x > y ? x : y; }
+    static constexpr int EPI_BYTES = SLICED ? larger(EPI_BUF + 7 * PIECE, larger(2 * (EPI_BUF + 3 * PIECE), 4 * (EPI_BUF + PIECE)))
+                                            : EPI_WARPS * EPI_BUF;
     static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
     // full[FULLS], empty[STAGES], tfull[2], tempty[2], drain, then with COPIER: cdrain and, per group of scales,
     // sffull (packed ones have landed), sfready (grouped ones are in tensor memory), sfempty (their MMAs are done)

@@ -345,7 +345,9 @@ def test_sliced_tiles(M, F, K, kind, slices):
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("M,F,N,slices", [(40, 80, 8200, 8), (300, 272, 4104, 8), (300, 1040, 4104, 4),
-                                              (129, 2064, 8232, 4), (520, 1552, 4176, 2), (520, 1552, 4160, 1)])
+                                              (129, 2064, 8232, 4), (520, 1552, 4176, 2), (520, 1552, 4160, 1),
+                                              (300, 528, 8200, 8), (200, 1040, 4096, 4), (256, 2048, 2048, 2),
+                                              (33, 528, 3000, 4)])
 def test_sliced_backward(M, F, N, kind, slices):
     DY, W2, (CK, SF, g, u) = backward_case(M, F, N, kind)
     with gemm.GatedBackPlan(M, F, N, kind) as plan:
@@ -416,12 +418,13 @@ def test_what_a_run_launches(M, F, K, kind, flags, launches, slices):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
-@pytest.mark.parametrize("M,F,N,tile", [(1000, 1296, 72, 128), (520, 1040, 648, 64), (129, 4112, 8, 64), (64, 16, 1000, 64)])
-def test_backward_widths_of_single_tiles(M, F, N, kind, tile):
+@pytest.mark.parametrize("M,F,N,tile,slices", [(1000, 1296, 72, 128, 1), (520, 1040, 648, 64, 1), (129, 4112, 8, 64, 1),
+                                               (64, 16, 1000, 64, 2)])
+def test_backward_widths_of_single_tiles(M, F, N, kind, tile, slices):
     """Tiles of 64 columns where all of them run at once, else of 128."""
     DY, W2, (CK, SF, g, u) = backward_case(M, F, N, kind)
     with gemm.GatedBackPlan(M, F, N, kind, ONE) as plan:
-        assert (plan.info["tile_n"], plan.info["splits"], plan.info["cta_group"]) == (tile, 1, 1)
+        assert (plan.info["tile_n"], plan.info["splits"], plan.info["cta_group"]) == (tile, slices, 1)
         DZ, A = backward(plan, dev(DY), dev(W2), dev(CK), dev(SF), M, F, kind, True)
         check_backward(DZ, A, DY, W2, g, u, kind)
 
