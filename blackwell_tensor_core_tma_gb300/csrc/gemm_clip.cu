@@ -603,11 +603,20 @@ cudaError_t clip_few(const Call &k, const Table<M> &from) {
 // The stores' part of it alone costs 1 %.
 constexpr int64_t L2_BYTES = 60000000, KEEP_BYTES = 96000000;
 
+// CTAs of a list with little for each: with two per SM the second kernel's are on the SMs, and wait, before the first kernel's
+// leave, with five (of 48 registers a thread) they are not, 5 us in all.  One tensor of a million bf16 values 7.3 us, 11.5 with
+// five, 8 million 13.0 and 16.2; 300 tensors of 1 million 12.1 and 14.1, of 4 million 18.4 and 17.2.  A tensor counts as two steps
+// beside its own: its first and last elements.
+constexpr int FEW_PER_SM = 2, FEW_STEPS = 8;
+uint32_t ctas_of(uint32_t rows, int64_t steps, int count, int sms) {
+    const int most = std::min((steps + 2 * count <= FEW_STEPS * sms ? FEW_PER_SM : CTAS_PER_SM) * sms, MAX_PARTS);
+    return std::min(std::max(1u, rows), (uint32_t)most);
+}
+
 // The tensors in launches of up to N: all norms' kernels, then all scalings'
 template <int N>
 cudaError_t clip(const Call &k) {
     const int64_t launches = std::max<int64_t>(1, (k.count + N - 1) / N);
-    const int most = std::min(CTAS_PER_SM * k.sms, MAX_PARTS);
     Table<N> t;
     int parts = 0, grid = 0;
     bool any = false, few = false, large = false;
@@ -615,6 +624,7 @@ cudaError_t clip(const Call &k) {
         t.count = 0;
         t.rows = 0;
         t.copies = false;
+        int64_t steps = 0;
         const int64_t first = l * N, last = std::min<int64_t>(first + N, k.count);
         for (int64_t i = first; i < last; ++i) {
             const gemm_clip_tensor &from = k.tensors[i];
@@ -622,13 +632,15 @@ cudaError_t clip(const Call &k) {
             const uintptr_t apart = reinterpret_cast<uintptr_t>(from.g) ^ reinterpret_cast<uintptr_t>(from.c);
             t.e[t.count++] = Entry{static_cast<const uint8_t *>(from.g), static_cast<uint8_t *>(from.c), from.n, t.rows,
                                    (int16_t)from.type, (int16_t)((apart & 15) != 0)};
-            t.rows += (uint32_t)rows_of(from);
+            const int64_t rows = rows_of(from);
+            t.rows += (uint32_t)rows;
+            steps += (rows + STEP - 1) / STEP;
             t.copies = t.copies || (from.c && from.c != from.g);
             any = any || from.c;
         }
         few = launches == 1 && t.rows <= FEW_ROWS;
         large = launches == 1 && (int64_t)t.rows * ROW > L2_BYTES;
-        grid = few ? FEW_CTAS : (int)std::min<uint32_t>(std::max(1u, t.rows), (uint32_t)most);
+        grid = few ? FEW_CTAS : (int)ctas_of(t.rows, steps, t.count, k.sms);
         for (int b = 0, i = 0; b < grid; ++b) {
             const uint32_t begin = range_of(t.rows, (uint32_t)b, (uint32_t)grid).begin;
             while (i + 1 < t.count && t.e[i + 1].first <= begin) ++i;
