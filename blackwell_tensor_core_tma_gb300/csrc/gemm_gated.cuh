@@ -608,6 +608,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             };
 
             if constexpr (!Cfg::BACK) {
+                const uint32_t box_g = box + 2048, box_u = box_g + 1024;     // behind a's two KiB, a KiB each
                 auto finish = [&](int c, const uint32_t (&gr)[32], const uint32_t (&ur)[32]) {
                     if (c >= chunks) return;
                     const int f = f_warp + EPI_COLS * c;
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         round_chunk(a, bf16, box, lane);
                     }
                     if (p.has_z) {
-                        const uint32_t cg = quantise_chunk(g, box + 2048, lane), cu = quantise_chunk(u, box + 3072, lane);
+                        const uint32_t cg = quantise_chunk(g, box_g, lane), cu = quantise_chunk(u, box_u, lane);
                         if (row < p.M) {
                             uint8_t *sf = p.sfck + (block + (int64_t)row * blocks);
                             sf[0] = (uint8_t)cg;
@@ -647,8 +648,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         const int x = checked_x<1>(p.status, f, p.F), y = checked_y(p.status, m_warp, p.M);
                         tma_store_2d_hint(&tmA, box, x, y, stream_pol);
                         if (p.has_z) {
-                            tma_store_3d_hint(&tmZ, box + 2048, x, 0, y, stream_pol);
-                            tma_store_3d_hint(&tmZ, box + 3072, x, 1, y, stream_pol);
+                            tma_store_3d_hint(&tmZ, box_g, x, 0, y, stream_pol);
+                            tma_store_3d_hint(&tmZ, box_u, x, 1, y, stream_pol);
                         }
                         bulk_commit_group();
                     }
