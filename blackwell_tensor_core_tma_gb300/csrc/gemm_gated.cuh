@@ -20,9 +20,10 @@
 //     (GROUPED: single CTAs, whose products are short, where every row of scales begins at a multiple of 16 bytes) are
 //     read as the operands' owners have them: the copying warp loads sixteen bytes of a row (a group of four
 //     k-blocks) ahead of their use, writes the group's words to shared memory in tensor memory's order and copies them
-//     there, into a ring of groups of its own: 64 x 8192 x 4096 takes 18 us, 24.7 with the packing kernel.  (For pairs
-//     the way over both CTAs' warps takes 2 us per group, twice its MMAs' time: 4096 x 8192 x 8192 458 us, 385 with the
-//     packing kernel; rows that begin anywhere cost ten loads for one, 30 us at 64 x 8192 x 4064.)
+//     there, into a ring of groups of its own: 64 x 8192 x 4096 takes 17.4 us, 22.6 with the packing kernel (captured 17.7
+//     and 20.3).  (For pairs the way over both CTAs' warps takes 2 us per group, twice its MMAs' time: 4096 x 8192 x 8192 458 us,
+//     385 with the packing kernel; rows that begin anywhere cost ten loads for one, 30 us at 64 x 8192 x 4064; a second form for
+//     rows at multiples of 8 bytes in the same kernel costs the first one 2.5 us.)
 //   * A thread owns a row; its chunk of 32 columns is one scale block of e4m3, so that a block's
 //     maximum is a thread's own.
 //   * Backward: B is N-contiguous (W2 as the forward product has it), g and u come as 8-bit codes
