@@ -1084,14 +1084,14 @@ namespace {
 // better form on average, 9 % at most.  For example, bf16, single CTAs and pairs: 1024 x 2048 x 4096 33.8 and 23.6, 256 x
 // 4096 x 4096 18.9 and 19.9, 256 x 2048 x 4096 17.9 whole, 13.6 in two slices, and 19.3.
 struct GatedForms {
-    double launch1, epilogue1, tile1, kb1;    // single CTAs
+    double launch1, epilogue1, tile1, kb1, kb_sliced;    // single CTAs
     double launch2, epilogue2, tile2, kb2;    // pairs
     double half;                              // a round of halved tiles, of a whole one's time
 };
 GatedForms gated_forms(GatedForm form) {
-    if (form == GATED_BACK) return {3.6, 4.2, 1.2, 0.255, 3.6, 9.0, 5.0, 0.31, 0.75};
-    if (form == GATED_F16) return {2.9, 1.4, 0.1, 0.245, 3.0, 2.75, 0.6, 0.30, 0.85};
-    return {3.4, 1.2, 0.35, 0.375, 5.5, 2.9, 1.5, 0.33, 0.85};
+    if (form == GATED_BACK) return {3.6, 4.2, 1.2, 0.22, 0.255, 3.6, 9.0, 5.0, 0.31, 0.75};
+    if (form == GATED_F16) return {2.9, 1.3, 0.1, 0.215, 0.245, 3.0, 2.75, 0.6, 0.30, 0.85};
+    return {3.4, 1.2, 0.35, 0.375, 0.375, 5.5, 2.9, 1.5, 0.33, 0.85};
 }
 constexpr double GATED_EXCHANGE = 2.4;
 constexpr int GATED_SLICE_KB = 8;             // k-blocks of the shortest slice: 4096 x 512 x 1024 7.5 us in none, 7.7 in two
@@ -1099,7 +1099,8 @@ double gated_single_time(GatedForm form, int64_t tiles, int num_kb, int units, i
     const GatedForms f = gated_forms(form);
     const double rounds = slices > 1 ? 1.0 : (double)((tiles + units - 1) / units);
     const int kb = (num_kb + slices - 1) / slices;
-    return f.launch1 + rounds * std::max(f.epilogue1, f.tile1 + f.kb1 * kb) + (slices > 1 ? GATED_EXCHANGE : 0.0);
+    return f.launch1 + rounds * std::max(f.epilogue1, f.tile1 + (slices > 1 ? f.kb_sliced : f.kb1) * kb) +
+           (slices > 1 ? GATED_EXCHANGE : 0.0);
 }
 // Backward: tiles of half the width, whole or sliced, where all run at once.  A tile's epilogue, which bounds a short sum (1300
 // instructions of a warp for 32 columns), is on twice as many SMs, and two warps issue its MMAs (gemm_gated.cuh): 200 x 1040 x 528

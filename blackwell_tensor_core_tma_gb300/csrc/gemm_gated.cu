@@ -11,7 +11,7 @@ namespace gb300 {
 namespace {
 
 using F16Pair = GatedInstance<GatedCfg<2, KIND_F16, false, 128, 6, 2, 8>>;
-using F16Single = GatedInstance<GatedCfg<1, KIND_F16, false, 64, 6, 2, 8>>;
+using F16Single = GatedInstance<GatedCfg<1, KIND_F16, false, 64, 6, 2, 8, 0, false, false, 2>>;
 using F16Sliced = GatedInstance<GatedCfg<1, KIND_F16, false, 64, 5, 2, 8, 0, false, true>>;
 using Mx8Pair = GatedInstance<GatedCfg<2, KIND_MXF8, false, 128, 5, 1, 8, 2>>;
 using Mx8Single = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 5, 2, 8, 2, true>>;
@@ -19,7 +19,7 @@ using Mx8SinglePacked = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 5, 2, 8,
 using Mx8Sliced = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 4, 2, 8, 2, true, true>>;
 using Mx8SlicedPacked = GatedInstance<GatedCfg<1, KIND_MXF8, false, 64, 4, 2, 8, 1, false, true>>;
 using BackPair = GatedInstance<GatedCfg<2, KIND_F16, true, 256, 5, 2, 8>>;
-using BackSingle = GatedInstance<GatedCfg<1, KIND_F16, true, 128, 5, 2, 8>>;
+using BackSingle = GatedInstance<GatedCfg<1, KIND_F16, true, 128, 5, 2, 8, 0, false, false, 2>>;
 using BackNarrow = GatedInstance<GatedCfg<1, KIND_F16, true, 64, 7, 2, 8, 0, false, false, 2>>;
 using BackNarrowSliced = GatedInstance<GatedCfg<1, KIND_F16, true, 64, 7, 2, 8, 0, false, true, 2>>;
 using BackSliced = GatedInstance<GatedCfg<1, KIND_F16, true, 128, 5, 2, 8, 0, false, true>>;

@@ -32,7 +32,8 @@
 //     are 11 to 12 us of the rest each, the arithmetic 1.5.)
 //   * Two warps may issue a CTA's MMAs, every other k-block each, into accumulators that the epilogue adds: one thread takes 450
 //     clocks for a k-block's four MMAs, their wait and their commit, whatever their N.  Backward tiles of 64 columns: 0.158 us per
-//     k-block, 0.237 with one.  (128 columns gain nothing: there the operands' way from L2 takes as long.)
+//     k-block, 0.237 with one.  Tiles of 128: forward 512 x 2048 x 2048 9.8 us, 10.8, backward 1024 x 2048 x 1024 9.4, 9.9; sliced
+//     ones, whose operands' way from L2 takes as long, 128 x 4096 x 4096 17.8, 17.5 with one.
 //   * Where tiles are few, a tile's K is cut into slices over the single CTAs of a cluster, which exchange their sums
 //     before the unit: each finishes the share of the tile's 32 x 32 pieces that it owns, adding all slices in their order.
 // Every wait is bounded as in gemm_tc_kernel.
