@@ -1080,9 +1080,9 @@ namespace {
 // The form of a gated product: single CTAs with 128 x 64 (backward 128 x 128) tiles, whose K may be cut into slices, or CTA
 // pairs with 256 x 128 (256 x 256) ones.  Estimated time in microseconds = a launch + rounds of tiles x the longer of a
 // tile's epilogue and its k-blocks (+ the exchange of slices), constants fitted to 140 shapes of each kind of operand (M 32
-// to 4096, F 512 to 8192, K 256 to 8192), both forms of each measured; the rule's choice is within 0.3 % of the
-// better form on average, 9 % at most.  For example, bf16, single CTAs and pairs: 1024 x 2048 x 4096 33.8 and 23.6, 256 x
-// 4096 x 4096 18.9 and 19.9, 256 x 2048 x 4096 17.9 whole, 13.6 in two slices, and 19.3.
+// to 4096, F 512 to 8192, K 256 to 8192), both forms of each measured; the rule's choice is within 0.2 % of the
+// better form on average, 9 % at most.  For example, bf16, single CTAs and pairs: 1024 x 2048 x 4096 29.6 and 23.4, 256 x
+// 4096 x 4096 17.5 and 20.1, 256 x 2048 x 4096 13.3 in two slices and 19.5.
 struct GatedForms {
     double launch1, epilogue1, tile1, kb1, kb_sliced;    // single CTAs
     double launch2, epilogue2, tile2, kb2;    // pairs
