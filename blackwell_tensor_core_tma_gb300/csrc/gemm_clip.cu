@@ -302,19 +302,21 @@ __device__ __forceinline__ void norm_rows(const T &t, const Range &r, int start,
     }
 }
 
-// limit / norm as a product of two: where it is below fp32's normal numbers' upper part, a power of two and the rest
+// limit / norm as a product of two: where it is below 2^-100, a power of two and the rest.  The rest comes first: it is below one,
+// and where it takes a value below fp32's normal numbers the power leaves zero of that.
 struct Factor {
     float rest, power;
     bool one;
-    __device__ __forceinline__ float operator()(float v) const { return v * power * rest; }
+    __device__ __forceinline__ float operator()(float v) const { return v * rest * power; }
 };
 // min(1, limit / norm); a norm that is not a number makes a factor that is none
 __device__ __forceinline__ Factor factor_of(const Sum &s, float limit, float &norm) {
     if (!any_bits(s.rest) && s.high >= 0x1p-100f) {            // at least the largest square, and at most 2^125
         norm = sqrtf(s.high + s.low);
-        const bool one = norm <= limit;
-        const float power = limit < 0x1p-60f ? 0x1p-60f : 1.f;
-        return {one ? 1.f : limit / power / norm, one ? 1.f : power, one};
+        if (norm <= limit) return {1.f, 1.f, true};
+        const float ratio = limit / norm;
+        if (ratio >= 0x1p-100f) return {ratio, 1.f, false};
+        return {limit * 0x1p100f / norm, 0x1p-100f, false};
     }
     const double exact = sqrt((double)s.high + (double)s.low + s.rest), ratio = (double)limit / exact;
     norm = (float)exact;
@@ -333,11 +335,11 @@ __device__ __forceinline__ void scale_pieces(Pieces &p, uint4 *to, int left, con
         float v[8];
         int n = 0;
         pairs<TYPE>(p.q[i], [&](float2 f) {
+            f = fma2(f, rest, none);
             if (factor.power != 1.f) {
                 f.x *= factor.power;
                 f.y *= factor.power;
             }
-            f = fma2(f, rest, none);
             v[n++] = f.x;
             v[n++] = f.y;
         });
