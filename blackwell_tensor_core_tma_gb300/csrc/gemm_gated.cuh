@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                             on = f < p.F;
                         }
                         r.w[b][k] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                        if (on) r.w[b][k] = __ldg(reinterpret_cast<const uint4 *>((b == 0 ? p.sfx : p.sfw) + row * sfk) + g);
+                        if (on) r.w[b][k] = reinterpret_cast<const uint4 *>((b == 0 ? p.sfx : p.sfw) + row * sfk)[g];
                     }
                 return r;
             };

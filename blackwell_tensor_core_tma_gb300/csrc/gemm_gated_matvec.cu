@@ -89,7 +89,7 @@ __device__ __forceinline__ uint32_t shared4(uint32_t at) {
 }
 
 __device__ __forceinline__ uint4 load_row(const void *p, bool on) {
-    return on ? __ldg(static_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
+    return on ? *static_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
 }
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) few_scaled_kernel(const __gri
             uint32_t w = 0x7F7F7F7Fu;
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                if (f < p.F && 4 * c + b < blocks) w = (w & ~(0xFFu << 8 * b)) | (uint32_t)__ldg(sf + b) << 8 * b;
+                if (f < p.F && 4 * c + b < blocks) w = (w & ~(0xFFu << 8 * b)) | (uint32_t)sf[b] << 8 * b;
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(sf_to), "r"(w) : "memory");
         }
     };

@@ -31,3 +31,11 @@ def test_no_store_to_a_cta_that_has_not_begun():
     # and once more behind the stores, before the sums are read
     assert store < code.find("cluster_arrive()", store) < code.find("cluster_wait()", store) < code.index("all.add(")
     assert code.count("cluster_arrive()") == code.count("cluster_wait()") == 2
+
+
+def test_no_load_may_be_moved_ahead_of_the_wait_for_earlier_kernels():
+    """A kernel that begins while the one before it still writes: no load that takes its data to be the same all through."""
+    names = [n for n in sorted(os.listdir(build.CSRC)) if "wait_for_previous()" in source(n)]
+    assert {"gemm_gated.cuh", "gemm_gated_matvec.cu", "gemm_clip.cu", "gemm_norm.cu", "gemm_gate.cu", "gemm_matvec.cu"} <= set(names)
+    for name in names:
+        assert not re.search(r"__ldg\s*\(|ld\.global(\.\w+)*\.nc\b|const\s[^;,{}()]*\*\s*__restrict__", source(name)), name
