@@ -158,3 +158,42 @@ def test_replays_element_by_element(sizes):
         check(c, 0.25, float(norms[1]), [t.cpu() for t in C2])
         assert float(norms[1]) == float(norms[2]) == float(norms[3])
         assert all(torch.equal(a, b) for a, b in zip(C2, C3))
+
+
+@pytest.mark.parametrize("sizes", [[3001, 5, 1030, 77, 4097], [200003, 5, 90001, 77, 70001], [3, 41, 5, 16, 1] * 400],
+                         ids=["cluster", "kernels", "launches"])
+def test_lists_of_every_kind_of_output(sizes):
+    """In one list: tensors that only count, in place, written elsewhere, and elsewhere at another place of 16 bytes."""
+    G = make(sizes, ["f32", "bf16", "f16"])
+    kinds = [("f32", "bf16", "f16")[i % 3] for i in range(len(G))]
+    want = exact_norm(G)
+    for limit in (0.3 * want, 3.0 * want):
+        tensors, outs = [], []
+        for i, (g, k) in enumerate(zip(G, kinds)):
+            src = g.cuda()
+            pool = torch.zeros(g.numel() + 16, dtype=g.dtype, device="cuda")
+            c = (None, src, pool[8:8 + g.numel()], pool[1:1 + g.numel()])[i % 4]
+            tensors.append((src, c, k))
+            outs.append((src, c, pool))
+        norm = torch.empty(1, device="cuda")
+        work = torch.empty(gemm.GEMM_CLIP_WORKSPACE, dtype=torch.uint8, device="cuda")
+        gemm.gemm_clip_run(gemm.clip_tensors(tensors), limit, norm, work, stream=torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        written = [i for i, (_, c, _) in enumerate(outs) if c is not None]
+        assert abs(float(norm) - want) <= NORM * want
+        factor = min(1.0, float(torch.tensor(limit)) / want)
+        for i in written:
+            g, c, v = G[i], outs[i][1].cpu(), G[i].double() * factor
+            if factor == 1.0:
+                assert torch.equal(c, g)
+            else:
+                tol = ref.half_ulp(v, kinds[i]) * (1 + 2.0 ** -10) + (NORM + 3 * ref.U) * v.abs()
+                ref.assert_within("c", c, v, tol + 2.0 ** -149)
+        for i, (src, c, pool) in enumerate(outs):
+            if c is not src:
+                assert torch.equal(src.cpu(), G[i])
+            start = {2: 8, 3: 1}.get(i % 4)
+            rest = pool.clone()
+            if start is not None:
+                rest[start:start + G[i].numel()] = 0
+            assert not rest.any()
