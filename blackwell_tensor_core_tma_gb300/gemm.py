@@ -418,7 +418,7 @@ class ClipTensors:
                 for x in (g, c):
                     if x is not None and not (x.is_contiguous() and x.numel() == g.numel() and x.dtype == g.dtype):
                         raise ValueError("tensors are contiguous, and c has g's size and type")
-                if TORCH_NAMES[DTYPE.get(kind, kind)] != str(g.dtype):
+                if TORCH_NAMES.get(DTYPE.get(kind, kind)) != str(g.dtype):
                     raise ValueError(f"{g.dtype} is not {kind}")
             entry.g, entry.c, entry.n, entry.type = _ptr(g), _ptr(c), n[0] if n else g.numel(), DTYPE.get(kind, kind)
 
