@@ -376,6 +376,10 @@ __device__ __forceinline__ uint32_t largest2(uint32_t a, uint32_t b) {          
 constexpr int CHUNK = 128;                                 // of k: a line of a weight row
 constexpr int STAGE = 16 * 128 + 16 * 4;                   // 8 rows of g, 8 of u, and their scales
 constexpr int WIDE_WARPS = 16;
+// bf16 activations: a chunk's sum of up to 2^15 |w| for each of 128 k takes the weights' scales before the token's power of two, so
+// 2^-22 goes with the scales, and no weight that fp32 holds takes it past fp32.  The power of two has 2^14 of that back, the
+// joined sums 2^8.  (Far below, a block's sum is off by up to 2^-142 of the largest activation.)
+constexpr float SCALE_DOWN = 0x1p-22f, SUMS_UP = 0x1p8f;
 template <int NG>
 struct Wide {
     static constexpr int DEPTH = NG == 1 ? 4 : 3;                                   // stages of a warp's ring
@@ -536,9 +540,9 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) few_scaled_kernel(const __gri
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     scales(shared4(from + 16 * 128 + 32 * z + 4 * at.r), scale[z]);
-                    if constexpr (BF16) {                 // sums as large as the weights', not 2^14 times that
+                    if constexpr (BF16) {
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) scale[z][b] *= 0x1p-14f;
+                        for (int b = 0; b < 4; ++b) scale[z][b] *= SCALE_DOWN;
                     }
                 }
 #pragma unroll
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) few_scaled_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < NG; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[at.warp][j][e][at.lane] = acc[j][e];
+            for (int e = 0; e < 4; ++e) part[at.warp][j][e][at.lane] = BF16 ? acc[j][e] * SUMS_UP : acc[j][e];
         __syncthreads();
         const int outputs = p.groups * 64 * NG;
         float sums[TURNS][2];

@@ -464,7 +464,9 @@ gemm_status gemm_gated_back_run(gemm_plan_t p, const void *DY, const void *W2, c
  * The gated product for 1 to 16 rows: one token, or a few, through a gated plan's weights.  X: M x K and A: M x F of type
  * x = a, GEMM_BF16 or GEMM_F16; W: 2F x K of type w = x, or GEMM_E4M3 with SFW as above.  Sums in fp32, in an order that depends on
  * M, F, K, the types, the GPU's SM count and how many clusters it runs at once.  e4m3 weights meet activations in fp16: bf16 ones relative to the
- * largest of their token's 128 aligned k, of which those below 2^-31 are off by up to 2^-39 of it.  Any F from 1 to 2^20 (GEMM_ERR_INVALID_ARG);
+ * largest of their token's 128 aligned k, of which those below 2^-31 are off by up to 2^-39 of it; and a sum
+ * over 32 of k may be off by 2^-142 of that largest one, which counts beside weights below 2^-118 alone.  Weights are finite in
+ * fp32.  Any F from 1 to 2^20 (GEMM_ERR_INVALID_ARG);
  * K % 8 == 0, for e4m3 K % 16 == 0 (GEMM_ERR_ALIGNMENT); M > 16 or K > 32768: GEMM_ERR_UNSUPPORTED.
  * It takes no plan, and is otherwise as the operators above.
  */

@@ -3,9 +3,12 @@ any address, one plan's runs one behind the other."""
 import pytest
 
 from blackwell_tensor_core_tma_gb300 import gemm
+from tests import gatedref as gr
+from tests import opsref as ref
 from tests.test_gated_gpu import ONE, TWO, Out, check, dev, operands, scaled
 from tests.test_gated_matvec_gpu import case
 from tests.test_gated_matvec_gpu import check as check_few
+from tests.test_gated_matvec_gpu import run as few
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -135,3 +138,27 @@ def test_operands_written_just_before():
         assert plan.last_status() == back.last_status() == gemm.GEMM_OK
     for x, y in zip(apart, together):
         assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(x, y))
+
+
+@pytest.mark.parametrize("M", [2, 11])
+@pytest.mark.parametrize("x_scale,low,high", [(2.0 ** -105, 225, 247), (2.0 ** -90, 240, 247), (2.0 ** 110, 10, 24), (2.0 ** 122, 0, 6)])
+def test_few_rows_at_the_ends_of_the_weights(x_scale, low, high, M):
+    """e4m3 weights up to fp32's largest and down to its smallest against bf16 activations that bring them to ordinary numbers."""
+    F, K = 24, 640
+    gen = torch.Generator().manual_seed(low)
+    W = torch.randint(0, 256, (2 * F, K), generator=gen, dtype=torch.uint8)
+    W[(W & 127) == 127] = 126
+    SF = torch.randint(low, high + 1, (2 * F, K // 32), generator=gen, dtype=torch.uint8)
+    wide = ref.decode_e4m3(W) * ref.spread(SF, K)
+    wide = torch.where(wide.abs() > float(torch.finfo(torch.float32).max), 0.0, wide)
+    W[wide == 0] = 0
+    X = (torch.randn(M, K, generator=gen).double() * x_scale * torch.exp2(-torch.arange(M).double())[:, None]).to(torch.bfloat16)
+    g, u, want, _, _, tol = gr.gated(X.double(), wide)
+    A = few(M, F, K, "bf16", "e4m3", X, W, SF)
+    # off by 2^-39 of the largest of a token's 128 k, times the weights there, and for each of their four blocks by 2^-142 of it
+    most = torch.stack([c.abs().amax(1) for c in X.double().split(128, 1)], 1)
+    heavy = torch.stack([c.abs().sum(1) for c in wide.split(128, 1)], 1)
+    lost = most @ (heavy.t() * 2.0 ** -39 + 4 * 2.0 ** -142)
+    tol = tol + 1.2 * (lost[:, :F] * (u.abs() + lost[:, F:]) + lost[:, F:] * g.abs()) + 1e-42
+    assert want.isfinite().all() and want.abs().max() < 3e38
+    gr.assert_output("a", A, None, want, tol, "bf16")
