@@ -205,7 +205,7 @@ struct Ring {
 };
 
 // A lane's 16 bytes are 8 k of its row, the four lanes of a row have 32 k side by side.  Bound by memory: 1 x 8192 x 4096 bf16
-// 20.9 us, 6430 GB/s (95 % of a copy's rate), 8 rows 21.3, 16 rows 23.2.  (Loads to registers, as many as fit, leave memory
+// 20.8 to 21.2 us, 6350 to 6450 GB/s (93 to 95 % of a copy's rate), 8 rows 21.3, 16 rows 23.2.  (Loads to registers, as many as fit, leave memory
 // waiting while a warp computes: 23.3, 23.9 and 28.6.)  Eight columns per CTA and four stages for up to eight rows, sixteen
 // columns for more, whose lines are half of a stage: 16 columns and one row 21.1, 8 columns and 16 rows 27.8.
 template <typename XT, int NG, int G, int DEPTH>
@@ -367,8 +367,8 @@ __device__ __forceinline__ uint32_t largest2(uint32_t a, uint32_t b) {          
 // fp16 activations meet the codes as they are.  bf16 ones are brought to fp16 by a power of two for each token's 128 of k,
 // which puts the largest of them at 2^14 to 2^15: those down to 2^-31 of it are exact, smaller ones off by 2^-39 of it at
 // most.  That is done once for all columns of a CTA: its sixteen warps have 8 columns each of up to 128, or share
-// K between them; the activations lie in shared memory, a phase of K's chunks ahead.  1 x 8192 x 8192 25.1 us (5500 GB/s), 8 rows
-// 28, 16 rows 35.3: the weights' way through shared memory and the chains of MMAs behind it (16 rows with no weights loaded take
+// K between them; the activations lie in shared memory, a phase of K's chunks ahead.  1 x 8192 x 8192 24.4 to 25 us (5600 GB/s), 8 rows
+// 28, 16 rows 35.2: the weights' way through shared memory and the chains of MMAs behind it (16 rows with no weights loaded take
 // 27, without the products with scales 32.6, without conversions or reads of activations no less).  Tried, for 1, 8 and 16 rows:
 // each warp a part of K, its activations converted by itself 28.4, 29.1 and 46; weights made bf16 by their bits and a product, from
 // registers 35, 36 and 43; 24 warps with 80 registers 25.8, 30.2 and 41.8; weights by tensor boxes, one per chunk 25.9, 29 and

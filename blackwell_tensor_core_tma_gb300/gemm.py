@@ -408,7 +408,8 @@ TORCH_NAMES = {GEMM_F32: "torch.float32", GEMM_BF16: "torch.bfloat16", GEMM_F16:
 
 class ClipTensors:
     """The list of tensors of gemm_clip_run, laid out once: (g, c, type) with g and c torch tensors (c may be g or None), or
-    (g, c, type, n) with addresses.  Keeps the tensors alive."""
+    (g, c, type, n) with addresses.  Keeps the tensors alive.  Laying out 291 tensors takes some 400 us of the host's time: keep the
+    list for as long as they stay where they are."""
 
     def __init__(self, tensors):
         self.tensors = [tuple(t) for t in tensors]

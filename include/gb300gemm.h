@@ -482,8 +482,9 @@ gemm_status gemm_gated_matvec_run(int64_t M, int64_t F, int64_t K, gemm_dtype x,
  * Each tensor has n >= 0 consecutive elements of type GEMM_F32, GEMM_BF16 or GEMM_F16, at addresses that are multiples of the element's
  * size (GEMM_ERR_ALIGNMENT); c has g's type, and is g itself, apart from every g and other c, or NULL (the tensor counts and is not
  * written).  The list is read before the call returns.  NORM: one fp32 on the device.  limit >= 0; infinity
- * scales nothing.  Squares neither overflow nor vanish on their way: the sums are exact to fp32's precision over its whole range.  A NaN
- * among the elements makes NORM and every c NaN; an infinity makes NORM infinite, finite c zero and its own c NaN (unless
+ * scales nothing.  Squares neither overflow nor vanish on their way: over fp32's whole range NORM is within 6.5 * 2^-24 of its value,
+ * relative to it, and each c within 9.5 * 2^-24, both beside their type's rounding and however small g or the limit.  A NaN among the
+ * elements makes NORM and every c NaN; an infinity makes NORM infinite, finite c zero and its own c NaN (unless
  * limit is infinite).  A c that equals its g is not written where nothing is scaled.  The workspace has GEMM_CLIP_WORKSPACE bytes
  * (less: GEMM_ERR_INVALID_ARG), 16-byte aligned, whose contents do not matter before or after; calls that may overlap on
  * the GPU need one each.  Results do not depend on timing, but on the list's order, the alignment of its tensors and
